@@ -28,13 +28,20 @@
  *                      the score against golden labels, gradients of W^DQ,
  *                      W^IUQ and W^w with the keys frozen
  *                                                  [BLOG] §4 训练, [HYPER] 方法
+ *   lsa_kv_append      a step's (or a prompt's) keys and values into a paged
+ *                      cache, keys and queries rotated by their positions
+ *   lsa_attend         attention over that cache: all of it, or a sliding
+ *                      window and the first tokens    [HYPER] 方法 (sliding window)
+ *   lsa_attend_topk    attention of one token per sequence over the entries the
+ *                      native top-k listed, the window and the first tokens
+ *                                       [BLOG] §2.2, [HYPER] 方法 (C^CoreComp)
  *
  * Conventions shared by every call:
  *  - Ownership: the caller allocates every buffer. Pointers marked "dev" are
  *    device memory on the current HIP device; pointers marked "host" are host
  *    memory read during the call only. The library never allocates, frees or
  *    synchronises. Its only scratch space is the caller's workspace (top-k,
- *    golden labels and the training step).
+ *    golden labels, the training step and attention).
  *  - Asynchrony: kernels are enqueued on `stream` and the call returns at once.
  *    Results are valid once the stream reaches that point. Calls are reentrant.
  *  - Errors: every argument is checked on the host before anything is enqueued.
@@ -514,6 +521,143 @@ lsa_status lsa_train_step(const void* h /* dev */, const void* w_dq /* dev */, c
                           float* g_dq /* dev [r, d] */, float* g_iuq /* dev [n_h*d_h, r] */,
                           float* g_w /* dev [n_h, d] */, void* workspace /* dev */, size_t workspace_bytes,
                           hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The paged cache of lsa_kv_append, lsa_attend and lsa_attend_topk. These three
+ * calls count tokens, not entries: position s of sequence b is slot
+ * s % page_tokens of page page_table[b * table_stride + s / page_tokens].
+ *
+ * k and v are [n_pages, n_kv, page_tokens, d_h], so the tokens of one page and
+ * key head are contiguous. dtype is LSA_BF16, or LSA_FP8_E4M3 with one fp32
+ * scale per page and key head, k_scale and v_scale [n_pages, n_kv]: a stored
+ * code c stands for c * scale. Scales of pages in use must be positive and
+ * finite. kv_len[b] is the number of cached tokens of sequence b, the call's
+ * own new tokens included; it is read on the device, so a captured call follows
+ * it.
+ * Supported: page_tokens 16, 32, 64 or 128; d_h 64 or 128; 1 <= n_kv <= 1024;
+ * k and v 16-byte aligned. A page number outside [0, n_pages) is a page
+ * with no tokens: nothing is stored there and attention does not see it. The
+ * same holds for positions at or beyond table_stride * page_tokens. Pages may
+ * be shared between sequences for reading; a page that one call appends to may
+ * belong to one sequence only.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  void* k;                    /* dev [n_pages, n_kv, page_tokens, d_h] */
+  void* v;                    /* dev, the same */
+  float* k_scale;             /* dev [n_pages, n_kv] for LSA_FP8_E4M3, else NULL */
+  float* v_scale;             /* dev, the same */
+  const int32_t* page_table;  /* dev [B, table_stride] */
+  const int32_t* kv_len;      /* dev [B] */
+  int64_t table_stride;
+  int32_t n_pages, n_kv, page_tokens, d_h;
+  lsa_dtype dtype;
+} lsa_kv_cache;
+
+/* ------------------------------------------------------------------------
+ * lsa_kv_append: store the new tokens' keys and values, and rotate keys and
+ * queries by their positions on the way.
+ *
+ * Sequence b has n_b = new_offsets[b+1] - new_offsets[b] new tokens (none is
+ * fine); its i-th is row new_offsets[b] + i of k_new, v_new and q, and goes to
+ * position p = kv_len[b] - n_b + i (a negative one is not stored). k_new and
+ * v_new are bf16 [rows, n_kv, d_h], q (or NULL) is bf16 [rows, n_q, d_h]; rows
+ * are k_stride, v_stride and q_stride elements apart, so they may be parts of
+ * one projection's output. q_out is bf16 [rows, n_q, d_h], contiguous, and may
+ * be q itself when q is contiguous. Rows outside the sequences are not touched.
+ *
+ * Rotation: pair j < rot_dim / 2 turns by the angle p * inv_freq[j],
+ *   (x, y) -> (x cos - y sin, y cos + x sin),
+ * where the pair is dimensions (j, j + rot_dim / 2) for LSA_ROPE_HALVES and
+ * (2j, 2j + 1) for LSA_ROPE_PAIRS. Dimensions from rot_dim on, and v, are stored
+ * as they are. The angle is formed in fp64, the rotation in fp32. positions, if
+ * non-NULL, gives each row's p for the rotation only. LSA_ROPE_NONE rotates
+ * nothing; inv_freq and rot_dim are then ignored.
+ *
+ * LSA_BF16 stores the value rounded once to nearest even. LSA_FP8_E4M3: for each
+ * page and key head, need is the least power of two (at least 2^-118) with
+ * |x| <= 448 need for every finite new value x on the page. If the page's slot 0
+ * is among the new tokens, its scale becomes need; otherwise it becomes
+ * max(scale, need), and where that grew, the page's earlier codes c are replaced
+ * by e4m3(c * old / new), which is exact unless the result is subnormal in
+ * e4m3. New values are stored as e4m3(x / scale), to nearest even; infinities
+ * and NaN are stored as NaN. Slots behind the last new token are left as they
+ * are.
+ * Supported: 1 <= B <= 4096; rot_dim a positive multiple of 16 up to d_h;
+ * strides multiples of 8; k_new, v_new, q and q_out 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+enum { LSA_ROPE_NONE = 0, LSA_ROPE_HALVES = 1, LSA_ROPE_PAIRS = 2 };
+lsa_status lsa_kv_append(const lsa_kv_cache* cache /* host */, int32_t B, const void* k_new /* dev */,
+                         int64_t k_stride, const void* v_new /* dev */, int64_t v_stride,
+                         const void* q /* dev or NULL */, int64_t q_stride, void* q_out /* dev */, int32_t n_q,
+                         const int64_t* new_offsets /* dev [B+1] */,
+                         const int64_t* new_offsets_host /* host [B+1] */, int32_t rope,
+                         const float* inv_freq /* dev [rot_dim / 2] */, int32_t rot_dim,
+                         const int32_t* positions /* dev [rows] or NULL */, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * lsa_attend: causal attention of the newest tokens over the cache.
+ *
+ * Sequence b's queries are rows q_offsets[b] .. q_offsets[b+1] of q
+ * ([rows, n_q, d_h] bf16, rows q_stride elements apart), the last of them at
+ * position kv_len[b] - 1; one row per sequence is a decode step, all of a prompt a
+ * prefill, and both may be mixed. Query head i reads key head i / (n_q / n_kv).
+ * A query at position p sees position s <= p if window == 0, or
+ * s > p - window, or s < sinks:
+ *   out = sum_s P_s V_s, P = softmax over the seen s of softmax_scale * q . K_s.
+ * out is [rows, n_q, d_h] bf16 (rows out_stride elements apart); lse, if
+ * non-NULL, is [rows, n_q] fp32 contiguous and receives
+ * ln sum_s exp(softmax_scale * q . K_s). A query that sees nothing gets
+ * out = 0 and lse = -inf. What is cached at positions a query does not see,
+ * infinities and NaN too, has no effect on its row. Rows outside the sequences are
+ * not touched.
+ *
+ * max_kv_len bounds kv_len on the host (for the launch's shape); a larger kv_len
+ * counts as max_kv_len. It must not exceed table_stride * page_tokens.
+ * Precision: products of bf16 (e4m3 codes are exact in bf16) accumulate in fp32;
+ * the softmax is fp32; probabilities are rounded to bf16 for the second product.
+ * The workspace holds lsa_attend_workspace_size(...) bytes of device memory for the
+ * same sizes, 16-byte aligned (it may be NULL if that is 0); its contents on entry do
+ * not matter. Calls that may overlap in time need workspaces of their own; so do
+ * two captured graphs that may.
+ * Supported: 1 <= B <= 4096; n_q a multiple of n_kv, n_q <= 1024 * n_kv; at most
+ * 2^31 - 1 query rows times heads; strides multiples of 8; q and out 16-byte
+ * aligned; out must not overlap q.
+ * ---------------------------------------------------------------------- */
+size_t lsa_attend_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h,
+                                 const int64_t* q_offsets_host /* host [B+1] */, int32_t max_kv_len,
+                                 int32_t window, int32_t sinks);
+lsa_status lsa_attend(const lsa_kv_cache* cache /* host */, int32_t B, const void* q /* dev */, int64_t q_stride,
+                      int32_t n_q, const int64_t* q_offsets /* dev [B+1] */,
+                      const int64_t* q_offsets_host /* host [B+1] */, int32_t max_kv_len, float softmax_scale,
+                      int32_t window, int32_t sinks, void* out /* dev */, int64_t out_stride,
+                      float* lse /* dev or NULL */, void* workspace /* dev */, size_t workspace_bytes,
+                      hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * lsa_attend_topk: attention of one token per sequence over listed entries, the
+ * last `window` tokens and the first `sinks` ones: the core attention over
+ * C^CoreComp and the sliding window.
+ *
+ * idx [B, k] and count [B] are what lsa_topk and lsa_topk_step write for one
+ * layer: the first count[b] of row b are ascending entry numbers, the rest is
+ * not read. Entry e covers positions e * entry_tokens ..
+ * e * entry_tokens + entry_tokens - 1. The query of sequence b is row b of q
+ * ([B, n_q, d_h] bf16), at position p = kv_len[b] - 1. It sees position s <= p
+ * if s's entry is listed, or s > p - window, or s < sinks (here window == 0 is no
+ * window). A position that is seen for several reasons, and an entry that is
+ * listed twice in a row, counts once. Negative entries are skipped.
+ * Everything else is as for lsa_attend, except that the host gives no bound: a kv_len
+ * beyond table_stride * page_tokens counts as that.
+ * Supported: as lsa_attend, with 1 <= k <= 65536 and 1 <= entry_tokens <= 128.
+ * ---------------------------------------------------------------------- */
+size_t lsa_attend_topk_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h, int32_t k,
+                                      int32_t entry_tokens, int32_t window, int32_t sinks);
+lsa_status lsa_attend_topk(const lsa_kv_cache* cache /* host */, int32_t B, const void* q /* dev */,
+                           int64_t q_stride, int32_t n_q, const int32_t* idx /* dev [B, k] */,
+                           const int32_t* count /* dev [B] */, int32_t k, int32_t entry_tokens,
+                           float softmax_scale, int32_t window, int32_t sinks, void* out /* dev */,
+                           int64_t out_stride, float* lse /* dev or NULL */, void* workspace /* dev */,
+                           size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * lsa_debug_range_errors: in a debug build (compiled with LSA_DEBUG_CHECKS=1),

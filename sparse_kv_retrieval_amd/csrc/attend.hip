@@ -1,0 +1,598 @@
+// lsa_attend and lsa_attend_topk: attention over the paged cache, keys split among waves.
+//
+// Mathematics. For a row (one query head of one token) and the keys it sees,
+//   out = sum_s 2^(x_s - m) V_s / sum_s 2^(x_s - m),  x_s = scale * log2(e) * q . K_s,
+// with a running maximum m, so one pass over the keys is enough and any split of the keys can be
+// joined: partial (m, l, o) triples add after scaling by 2^(m - m').
+//
+// Layout. Both products are formed transposed. S^T = K Q^T puts one row per lane (column
+// lane % 16 of the 16x16 result) and four keys of it in the lane's registers, so the softmax needs
+// no lane exchange except for a new maximum, and the four + four probabilities of a 32-key tile are
+// already the operand of O^T = V^T P^T: the contraction may number its keys in any order, and the
+// one that the registers hold is used. V^T's operand then wants, for each dimension, those eight
+// keys of a lane group: every lane loads the same D/16 dimensions of its group's eight rows and
+// transposes the small block in registers. Keys and values go from HBM to registers with no
+// exchange through LDS; nothing is read twice.
+//
+// Precision. q and bf16 keys enter the matrix cores as they are, e4m3 codes widen to bf16 exactly;
+// page scales multiply the fp32 score (keys) and the probability (values). The probability is
+// rounded once, to bf16, for the second product; sums and accumulators are fp32.
+//
+// The maximum follows the scores lazily: it is raised (and the accumulators rescaled) only when
+// some score exceeds it by 2^8. Probabilities then stay below 2^8, and no bit is lost in fp32 or
+// bf16, whose exponents have room.
+#include "kv.hpp"
+
+namespace lsa {
+
+static constexpr int AT_WAVES = 4;
+static constexpr int AT_THREADS = 64 * AT_WAVES;
+static constexpr float LAZY = 8.0f;
+static constexpr float LOWEST = -3.402823466e38f;  // running maximum of a row that has seen nothing
+static constexpr float LN2 = 0.6931471805599453f;
+
+// One row block: rows r0 .. r0 + n - 1 of sequence b for key head h.
+struct Rows {
+  int32_t b, n, r0;
+  int32_t p0;          // position of the sequence's first query token (negative: it has fewer cached tokens)
+  int32_t p_lo, p_hi;  // positions of the block's first and last row
+  int64_t t0;          // row number of the sequence's first token in q
+  TileRange near;      // tiles seen by position
+  int32_t tiles;       // those and the listed ones
+};
+
+template <bool LISTED>
+__device__ __forceinline__ void set_block(const AttendArgs& a, int64_t n_tok, int64_t j, int M, Rows* w) {
+  const int64_t rows = n_tok * a.G;
+  w->r0 = (int32_t)(j * M);
+  w->n = (int32_t)min((int64_t)M, rows - j * M);
+  const int32_t len = min(max(a.c.kv_len[w->b], 0), a.max_kv_len);
+  w->p0 = (int32_t)(len - n_tok);
+  w->p_lo = w->p0 + w->r0 / a.G;
+  w->p_hi = w->p0 + (w->r0 + w->n - 1) / a.G;
+  if constexpr (LISTED) {
+    const int64_t some = (int64_t)min(max(a.count[w->b], 0), a.k) * a.r;
+    if (a.window > 0) {
+      w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks);
+    } else {
+      const int32_t end = w->p_hi < 0 ? 0 : w->p_hi / 32 + 1, s = a.sinks / 32 + (a.sinks % 32 != 0);
+      w->near.n_first = w->near.n = min(s, end);
+      w->near.first_b = 0;
+    }
+    w->tiles = w->p_hi < 0 ? 0 : w->near.n + (int32_t)((some + 31) / 32);
+  } else {
+    w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks);
+    w->tiles = w->near.n;
+  }
+}
+
+template <bool LISTED>
+__device__ __forceinline__ bool find_rows(const AttendArgs& a, int64_t block, int M, Rows* w) {
+  int64_t n_tok, j;
+  if constexpr (LISTED) {
+    const int per = (a.G + M - 1) / M;
+    w->b = (int)(block / per);
+    w->t0 = w->b;
+    n_tok = 1;
+    j = block % per;
+  } else {
+    auto slot_of = [&](int x) -> int64_t { return (a.off[x] - a.first_row) * a.G / M + x; };
+    w->b = wave_find(a.B, block, slot_of);
+    w->t0 = a.off[w->b];
+    n_tok = a.off[w->b + 1] - w->t0;
+    j = block - slot_of(w->b);
+    if (j * M >= n_tok * a.G) return false;
+  }
+  set_block<LISTED>(a, n_tok, j, M, w);
+  return true;
+}
+
+// One wave's tile of 32 keys in registers.
+template <bool FP8, int D>
+struct Tile {
+  static constexpr int ROW = D * (FP8 ? 1 : 2);            // bytes of a cached row
+  static constexpr int KL = ROW / 64;                      // 16-byte loads per lane and 16 keys
+  static constexpr int VPL = D / 16;                       // dimensions a lane loads of each of its 8 value rows
+  static constexpr int VB = VPL * (FP8 ? 1 : 2);           // bytes of them
+  u32x4 k[2][KL];
+  uint32_t v[8][VB / 4];
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const u32x4 x = *(const u32x4*)p;
+    w[0] = x[0]; w[1] = x[1]; w[2] = x[2]; w[3] = x[3];
+  } else if constexpr (N == 2) {
+    const u32x2 x = *(const u32x2*)p;
+    w[0] = x[0]; w[1] = x[1];
+  } else {
+    w[0] = *(const uint32_t*)p;
+  }
+}
+
+// Operand of contraction step s for the lane's key. The dimensions are numbered as the loads bring
+// them: FP8 step 2c + e holds 64 c + 16 g + 8 e + j, bf16 step s holds 32 s + 8 g + j (j = 0..7).
+template <bool FP8, int D>
+__device__ __forceinline__ bf16x8 k_operand(const Tile<FP8, D>& t, int sub, int s) {
+  if constexpr (FP8) {
+    const u32x4 x = t.k[sub][s >> 1];
+    const u32x2 lo = e4m3x4_to_bf16x4(x[2 * (s & 1)]), hi = e4m3x4_to_bf16x4(x[2 * (s & 1) + 1]);
+    return as_bf16x8((u32x4){lo[0], lo[1], hi[0], hi[1]});
+  } else {
+    return as_bf16x8(t.k[sub][s]);
+  }
+}
+template <bool FP8>
+__device__ __forceinline__ int q_dim(int s, int g) {
+  return FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+}
+
+// Operand of the second product, dimension VPL * (lane % 16) + i: the lane group's 8 keys, in the
+// order of the probabilities (4g .. 4g+3 of the first 16 keys, then of the second 16).
+template <bool FP8, int D>
+__device__ __forceinline__ bf16x8 v_operand(const Tile<FP8, D>& t, int i) {
+  if constexpr (FP8) {
+    const int w = i / 4, c = i % 4;
+    const uint32_t sel = 0x0C0C0000u | ((uint32_t)c << 8) | (uint32_t)(c + 4);  // byte c of two dwords
+    u32x4 r;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t lo = __builtin_amdgcn_perm(t.v[4 * x][w], t.v[4 * x + 1][w], sel);
+      const uint32_t hi = __builtin_amdgcn_perm(t.v[4 * x + 2][w], t.v[4 * x + 3][w], sel);
+      const u32x2 y = e4m3x4_to_bf16x4(lo | (hi << 16));
+      r[2 * x] = y[0];
+      r[2 * x + 1] = y[1];
+    }
+    return as_bf16x8(r);
+  } else {
+    const int w = i / 2;
+    const uint32_t sel = i % 2 ? 0x07060302u : 0x05040100u;  // upper or lower halves of two dwords
+    u32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = __builtin_amdgcn_perm(t.v[2 * j + 1][w], t.v[2 * j][w], sel);
+    return as_bf16x8(r);
+  }
+}
+
+// The elements of a dword that are not finite, as a mask over its bits.
+template <bool FP8>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  if constexpr (FP8) {
+    const uint32_t hit = (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;  // code 7F or FF
+    return hit * 0xFFu;
+  } else {
+    return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+  }
+}
+
+template <bool FP8>
+__device__ __forceinline__ float element(const char* row, int d) {
+  if constexpr (FP8) {
+    return __builtin_amdgcn_cvt_f32_fp8((int)*(const uint8_t*)(row + d), 0);
+  } else {
+    return bf16_bits_to_f32(*(const uint16_t*)(row + 2 * d));
+  }
+}
+
+template <bool FP8, int D, int RT, bool LISTED>
+__global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendArgs a) {
+  using TileT = Tile<FP8, D>;
+  constexpr int KS = D / 32, VPL = TileT::VPL, ROW = TileT::ROW, M = 16 * RT;
+  constexpr int RUN = LISTED ? ATTEND_MAX_RUN_LISTED : ATTEND_MAX_RUN;
+  constexpr int PLACES = LISTED ? 32 : 2;  // places resolved per tile: single keys, or 16 in a row
+  __shared__ int64_t s_row[RUN * PLACES];  // cached row of the place, or -1: nothing there
+  __shared__ float s_ks[FP8 ? RUN * PLACES : 1], s_vs[FP8 ? RUN * PLACES : 1];
+  __shared__ float s_o[AT_WAVES][16][D + 4];
+  __shared__ float s_m[AT_WAVES][16], s_l[AT_WAVES][16];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), col = lane & 15, g = lane >> 4;
+  const int64_t id = blockIdx.x;
+  const int h = (int)(id % a.c.n_kv);
+  const int split = (int)((id / a.c.n_kv) % a.splits);
+  Rows w;
+  if (!find_rows<LISTED>(a, id / ((int64_t)a.c.n_kv * a.splits), M, &w)) return;
+  const int parts = (w.tiles + a.run - 1) / a.run;
+  if (split > 0 && split >= parts) return;
+  const int first = split * a.run, count = min(a.run, w.tiles - first);  // count is 0 where nothing is seen
+
+  // the block's queries: lane column = row
+  bf16x8 q[RT][KS];
+  int32_t p_row[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = rt * 16 + col;
+    const bool live = r < w.n;
+    const int row = w.r0 + (live ? r : w.n - 1);
+    const int tok = row / a.G;
+    p_row[rt] = w.p0 + tok;
+    const uint16_t* src = a.q + (w.t0 + tok) * a.q_stride + (int64_t)(h * a.G + (row - tok * a.G)) * D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      u32x4 x = *(const u32x4*)(src + q_dim<FP8>(s, g));
+      if (!live) x = (u32x4){0, 0, 0, 0};
+      q[rt][s] = as_bf16x8(x);
+    }
+  }
+
+  f32x4 acc[RT][VPL];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = LOWEST;
+    l[rt] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[rt][i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  }
+
+  int base = first;  // first of the resolved tiles
+  // where the keys of tiles tile0 .. tile0 + n - 1 lie
+  auto resolve = [&](int tile0, int n) {
+    for (int i = tid; i < n * PLACES; i += AT_THREADS) {
+      const int tile = tile0 + i / PLACES;
+      int64_t tok = -1;
+      if constexpr (LISTED) {
+        if (tile < w.near.n) {
+          tok = (int64_t)w.near.tile(tile) * 32 + i % 32;
+          const bool seen = tok <= w.p_hi && ((a.window > 0 && tok > (int64_t)w.p_hi - a.window) || tok < a.sinks);
+          tok = seen ? tok : -1;
+        } else {
+          const int64_t at = (int64_t)(tile - w.near.n) * 32 + i % 32;
+          const int64_t e = at / a.r;
+          if (e < min(a.count[w.b], a.k)) {
+            const int32_t* list = a.idx + (int64_t)w.b * a.k;
+            const int32_t entry = list[e];
+            tok = (int64_t)entry * a.r + at % a.r;
+            const bool near = (a.window > 0 && tok > (int64_t)w.p_hi - a.window) || tok < a.sinks;
+            if (entry < 0 || tok > w.p_hi || near || (e > 0 && list[e - 1] == entry)) tok = -1;
+          }
+        }
+      } else {
+        tok = (int64_t)w.near.tile(tile) * 32 + (i % 2) * 16;
+        // no row sees any of the 16: the page may not be the sequence's any more
+        if (tok > w.p_hi || (a.window > 0 && tok + 15 <= (int64_t)w.p_lo - a.window && tok >= a.sinks)) tok = -1;
+      }
+      int64_t row = -1;
+      if (tok >= 0) {
+        const int32_t page = a.c.table[w.b * a.c.table_stride + (tok >> a.c.pt_log2)];
+        if (page >= 0 && page < a.c.n_pages) {
+          const int64_t t = (int64_t)page * a.c.n_kv + h;
+          row = (t << a.c.pt_log2) + (tok & ((1 << a.c.pt_log2) - 1));
+          if constexpr (FP8) {
+            s_ks[i] = a.c.k_scale[t] * a.scale_log2;
+            s_vs[i] = a.c.v_scale[t];
+          }
+        }
+      }
+      if (FP8 && row < 0) s_ks[i] = s_vs[i] = 0.f;
+      s_row[i] = row;
+    }
+  };
+
+  // Loads of the resolved tile i. A place with nothing reads row 0 of the cache; what it brings is masked.
+  auto load = [&](int i, TileT& t) {
+    if constexpr (LISTED) {
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const int64_t row = max(s_row[32 * i + 16 * sub + col], (int64_t)0);
+#pragma unroll
+        for (int c = 0; c < TileT::KL; ++c) t.k[sub][c] = *(const u32x4*)(a.c.k + row * ROW + 64 * c + 16 * g);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t row = max(s_row[32 * i + 16 * (j / 4) + 4 * g + j % 4], (int64_t)0);
+        load_words(a.c.v + row * ROW + col * TileT::VB, t.v[j]);
+      }
+    } else {
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const int64_t row = max(uni(s_row[2 * i + sub]), (int64_t)0);
+        const char* kb = a.c.k + row * ROW;
+        const char* vb = a.c.v + row * ROW;
+#pragma unroll
+        for (int c = 0; c < TileT::KL; ++c) t.k[sub][c] = *(const u32x4*)(kb + (uint32_t)(col * ROW + 64 * c + 16 * g));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_words(vb + (uint32_t)((4 * g + j) * ROW + col * TileT::VB), t.v[4 * sub + j]);
+      }
+    }
+  };
+
+  auto compute = [&](int i, TileT& t) {
+    // x[rt][j]: score, base 2, of key 16 (j / 4) + 4 g + j % 4
+    float x[RT][8];
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      f32x4 s[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) s[rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        const bf16x8 kk = k_operand<FP8, D>(t, sub, c);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) s[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[rt][c], s[rt], 0, 0, 0);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float f = a.scale_log2;
+          if constexpr (FP8) f = LISTED ? s_ks[32 * i + 16 * sub + 4 * g + j] : s_ks[2 * i + sub];
+          x[rt][4 * sub + j] = s[rt][j] * f;
+        }
+    }
+    // masks
+    bool rescue = false;
+    if constexpr (LISTED) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool gone = s_row[32 * i + 16 * (j / 4) + 4 * g + j % 4] < 0;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) x[rt][j] = gone ? -__builtin_inff() : x[rt][j];
+#pragma unroll
+        for (int e = 0; e < TileT::VB / 4; ++e) t.v[j][e] = gone ? 0u : t.v[j][e];
+      }
+    } else {
+      const int t0 = w.near.tile(base + i) * 32;
+      const bool here0 = uni(s_row[2 * i]) >= 0, here1 = uni(s_row[2 * i + 1]) >= 0;
+      const bool whole = here0 && here1 && t0 + 31 <= w.p_lo &&
+                         (a.window == 0 || (int64_t)t0 > (int64_t)w.p_hi - a.window || t0 + 31 < a.sinks);
+      if (!whole) {
+        uint32_t odd = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int tok = t0 + 16 * (j / 4) + 4 * g + j % 4;
+          const bool here = j < 4 ? here0 : here1;
+          const bool some = here && tok <= w.p_hi &&
+                            (a.window == 0 || (int64_t)tok > (int64_t)w.p_lo - a.window || tok < a.sinks);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const bool seen = here && tok <= p_row[rt] &&
+                              (a.window == 0 || (int64_t)tok > (int64_t)p_row[rt] - a.window || tok < a.sinks);
+            x[rt][j] = seen ? x[rt][j] : -__builtin_inff();
+          }
+#pragma unroll
+          for (int e = 0; e < TileT::VB / 4; ++e) {
+            t.v[j][e] = some ? t.v[j][e] : 0u;
+            odd |= not_finite<FP8>(t.v[j][e]);
+          }
+        }
+        // A value that is not finite would reach rows that do not see it as 0 * inf. Such values are
+        // taken out of the product and added below to the rows that see them.
+        if (w.p_lo != w.p_hi && __any(odd != 0)) {
+          rescue = true;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < TileT::VB / 4; ++e) t.v[j][e] &= ~not_finite<FP8>(t.v[j][e]);
+        }
+      }
+    }
+    // softmax
+    bf16x8 p[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float top = x[rt][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top = fmaxf(top, x[rt][j]);
+      if (__any(top > m[rt] + LAZY)) {
+        const float up = fmaxf(m[rt], max_column(top));
+        const float f = __builtin_amdgcn_exp2f(m[rt] - up);
+        m[rt] = up;
+        l[rt] *= f;
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) acc[rt][e] *= f;
+      }
+      u32x4 packed;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        float y0 = __builtin_amdgcn_exp2f(x[rt][j] - m[rt]), y1 = __builtin_amdgcn_exp2f(x[rt][j + 1] - m[rt]);
+        l[rt] += y0 + y1;
+        if constexpr (FP8) {
+          const int at = LISTED ? 32 * i + 16 * (j / 4) + 4 * g + j % 4 : 2 * i + j / 4;
+          y0 *= s_vs[at];
+          y1 *= s_vs[LISTED ? at + 1 : at];
+        }
+        packed[j / 2] = pack_bf16(y0, y1);
+      }
+      p[rt] = as_bf16x8(packed);
+    }
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) {
+      const bf16x8 vv = v_operand<FP8, D>(t, e);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) acc[rt][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, p[rt], acc[rt][e], 0, 0, 0);
+    }
+    if constexpr (!LISTED) {
+      if (rescue) {
+        const int t0 = w.near.tile(base + i) * 32;
+        for (int j = 0; j < 32; ++j) {
+          const int64_t row = uni(s_row[2 * i + j / 16]);
+          if (row < 0) continue;
+          const char* src = a.c.v + (row + j % 16) * ROW;
+          const int tok = t0 + j;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const bool seen = tok <= p_row[rt] &&
+                              (a.window == 0 || (int64_t)tok > (int64_t)p_row[rt] - a.window || tok < a.sinks);
+#pragma unroll
+            for (int e = 0; e < VPL; ++e)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float y = element<FP8>(src, VPL * (4 * g + c) + e);
+                if (seen && !(fabsf(y) < __builtin_inff())) acc[rt][e][c] += y;
+              }
+          }
+        }
+      }
+    }
+  };
+
+  for (int done = 0; done < count; done += RUN) {
+    const int n = min(RUN, count - done);
+    base = first + done;
+    if (done) __syncthreads();
+    resolve(base, n);
+    __syncthreads();
+    if (wave >= n) continue;
+    // two tiles in registers: the loads of the next one are in flight while one is worked on
+    TileT t0, t1;
+    int i = wave;
+    load(i, t0);
+    for (;;) {
+      const int j = i + AT_WAVES;
+      if (j < n) load(j, t1);
+      compute(i, t0);
+      if (j >= n) break;
+      i = j + AT_WAVES;
+      if (i < n) load(i, t0);
+      compute(j, t1);
+      if (i >= n) break;
+    }
+  }
+
+  // join the waves' partial results, 16 rows at a time
+  for (int rt = 0; rt < RT; ++rt) {
+    if (rt * 16 >= w.n) break;
+    if (rt) __syncthreads();
+#pragma unroll
+    for (int k = 0; k < RT; ++k) {
+      if (k != rt) continue;
+      const float sum = sum_column(l[k]);
+      if (g == 0) {
+        s_m[wave][col] = m[k];
+        s_l[wave][col] = sum;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) s_o[wave][col][VPL * (4 * g + c) + e] = acc[k][e][c];
+    }
+    __syncthreads();
+    const int r = tid / 16, d0 = (tid % 16) * VPL;
+    if (rt * 16 + r < w.n) {
+      float top = s_m[0][r], sum = 0.f, o[VPL];
+#pragma unroll
+      for (int v = 1; v < AT_WAVES; ++v) top = fmaxf(top, s_m[v][r]);
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int v = 0; v < AT_WAVES; ++v) {
+        const float f = __builtin_amdgcn_exp2f(s_m[v][r] - top);
+        sum += s_l[v][r] * f;
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) o[e] += s_o[v][r][d0 + e] * f;
+      }
+      const int row = w.r0 + rt * 16 + r, tok = row / a.G, head = h * a.G + (row - tok * a.G);
+      if (parts <= 1) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t* dst = a.out + (w.t0 + tok) * a.out_stride + (int64_t)head * D + d0;
+#pragma unroll
+        for (int e = 0; e < VPL; e += 4)
+          *(u32x2*)(dst + e) = (u32x2){pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv)};
+        if (a.lse && tid % 16 == 0)
+          a.lse[(w.t0 + tok) * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (top + __log2f(sum)) * LN2;
+      } else {
+        const int64_t at = ((int64_t)split * a.T + (w.t0 - a.first_row + tok)) * a.n_q + head;
+#pragma unroll
+        for (int e = 0; e < VPL; e += 4) *(f32x4*)(a.part_o + at * D + d0 + e) = (f32x4){o[e], o[e + 1], o[e + 2], o[e + 3]};
+        if (tid % 16 == 0) *(f32x2*)(a.part_ml + 2 * at) = (f32x2){top, sum};
+      }
+    }
+  }
+}
+
+// Joins the partial results of rows whose keys were split: one wave per row.
+template <int D, bool LISTED>
+__global__ __launch_bounds__(AT_THREADS) void attend_join_kernel(const AttendArgs a, int M) {
+  const int lane = threadIdx.x & 63;
+  const int64_t id = (int64_t)blockIdx.x * AT_WAVES + (threadIdx.x >> 6);
+  if (id >= a.T * a.n_q) return;
+  const int64_t t = id / a.n_q;
+  const int head = (int)(id - t * a.n_q);
+  Rows w;
+  int64_t n_tok = 1;
+  if constexpr (LISTED) {
+    w.b = (int)t;
+    w.t0 = t;
+  } else {
+    if (t + a.first_row >= a.off[a.B]) return;
+    w.b = upper_seq(a.off, a.B, t + a.first_row);
+    w.t0 = a.off[w.b];
+    n_tok = a.off[w.b + 1] - w.t0;
+  }
+  const int64_t row = (t + a.first_row - w.t0) * a.G + head % a.G;
+  set_block<LISTED>(a, n_tok, row / M, M, &w);
+  const int parts = (w.tiles + a.run - 1) / a.run;
+  if (parts <= 1) return;
+  const int64_t step = a.T * a.n_q;
+  float top = LOWEST;
+  for (int s = lane; s < parts; s += 64) top = fmaxf(top, a.part_ml[2 * (s * step + id)]);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  constexpr int W = D / 64;
+  float sum = 0.f, acc[W] = {};
+  for (int s0 = 0; s0 < parts; s0 += 64) {
+    const int n = min(64, parts - s0);
+    float f = 0.f, part = 0.f;
+    if (lane < n) {
+      const f32x2 ml = *(const f32x2*)(a.part_ml + 2 * ((s0 + lane) * step + id));
+      f = __builtin_amdgcn_exp2f(ml[0] - top);
+      part = ml[1] * f;
+    }
+    sum += part;
+    for (int s = 0; s < n; s += 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // lanes from n on hold a factor of 0
+        const float x = __shfl(f, s + u);
+        const float* src = a.part_o + ((s0 + min(s + u, n - 1)) * step + id) * D + lane * W;
+#pragma unroll
+        for (int e = 0; e < W; ++e) acc[e] += src[e] * x;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint16_t* dst = a.out + (t + a.first_row) * a.out_stride + (int64_t)head * D + lane * W;
+  if constexpr (W == 2) {
+    *(uint32_t*)dst = pack_bf16(acc[0] * inv, acc[1] * inv);
+  } else {
+    *dst = (uint16_t)pack_bf16(acc[0] * inv, 0.f);
+  }
+  if (a.lse && lane == 0)
+    a.lse[(t + a.first_row) * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (top + __log2f(sum)) * LN2;
+}
+
+template <bool FP8, int D, bool LISTED>
+static hipError_t launch_rows(const AttendArgs& a, int row_tiles, hipStream_t s) {
+  const dim3 grid((unsigned)(a.blocks * a.splits * a.c.n_kv));
+  if (row_tiles == 1) attend_split_kernel<FP8, D, 1, LISTED><<<grid, AT_THREADS, 0, s>>>(a);
+  else if (row_tiles == 2) attend_split_kernel<FP8, D, 2, LISTED><<<grid, AT_THREADS, 0, s>>>(a);
+  else attend_split_kernel<FP8, D, 4, LISTED><<<grid, AT_THREADS, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool LISTED>
+static hipError_t launch_dim(const AttendArgs& a, bool fp8, int d, int row_tiles, hipStream_t s) {
+  if (d == 64) return fp8 ? launch_rows<true, 64, LISTED>(a, row_tiles, s) : launch_rows<false, 64, LISTED>(a, row_tiles, s);
+  return fp8 ? launch_rows<true, 128, LISTED>(a, row_tiles, s) : launch_rows<false, 128, LISTED>(a, row_tiles, s);
+}
+
+hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_tiles, bool listed, hipStream_t s) {
+  return listed ? launch_dim<true>(a, fp8, d, row_tiles, s) : launch_dim<false>(a, fp8, d, row_tiles, s);
+}
+
+hipError_t launch_attend_join(const AttendArgs& a, int d, int row_tiles, bool listed, hipStream_t s) {
+  const dim3 grid((unsigned)((a.T * a.n_q + AT_WAVES - 1) / AT_WAVES));
+  const int M = 16 * row_tiles;
+  if (listed) {
+    if (d == 64) attend_join_kernel<64, true><<<grid, AT_THREADS, 0, s>>>(a, M);
+    else attend_join_kernel<128, true><<<grid, AT_THREADS, 0, s>>>(a, M);
+  } else {
+    if (d == 64) attend_join_kernel<64, false><<<grid, AT_THREADS, 0, s>>>(a, M);
+    else attend_join_kernel<128, false><<<grid, AT_THREADS, 0, s>>>(a, M);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace lsa

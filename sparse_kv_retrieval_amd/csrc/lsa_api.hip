@@ -10,6 +10,7 @@
 #include <string>
 
 #include "kernels.hpp"
+#include "kv.hpp"
 
 using namespace lsa;
 
@@ -641,6 +642,268 @@ lsa_status lsa_train_step(const void* h, const void* w_dq, const void* w_iuq, co
   a.gamma = gamma; a.alpha = alpha; a.inv_total = total > 0 ? (float)(1.0 / (double)total) : 0.f;
   e = launch_train(a, stream);
   return e == hipSuccess ? LSA_OK : hip_fail("lsa_train_step launch", e);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the paged cache
+namespace {
+
+// Limits of the paged-cache calls.
+constexpr int32_t kKvMaxB = 4096, kKvMaxHeads = 1024, kKvMaxGroup = 1024;
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;          // of 256 threads: a launch has fewer than 2^32
+constexpr size_t kPartialBytes = (size_t)256 << 20;    // partial attention results of one call, about
+
+bool multiple8(int64_t x) { return x % 8 == 0; }
+
+lsa_status check_cache(const lsa_kv_cache* c, bool* fp8, KvView* v) {
+  if (!c) return fail(LSA_ERR_INVALID_ARG, "cache is NULL");
+  const int32_t dt = dtype_value(c->dtype);
+  if (dt != LSA_BF16 && dt != LSA_FP8_E4M3) return fail(LSA_ERR_UNSUPPORTED, "the cache must be bf16 or fp8 (dtype %d)", dt);
+  *fp8 = dt == LSA_FP8_E4M3;
+  if (!c->k || !c->v || !c->page_table || !c->kv_len)
+    return fail(LSA_ERR_INVALID_ARG, "the cache's k, v, page_table and kv_len must be set");
+  if (*fp8 && (!c->k_scale || !c->v_scale)) return fail(LSA_ERR_INVALID_ARG, "an fp8 cache needs k_scale and v_scale");
+  if (!*fp8 && (c->k_scale || c->v_scale)) return fail(LSA_ERR_INVALID_ARG, "k_scale and v_scale are only for an fp8 cache");
+  if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
+    return fail(LSA_ERR_UNSUPPORTED, "page_tokens must be 16, 32, 64 or 128 (got %d)", c->page_tokens);
+  if (c->d_h != 64 && c->d_h != 128) return fail(LSA_ERR_UNSUPPORTED, "the cache's d_h must be 64 or 128 (got %d)", c->d_h);
+  if (c->n_kv < 1 || c->n_kv > kKvMaxHeads) return fail(LSA_ERR_UNSUPPORTED, "n_kv must be in [1, %d] (got %d)", kKvMaxHeads, c->n_kv);
+  if (c->n_pages < 1) return fail(LSA_ERR_INVALID_ARG, "n_pages must be >= 1 (got %d)", c->n_pages);
+  if (c->table_stride < 1 || c->table_stride > INT32_MAX / 16)
+    return fail(LSA_ERR_INVALID_ARG, "table_stride must be in [1, 2^27) (got %lld)", (long long)c->table_stride);
+  if (!aligned16(c->k) || !aligned16(c->v)) return fail(LSA_ERR_INVALID_ARG, "the cache's k and v must be 16-byte aligned");
+  *v = KvView{};
+  v->k = (char*)c->k; v->v = (char*)c->v; v->k_scale = c->k_scale; v->v_scale = c->v_scale;
+  v->table = c->page_table; v->kv_len = c->kv_len; v->table_stride = c->table_stride;
+  v->n_pages = c->n_pages; v->n_kv = c->n_kv;
+  v->pt_log2 = c->page_tokens == 16 ? 4 : c->page_tokens == 32 ? 5 : c->page_tokens == 64 ? 6 : 7;
+  return LSA_OK;
+}
+
+lsa_status check_rows(int32_t B, const int64_t* off, const int64_t* off_host, int32_t n_q, int32_t n_kv, const char* name) {
+  if (B < 1 || B > kKvMaxB) return fail(LSA_ERR_UNSUPPORTED, "B must be in [1, %d] (got %d)", kKvMaxB, B);
+  if (n_q < 1 || n_q % n_kv || n_q / n_kv > kKvMaxGroup)
+    return fail(LSA_ERR_UNSUPPORTED, "n_q must be a multiple of n_kv, at most %d times it (got %d for %d)", kKvMaxGroup, n_q, n_kv);
+  if (!off) return fail(LSA_ERR_INVALID_ARG, "%s is NULL", name);
+  lsa_status s;
+  if ((s = check_offsets(off_host, B, name)) != LSA_OK) return s;
+  if ((off_host[B] - off_host[0]) > INT32_MAX / std::max(n_q, n_kv))
+    return fail(LSA_ERR_UNSUPPORTED, "at most 2^31-1 rows times heads");
+  return LSA_OK;
+}
+
+// How an attention call is laid over the device; depends only on host arguments.
+struct AttendPlan {
+  int32_t row_tiles, splits, run;
+  int64_t blocks;  // row-block slots
+  size_t bytes;    // workspace
+};
+
+// Row blocks are as tall as the largest sequence needs, up to 64 rows. Keys are split in runs while
+// the row blocks alone do not fill the device (256 CUs, a few blocks each): to about 1024 blocks in
+// all, with runs of 4 tiles (one per wave) to `most` tiles, and not beyond kPartialBytes of partials.
+AttendPlan attend_plan(int64_t T, int32_t n_q, int32_t n_kv, int32_t d, int64_t max_tok, int64_t tiles, int32_t most,
+                       int64_t (*count)(const void*, int32_t, int64_t), const void* ctx) {
+  AttendPlan p{};
+  const int64_t G = n_q / n_kv, rows = max_tok * G;
+  p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  const int32_t M = 16 * p.row_tiles;
+  const int64_t filled = count(ctx, M, G) * n_kv;  // blocks with rows
+  tiles = std::max<int64_t>(tiles, 1);
+  int64_t run = tiles;
+  if (filled < 512) {
+    run = std::min<int64_t>(std::max<int64_t>((tiles * filled + 1023) / 1024, 4), most);
+    run = (run + 3) / 4 * 4;
+    const size_t per = (size_t)std::max<int64_t>(T, 1) * n_q * (d + 2) * 4;
+    const int64_t splits = std::max<int64_t>((int64_t)(kPartialBytes / per), 2);
+    run = std::max(run, (tiles + splits - 1) / splits);
+  }
+  p.run = (int32_t)std::min(run, tiles);
+  p.splits = (int32_t)((tiles + p.run - 1) / p.run);
+  p.bytes = p.splits > 1 ? (size_t)p.splits * T * n_q * (d + 2) * 4 : 0;
+  return p;
+}
+
+int64_t near_tiles(int64_t window, int64_t sinks) { return (sinks + 31) / 32 + (window > 0 ? (window + 30) / 32 + 1 : 0); }
+
+struct RaggedRows {
+  const int64_t* off;
+  int32_t B;
+};
+
+AttendPlan plan_ragged(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, const int64_t* off, int32_t max_kv_len,
+                       int32_t window, int32_t sinks) {
+  int64_t max_tok = 0;
+  for (int32_t b = 0; b < B; ++b) max_tok = std::max(max_tok, off[b + 1] - off[b]);
+  const int64_t T = off[B] - off[0], all = ((int64_t)max_kv_len + 31) / 32;
+  // a row block of several tokens sees that many more tiles; 64 rows are 64 tokens at most
+  const int64_t tiles = window > 0 ? std::min(all, near_tiles((int64_t)window + 63, sinks)) : all;
+  const RaggedRows ctx{off, B};
+  AttendPlan p = attend_plan(T, n_q, n_kv, d, max_tok, tiles, ATTEND_MAX_RUN,
+                             [](const void* c, int32_t M, int64_t G) {
+                               const RaggedRows& r = *static_cast<const RaggedRows*>(c);
+                               int64_t n = 0;
+                               for (int32_t b = 0; b < r.B; ++b) n += ((r.off[b + 1] - r.off[b]) * G + M - 1) / M;
+                               return n;
+                             }, &ctx);
+  p.blocks = T * (n_q / n_kv) / (16 * p.row_tiles) + B;
+  return p;
+}
+
+AttendPlan plan_listed(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t k, int32_t entry_tokens, int32_t window,
+                       int32_t sinks) {
+  const int64_t tiles = near_tiles(window, sinks) + ((int64_t)k * entry_tokens + 31) / 32;
+  AttendPlan p = attend_plan(B, n_q, n_kv, d, 1, tiles, ATTEND_MAX_RUN_LISTED,
+                             [](const void* c, int32_t M, int64_t G) { return *static_cast<const int32_t*>(c) * ((G + M - 1) / M); },
+                             &B);
+  const int64_t M = 16 * p.row_tiles;
+  p.blocks = B * ((n_q / n_kv + M - 1) / M);
+  return p;
+}
+
+// A window that reaches every cached token is none.
+void clip_window(int32_t max_kv_len, int32_t* window, int32_t* sinks) {
+  if (*window >= max_kv_len) *window = 0;
+  *sinks = *window > 0 ? std::min(*sinks, max_kv_len) : 0;
+}
+
+// The checks and launches that lsa_attend and lsa_attend_topk share. a.c, a.B, the rows and the keys are set.
+lsa_status attend_call(AttendArgs& a, const AttendPlan& p, bool fp8, int32_t d, bool listed, const void* q, int64_t q_stride,
+                       float softmax_scale, void* out, int64_t out_stride, float* lse, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  if (a.T == 0) return LSA_OK;  // no rows: q and out may be NULL
+  if (!q || !out) return fail(LSA_ERR_INVALID_ARG, "q and out must be set");
+  if (!aligned16(q) || !aligned16(out)) return fail(LSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if (q == out) return fail(LSA_ERR_INVALID_ARG, "out must not overlap q");
+  const int64_t row = (int64_t)a.n_q * d;
+  if (q_stride < row || out_stride < row || !multiple8(q_stride) || !multiple8(out_stride))
+    return fail(LSA_ERR_INVALID_ARG, "q_stride and out_stride must be multiples of 8, at least n_q * d_h = %lld", (long long)row);
+  if (!std::isfinite(softmax_scale)) return fail(LSA_ERR_INVALID_ARG, "softmax_scale must be finite");
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(LSA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
+    return fail(LSA_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", p.bytes, workspace_bytes);
+  if (p.bytes > 0 && !aligned16(workspace)) return fail(LSA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  if (p.blocks * p.splits * a.c.n_kv > kMaxBlocks || a.T * a.n_q > kMaxBlocks * 4)
+    return fail(LSA_ERR_UNSUPPORTED, "too many rows for one call");
+  a.q = (const uint16_t*)q; a.q_stride = q_stride; a.out = (uint16_t*)out; a.out_stride = out_stride; a.lse = lse;
+  a.G = a.n_q / a.c.n_kv;
+  a.blocks = p.blocks; a.splits = p.splits; a.run = p.run;
+  a.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+  a.part_o = (float*)workspace;
+  a.part_ml = a.part_o + (p.bytes ? (size_t)p.splits * a.T * a.n_q * d : 0);
+  hipError_t e = launch_attend_split(a, fp8, d, p.row_tiles, listed, stream);
+  if (e == hipSuccess && p.splits > 1) e = launch_attend_join(a, d, p.row_tiles, listed, stream);
+  return e == hipSuccess ? LSA_OK : hip_fail(listed ? "lsa_attend_topk launch" : "lsa_attend launch", e);
+}
+
+bool plan_sizes_ok(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h, int32_t window, int32_t sinks) {
+  return B >= 1 && B <= kKvMaxB && n_kv >= 1 && n_kv <= kKvMaxHeads && n_q >= 1 && n_q % n_kv == 0 &&
+         n_q / n_kv <= kKvMaxGroup && (d_h == 64 || d_h == 128) && window >= 0 && sinks >= 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+lsa_status lsa_kv_append(const lsa_kv_cache* cache, int32_t B, const void* k_new, int64_t k_stride, const void* v_new,
+                         int64_t v_stride, const void* q, int64_t q_stride, void* q_out, int32_t n_q,
+                         const int64_t* new_offsets, const int64_t* new_offsets_host, int32_t rope,
+                         const float* inv_freq, int32_t rot_dim, const int32_t* positions, hipStream_t stream) {
+  AppendArgs a{};
+  bool fp8 = false;
+  lsa_status s;
+  if ((s = check_cache(cache, &fp8, &a.c)) != LSA_OK) return s;
+  const int32_t n_kv = a.c.n_kv, d = cache->d_h;
+  if ((s = check_rows(B, new_offsets, new_offsets_host, q ? n_q : n_kv, n_kv, "new_offsets")) != LSA_OK) return s;
+  const int64_t T = new_offsets_host[B] - new_offsets_host[0];
+  if (T == 0) return LSA_OK;  // no rows: k_new, v_new and q may be NULL
+  if (!k_new || !v_new) return fail(LSA_ERR_INVALID_ARG, "k_new and v_new must be set");
+  if ((q == nullptr) != (q_out == nullptr)) return fail(LSA_ERR_INVALID_ARG, "q and q_out must be set together");
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(q) || !aligned16(q_out))
+    return fail(LSA_ERR_INVALID_ARG, "k_new, v_new, q and q_out must be 16-byte aligned");
+  const int64_t row = (int64_t)n_kv * d, q_row = (int64_t)n_q * d;
+  if (k_stride < row || v_stride < row || !multiple8(k_stride) || !multiple8(v_stride))
+    return fail(LSA_ERR_INVALID_ARG, "k_stride and v_stride must be multiples of 8, at least n_kv * d_h = %lld", (long long)row);
+  if (q && (q_stride < q_row || !multiple8(q_stride)))
+    return fail(LSA_ERR_INVALID_ARG, "q_stride must be a multiple of 8, at least n_q * d_h = %lld", (long long)q_row);
+  if (q && q == q_out && q_stride != q_row) return fail(LSA_ERR_INVALID_ARG, "q_out may be q only when q is contiguous");
+  if (rope != LSA_ROPE_NONE && rope != LSA_ROPE_HALVES && rope != LSA_ROPE_PAIRS)
+    return fail(LSA_ERR_INVALID_ARG, "unknown rope %d", rope);
+  if (rope != LSA_ROPE_NONE) {
+    if (!inv_freq) return fail(LSA_ERR_INVALID_ARG, "inv_freq must be set");
+    if (rot_dim < 16 || rot_dim % 16 || rot_dim > d)
+      return fail(LSA_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16 in [16, %d] (got %d)", d, rot_dim);
+  }
+  a.k_new = (const uint16_t*)k_new; a.v_new = (const uint16_t*)v_new; a.q = (const uint16_t*)q; a.q_out = (uint16_t*)q_out;
+  a.k_stride = k_stride; a.v_stride = v_stride; a.q_stride = q_stride;
+  a.off = new_offsets; a.positions = rope == LSA_ROPE_NONE ? nullptr : positions;
+  a.inv_freq = rope == LSA_ROPE_NONE ? nullptr : inv_freq;
+  a.first_row = new_offsets_host[0]; a.T = T; a.page_slots = append_page_slots(T, B, cache->page_tokens);
+  a.B = B; a.n_q = n_q; a.rot = rope == LSA_ROPE_NONE ? 0 : rot_dim;
+  // one block per page slot, key head, K and V; query blocks hold at least 32 rows times heads
+  if (a.page_slots * n_kv * 2 + (q ? T * n_q / 32 + 1 : 0) > kMaxBlocks)
+    return fail(LSA_ERR_UNSUPPORTED, "too many new tokens for one call");
+  const hipError_t e = launch_kv_append(a, fp8, d, rope, stream);
+  return e == hipSuccess ? LSA_OK : hip_fail("lsa_kv_append launch", e);
+}
+
+size_t lsa_attend_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h, const int64_t* q_offsets_host,
+                                 int32_t max_kv_len, int32_t window, int32_t sinks) {
+  if (!plan_sizes_ok(B, n_q, n_kv, d_h, window, sinks) || !q_offsets_host || max_kv_len < 0) return 0;
+  if (check_offsets(q_offsets_host, B, "q_offsets") != LSA_OK) return 0;
+  clip_window(max_kv_len, &window, &sinks);
+  return plan_ragged(B, n_q, n_kv, d_h, q_offsets_host, max_kv_len, window, sinks).bytes;
+}
+
+lsa_status lsa_attend(const lsa_kv_cache* cache, int32_t B, const void* q, int64_t q_stride, int32_t n_q,
+                      const int64_t* q_offsets, const int64_t* q_offsets_host, int32_t max_kv_len, float softmax_scale,
+                      int32_t window, int32_t sinks, void* out, int64_t out_stride, float* lse, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+  AttendArgs a{};
+  bool fp8 = false;
+  lsa_status s;
+  if ((s = check_cache(cache, &fp8, &a.c)) != LSA_OK) return s;
+  if ((s = check_rows(B, q_offsets, q_offsets_host, n_q, a.c.n_kv, "q_offsets")) != LSA_OK) return s;
+  if (window < 0 || sinks < 0) return fail(LSA_ERR_INVALID_ARG, "window and sinks must not be negative");
+  if (max_kv_len < 0 || max_kv_len > cache->table_stride * cache->page_tokens)
+    return fail(LSA_ERR_INVALID_ARG, "max_kv_len must be in [0, table_stride * page_tokens] (got %d)", max_kv_len);
+  if (max_kv_len > INT32_MAX - 64) return fail(LSA_ERR_UNSUPPORTED, "max_kv_len must be below 2^31 - 64");
+  clip_window(max_kv_len, &window, &sinks);
+  a.off = q_offsets; a.first_row = q_offsets_host[0]; a.T = q_offsets_host[B] - q_offsets_host[0];
+  a.B = B; a.n_q = n_q; a.max_kv_len = max_kv_len; a.window = window; a.sinks = sinks; a.r = 1;
+  const AttendPlan p = plan_ragged(B, n_q, a.c.n_kv, cache->d_h, q_offsets_host, max_kv_len, window, sinks);
+  return attend_call(a, p, fp8, cache->d_h, false, q, q_stride, softmax_scale, out, out_stride, lse, workspace,
+                     workspace_bytes, stream);
+}
+
+size_t lsa_attend_topk_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h, int32_t k,
+                                      int32_t entry_tokens, int32_t window, int32_t sinks) {
+  if (!plan_sizes_ok(B, n_q, n_kv, d_h, window, sinks) || k < 1 || entry_tokens < 1) return 0;
+  return plan_listed(B, n_q, n_kv, d_h, k, entry_tokens, window, sinks).bytes;
+}
+
+lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, int64_t q_stride, int32_t n_q,
+                           const int32_t* idx, const int32_t* count, int32_t k, int32_t entry_tokens,
+                           float softmax_scale, int32_t window, int32_t sinks, void* out, int64_t out_stride, float* lse,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  AttendArgs a{};
+  bool fp8 = false;
+  lsa_status s;
+  if ((s = check_cache(cache, &fp8, &a.c)) != LSA_OK) return s;
+  if (!plan_sizes_ok(B, n_q, a.c.n_kv, cache->d_h, 0, 0))
+    return fail(LSA_ERR_UNSUPPORTED, "B must be in [1, %d] and n_q a multiple of n_kv, at most %d times it", kKvMaxB, kKvMaxGroup);
+  if (!idx || !count) return fail(LSA_ERR_INVALID_ARG, "idx and count must be set");
+  if (k < 1 || k > 65536) return fail(LSA_ERR_UNSUPPORTED, "k must be in [1, 65536] (got %d)", k);
+  if (entry_tokens < 1 || entry_tokens > 128) return fail(LSA_ERR_UNSUPPORTED, "entry_tokens must be in [1, 128] (got %d)", entry_tokens);
+  if (window < 0 || sinks < 0) return fail(LSA_ERR_INVALID_ARG, "window and sinks must not be negative");
+  a.max_kv_len = (int32_t)std::min<int64_t>(cache->table_stride * cache->page_tokens, INT32_MAX - 64);
+  a.idx = idx; a.count = count; a.k = k; a.r = entry_tokens;
+  a.first_row = 0; a.T = B; a.B = B; a.n_q = n_q;
+  const AttendPlan p = plan_listed(B, n_q, a.c.n_kv, cache->d_h, k, entry_tokens, window, sinks);
+  a.window = std::min(window, a.max_kv_len); a.sinks = std::min(sinks, a.max_kv_len);
+  return attend_call(a, p, fp8, cache->d_h, true, q, q_stride, softmax_scale, out, out_stride, lse, workspace,
+                     workspace_bytes, stream);
 }
 
 }  // extern "C"

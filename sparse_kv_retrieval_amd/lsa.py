@@ -58,6 +58,15 @@ class TopkLayer(ctypes.Structure):
                 ("topk_idx_out", _vp), ("topk_score_out", _vp)]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("page_table", _vp), ("kv_len", _vp),
+                ("table_stride", _i64), ("n_pages", _i32), ("n_kv", _i32), ("page_tokens", _i32), ("d_h", _i32),
+                ("dtype", _i32)]
+
+
+ROPE = {None: 0, "none": 0, "halves": 1, "pairs": 2}
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -95,6 +104,14 @@ _golden = _sig("lsa_golden_labels", _i32, [_vp, _i64, _i32, _i32, _vp, _f32, _i3
 _train_ws = _sig("lsa_train_workspace_size", _sz, [_i32, _vp, _i32])
 _train = _sig("lsa_train_step", _i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
                                        _i32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+_kv_append = _sig("lsa_kv_append", _i32, [ctypes.POINTER(_KvCache), _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _vp,
+                                          _vp, _i32, _vp, _i32, _vp, _vp])
+_attend_ws = _sig("lsa_attend_workspace_size", _sz, [_i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32])
+_attend = _sig("lsa_attend", _i32, [ctypes.POINTER(_KvCache), _i32, _vp, _i64, _i32, _vp, _vp, _i32, _f32, _i32, _i32,
+                                    _vp, _i64, _vp, _vp, _sz, _vp])
+_attend_topk_ws = _sig("lsa_attend_topk_workspace_size", _sz, [_i32] * 8)
+_attend_topk = _sig("lsa_attend_topk", _i32, [ctypes.POINTER(_KvCache), _i32, _vp, _i64, _i32, _vp, _vp, _i32, _i32,
+                                              _f32, _i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp])
 _debug_range_errors = _sig("lsa_debug_range_errors", _i32, [_vp, ctypes.POINTER(_i64)])
 _last_error = _sig("lsa_last_error", ctypes.c_char_p, [])
 _version = _sig("lsa_version", _i32, [])
@@ -103,7 +120,8 @@ EXPORTED = ("lsa_project", "lsa_pack_weights_size", "lsa_pack_weights", "lsa_pro
             "lsa_score_select_ex", "lsa_topk_step", "lsa_topk_step_noalloc",
             "lsa_topk_score", "lsa_topk_select", "lsa_union_compact", "lsa_topk_workspace_size", "lsa_topk",
             "lsa_gather", "lsa_fetch_host", "lsa_golden_workspace_size", "lsa_golden_labels", "lsa_train_workspace_size",
-            "lsa_train_step", "lsa_debug_range_errors", "lsa_last_error",
+            "lsa_train_step", "lsa_kv_append", "lsa_attend_workspace_size", "lsa_attend",
+            "lsa_attend_topk_workspace_size", "lsa_attend_topk", "lsa_debug_range_errors", "lsa_last_error",
             "lsa_version")
 
 
@@ -335,3 +353,172 @@ def train_step(*, h, w_dq, w_iuq, w_w, keys, key_offsets, key_offsets_host, labe
                                     _p(mask_word_offsets), mop, int(B), int(d), int(r), int(n_h), int(d_h),
                                     float(gamma), float(alpha), _p(loss), _p(g_dq), _p(g_iuq), _p(g_w),
                                     _p(workspace), _nbytes(workspace), _stream(stream)))
+
+
+# ------------------------------------------------------------------ the paged cache
+def _refuse(fn, msg):
+    raise LsaError(fn, ERR_INVALID_ARG, msg)
+
+
+def _want(fn, name, t, dtype, shape, device, contiguous=True):
+    """Checks a tensor argument; None in `shape` is any size."""
+    if str(t.dtype) != "torch." + dtype:
+        _refuse(fn, f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        _refuse(fn, f"{name} must be {['any' if n is None else n for n in shape]} (got {list(t.shape)})")
+    if device is not None and t.device != device:
+        _refuse(fn, f"{name} must be on {device} (got {t.device})")
+    if contiguous and not t.is_contiguous():
+        _refuse(fn, f"{name} must be contiguous")
+
+
+def _row_stride(fn, name, t):
+    """Elements from one row of a [rows, heads, d] tensor to the next; a row itself is contiguous."""
+    rows, heads, d = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        _refuse(fn, f"the rows of {name} must be contiguous (strides {t.stride()})")
+    return t.stride(0) if rows > 1 else heads * d
+
+
+def _offsets(fn, name, off, host, B, rows, device):
+    """Checks device and host offsets of rows; returns (the host array, its pointer)."""
+    _want(fn, name, off, "int64", (B + 1,), device)
+    arr, ptr = _host64(host)
+    if arr.shape != (B + 1,):
+        _refuse(fn, f"{name}_host must have {B + 1} elements (got {arr.shape})")
+    if int(arr[B]) > rows:
+        _refuse(fn, f"{name}_host ends at {int(arr[B])}, behind the {rows} rows")
+    return arr, ptr
+
+
+def _launch(device, fn, call, args, stream):
+    """The call on the tensors' device, whichever is current, on `stream` or that device's current one."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        _check(fn, call(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn, call(*args, stream))
+
+
+class KvCache:
+    """The lsa_kv_cache of one layer: k and v [n_pages, n_kv, page_tokens, d_h] in bfloat16, or in
+    float8_e4m3fn with k_scale and v_scale [n_pages, n_kv] float32; page_table [B, pages] and kv_len [B] int32.
+
+    Holds the tensors. Their contents may change between calls; the tensors themselves stay."""
+
+    def __init__(self, *, k, v, page_table, kv_len, k_scale=None, v_scale=None):
+        fn = "KvCache"
+        if str(k.dtype) not in ("torch.bfloat16", "torch.float8_e4m3fn"):
+            _refuse(fn, f"k must be bfloat16 or float8_e4m3fn (got {k.dtype})")
+        if k.dim() != 4:
+            _refuse(fn, f"k must be [n_pages, n_kv, page_tokens, d_h] (got {list(k.shape)})")
+        fp8 = str(k.dtype) == "torch.float8_e4m3fn"
+        name = "float8_e4m3fn" if fp8 else "bfloat16"
+        _want(fn, "k", k, name, (None,) * 4, None)
+        _want(fn, "v", v, name, tuple(k.shape), k.device)
+        if fp8 != (k_scale is not None) or fp8 != (v_scale is not None):
+            _refuse(fn, "k_scale and v_scale are needed for float8_e4m3fn, and only for it")
+        if fp8:
+            _want(fn, "k_scale", k_scale, "float32", tuple(k.shape[:2]), k.device)
+            _want(fn, "v_scale", v_scale, "float32", tuple(k.shape[:2]), k.device)
+        _want(fn, "kv_len", kv_len, "int32", (None,), k.device)
+        _want(fn, "page_table", page_table, "int32", (kv_len.shape[0], None), k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table, self.kv_len = page_table, kv_len
+        self.device, self.B = k.device, kv_len.shape[0]
+        self.n_pages, self.n_kv, self.page_tokens, self.d_h = k.shape
+        self._c = _KvCache(_p(k), _p(v), _p(k_scale), _p(v_scale), _p(page_table), _p(kv_len), page_table.shape[1],
+                           self.n_pages, self.n_kv, self.page_tokens, self.d_h, FP8_E4M3 if fp8 else BF16)
+        self.ref = ctypes.byref(self._c)
+
+
+def kv_append(cache, k_new, v_new, *, new_offsets, new_offsets_host, q=None, q_out=None, inv_freq=None, rope="halves",
+              positions=None, stream=None):
+    """lsa_kv_append: k_new, v_new [rows, n_kv, d_h] and q [rows, n_q, d_h] bfloat16, with contiguous rows at any
+    distance; q_out [rows, n_q, d_h] contiguous; new_offsets [B + 1] int64 on the device and on the host; inv_freq
+    [rot_dim / 2] float32, None for no rotation; rope "halves" or "pairs"; positions [rows] int32 or None."""
+    fn = "lsa_kv_append"
+    dev, B = cache.device, cache.B
+    rows = k_new.shape[0]
+    _want(fn, "k_new", k_new, "bfloat16", (rows, cache.n_kv, cache.d_h), dev, False)
+    _want(fn, "v_new", v_new, "bfloat16", (rows, cache.n_kv, cache.d_h), dev, False)
+    n_q, qs = 0, 0
+    if (q is None) != (q_out is None):
+        _refuse(fn, "q and q_out must be set together")
+    if q is not None:
+        n_q = q.shape[1]
+        _want(fn, "q", q, "bfloat16", (rows, None, cache.d_h), dev, False)
+        _want(fn, "q_out", q_out, "bfloat16", (rows, n_q, cache.d_h), dev)
+        qs = _row_stride(fn, "q", q)
+    style = ROPE.get(rope, -1)
+    if style < 0:
+        _refuse(fn, f"unknown rope {rope!r}")
+    rot = 0
+    if inv_freq is None:
+        style = 0
+    else:
+        _want(fn, "inv_freq", inv_freq, "float32", (None,), dev)
+        rot = 2 * inv_freq.shape[0]
+    if positions is not None:
+        _want(fn, "positions", positions, "int32", (rows,), dev)
+    off, offp = _offsets(fn, "new_offsets", new_offsets, new_offsets_host, B, rows, dev)
+    _launch(dev, fn, _kv_append,
+            (cache.ref, B, k_new.data_ptr(), _row_stride(fn, "k_new", k_new), v_new.data_ptr(),
+             _row_stride(fn, "v_new", v_new), _p(q), qs, _p(q_out), n_q, new_offsets.data_ptr(), offp, style, _p(inv_freq),
+             rot, _p(positions)), stream)
+
+
+def attend_workspace_size(cache, *, n_q, q_offsets_host, max_kv_len, window=0, sinks=0) -> int:
+    """lsa_attend_workspace_size for this cache."""
+    off, offp = _host64(q_offsets_host)
+    return int(_attend_ws(off.size - 1, n_q, cache.n_kv, cache.d_h, offp, max_kv_len, window, sinks))
+
+
+def _attend_tensors(fn, cache, q, out, lse, workspace):
+    dev, rows = cache.device, q.shape[0]
+    _want(fn, "q", q, "bfloat16", (rows, None, cache.d_h), dev, False)
+    n_q = q.shape[1]
+    _want(fn, "out", out, "bfloat16", (rows, n_q, cache.d_h), dev, False)
+    if lse is not None:
+        _want(fn, "lse", lse, "float32", (rows, n_q), dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        _refuse(fn, f"workspace must be contiguous and on {dev}")
+    return n_q, _row_stride(fn, "q", q), _row_stride(fn, "out", out)
+
+
+def attend(cache, q, *, q_offsets, q_offsets_host, max_kv_len, out, scale, window=0, sinks=0, lse=None, workspace=None,
+           stream=None):
+    """lsa_attend: q and out [rows, n_q, d_h] bfloat16 with contiguous rows at any distance, lse [rows, n_q] float32
+    or None; q_offsets [B + 1] int64 on the device and on the host; workspace a tensor of at least
+    attend_workspace_size(...) bytes for the same arguments."""
+    fn = "lsa_attend"
+    n_q, qs, os_ = _attend_tensors(fn, cache, q, out, lse, workspace)
+    off, offp = _offsets(fn, "q_offsets", q_offsets, q_offsets_host, cache.B, q.shape[0], cache.device)
+    _launch(cache.device, fn, _attend,
+            (cache.ref, cache.B, q.data_ptr(), qs, n_q, q_offsets.data_ptr(), offp, max_kv_len, scale, window, sinks,
+             out.data_ptr(), os_, _p(lse), _p(workspace), _nbytes(workspace)), stream)
+
+
+def attend_topk_workspace_size(cache, *, n_q, k, entry_tokens=1, window=0, sinks=0) -> int:
+    """lsa_attend_topk_workspace_size for this cache."""
+    return int(_attend_topk_ws(cache.B, n_q, cache.n_kv, cache.d_h, k, entry_tokens, window, sinks))
+
+
+def attend_topk(cache, q, *, idx, count, out, scale, entry_tokens=1, window=0, sinks=0, lse=None, workspace=None,
+                stream=None):
+    """lsa_attend_topk: q and out [B, n_q, d_h] bfloat16, idx [B, k] and count [B] int32 as topk and topk_step
+    write them, lse [B, n_q] float32 or None; workspace of at least attend_topk_workspace_size(...) bytes."""
+    fn = "lsa_attend_topk"
+    if q.shape[0] != cache.B:
+        _refuse(fn, f"q must have one row per sequence (got {q.shape[0]} for {cache.B})")
+    n_q, qs, os_ = _attend_tensors(fn, cache, q, out, lse, workspace)
+    _want(fn, "idx", idx, "int32", (cache.B, None), cache.device)
+    _want(fn, "count", count, "int32", (cache.B,), cache.device)
+    _launch(cache.device, fn, _attend_topk,
+            (cache.ref, cache.B, q.data_ptr(), qs, n_q, idx.data_ptr(), count.data_ptr(), idx.shape[1], entry_tokens, scale,
+             window, sinks, out.data_ptr(), os_, _p(lse), _p(workspace), _nbytes(workspace)), stream)
