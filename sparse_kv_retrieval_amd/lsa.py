@@ -356,53 +356,68 @@ def train_step(*, h, w_dq, w_iuq, w_w, keys, key_offsets, key_offsets_host, labe
 
 
 # ------------------------------------------------------------------ the paged cache
+# These calls take a few microseconds on the device, so their checks are kept to a few comparisons per tensor;
+# the text of a refusal is only made when there is one.
 def _refuse(fn, msg):
     raise LsaError(fn, ERR_INVALID_ARG, msg)
 
 
-def _want(fn, name, t, dtype, shape, device, contiguous=True):
-    """Checks a tensor argument; None in `shape` is any size."""
-    if str(t.dtype) != "torch." + dtype:
-        _refuse(fn, f"{name} must be {dtype} (got {t.dtype})")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        _refuse(fn, f"{name} must be {['any' if n is None else n for n in shape]} (got {list(t.shape)})")
-    if device is not None and t.device != device:
-        _refuse(fn, f"{name} must be on {device} (got {t.device})")
-    if contiguous and not t.is_contiguous():
-        _refuse(fn, f"{name} must be contiguous")
+def _want(fn, name, t, dtype, shape, device):
+    """A contiguous tensor of this dtype and shape on the device of this index (-1: host)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(fn, f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on device {device} "
+                    f"(got {t.dtype}, {list(t.shape)}, strides {t.stride()}, device {t.get_device()})")
 
 
-def _row_stride(fn, name, t):
-    """Elements from one row of a [rows, heads, d] tensor to the next; a row itself is contiguous."""
-    rows, heads, d = t.shape
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-        _refuse(fn, f"the rows of {name} must be contiguous (strides {t.stride()})")
-    return t.stride(0) if rows > 1 else heads * d
+def _rows(fn, name, t, dtype, shape, device):
+    """A [rows, heads, d] tensor whose rows are contiguous, at any distance, which is returned."""
+    step, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != device or one != 1 or
+            (head != shape[2] and shape[1] > 1)):
+        _refuse(fn, f"{name} must be a {dtype} tensor of shape {list(shape)} with contiguous rows on device {device} "
+                    f"(got {t.dtype}, {list(t.shape)}, strides {t.stride()}, device {t.get_device()})")
+    return step if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _offsets(fn, name, off, host, B, rows, device):
     """Checks device and host offsets of rows; returns (the host array, its pointer)."""
-    _want(fn, name, off, "int64", (B + 1,), device)
-    arr, ptr = _host64(host)
-    if arr.shape != (B + 1,):
-        _refuse(fn, f"{name}_host must have {B + 1} elements (got {arr.shape})")
-    if int(arr[B]) > rows:
-        _refuse(fn, f"{name}_host ends at {int(arr[B])}, behind the {rows} rows")
-    return arr, ptr
+    if off.dtype is not _torch().int64 or off.shape != (B + 1,) or off.get_device() != device or not off.is_contiguous():
+        _want(fn, name, off, _torch().int64, (B + 1,), device)
+    if type(host) is not np.ndarray or host.dtype != np.int64 or not host.flags.c_contiguous:
+        host = _host64(host)[0]
+    if host.shape != (B + 1,) or host[B] > rows:
+        _refuse(fn, f"{name}_host must have {B + 1} elements and end within the {rows} rows (got {host.shape[0]}, "
+                    f"ending at {host[-1]})")
+    return host, host.__array_interface__["data"][0]
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
 
 
 def _launch(device, fn, call, args, stream):
-    """The call on the tensors' device, whichever is current, on `stream` or that device's current one."""
-    import torch
+    """The call on the device of this index, whichever is current, on `stream` or that device's current one."""
+    torch = _torch()
+    if device < 0:
+        _refuse(fn, "the tensors must be on a GPU")
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if device.index == torch.cuda.current_device():
-        _check(fn, call(*args, stream))
+    if device == torch._C._cuda_getDevice():
+        st = call(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn, call(*args, stream))
+            st = call(*args, stream)
+    if st != OK:
+        raise LsaError(fn, st, last_error())
 
 
 class KvCache:
@@ -412,29 +427,37 @@ class KvCache:
     Holds the tensors. Their contents may change between calls; the tensors themselves stay."""
 
     def __init__(self, *, k, v, page_table, kv_len, k_scale=None, v_scale=None):
-        fn = "KvCache"
-        if str(k.dtype) not in ("torch.bfloat16", "torch.float8_e4m3fn"):
-            _refuse(fn, f"k must be bfloat16 or float8_e4m3fn (got {k.dtype})")
-        if k.dim() != 4:
-            _refuse(fn, f"k must be [n_pages, n_kv, page_tokens, d_h] (got {list(k.shape)})")
-        fp8 = str(k.dtype) == "torch.float8_e4m3fn"
-        name = "float8_e4m3fn" if fp8 else "bfloat16"
-        _want(fn, "k", k, name, (None,) * 4, None)
-        _want(fn, "v", v, name, tuple(k.shape), k.device)
+        fn, torch = "KvCache", _torch()
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or k.dim() != 4:
+            _refuse(fn, f"k must be [n_pages, n_kv, page_tokens, d_h] in bfloat16 or float8_e4m3fn (got {k.dtype}, "
+                        f"{list(k.shape)})")
+        fp8 = k.dtype == torch.float8_e4m3fn
+        self.device = dev = k.get_device()
+        self.n_pages, self.n_kv, self.page_tokens, self.d_h = k.shape
+        _want(fn, "k", k, k.dtype, k.shape, dev)
+        _want(fn, "v", v, k.dtype, k.shape, dev)
         if fp8 != (k_scale is not None) or fp8 != (v_scale is not None):
             _refuse(fn, "k_scale and v_scale are needed for float8_e4m3fn, and only for it")
         if fp8:
-            _want(fn, "k_scale", k_scale, "float32", tuple(k.shape[:2]), k.device)
-            _want(fn, "v_scale", v_scale, "float32", tuple(k.shape[:2]), k.device)
-        _want(fn, "kv_len", kv_len, "int32", (None,), k.device)
-        _want(fn, "page_table", page_table, "int32", (kv_len.shape[0], None), k.device)
+            _want(fn, "k_scale", k_scale, torch.float32, k.shape[:2], dev)
+            _want(fn, "v_scale", v_scale, torch.float32, k.shape[:2], dev)
+        if kv_len.dim() != 1 or page_table.dim() != 2:
+            _refuse(fn, "kv_len must be [B] and page_table [B, pages]")
+        self.B = kv_len.shape[0]
+        _want(fn, "kv_len", kv_len, torch.int32, (self.B,), dev)
+        _want(fn, "page_table", page_table, torch.int32, (self.B, page_table.shape[1]), dev)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.page_table, self.kv_len = page_table, kv_len
-        self.device, self.B = k.device, kv_len.shape[0]
-        self.n_pages, self.n_kv, self.page_tokens, self.d_h = k.shape
         self._c = _KvCache(_p(k), _p(v), _p(k_scale), _p(v_scale), _p(page_table), _p(kv_len), page_table.shape[1],
                            self.n_pages, self.n_kv, self.page_tokens, self.d_h, FP8_E4M3 if fp8 else BF16)
         self.ref = ctypes.byref(self._c)
+
+
+def _three(fn, name, t):
+    shape = t.shape
+    if len(shape) != 3:
+        _refuse(fn, f"{name} must be [rows, heads, d_h] (got {list(shape)})")
+    return shape
 
 
 def kv_append(cache, k_new, v_new, *, new_offsets, new_offsets_host, q=None, q_out=None, inv_freq=None, rope="halves",
@@ -442,35 +465,35 @@ def kv_append(cache, k_new, v_new, *, new_offsets, new_offsets_host, q=None, q_o
     """lsa_kv_append: k_new, v_new [rows, n_kv, d_h] and q [rows, n_q, d_h] bfloat16, with contiguous rows at any
     distance; q_out [rows, n_q, d_h] contiguous; new_offsets [B + 1] int64 on the device and on the host; inv_freq
     [rot_dim / 2] float32, None for no rotation; rope "halves" or "pairs"; positions [rows] int32 or None."""
-    fn = "lsa_kv_append"
-    dev, B = cache.device, cache.B
-    rows = k_new.shape[0]
-    _want(fn, "k_new", k_new, "bfloat16", (rows, cache.n_kv, cache.d_h), dev, False)
-    _want(fn, "v_new", v_new, "bfloat16", (rows, cache.n_kv, cache.d_h), dev, False)
-    n_q, qs = 0, 0
-    if (q is None) != (q_out is None):
+    fn, torch = "lsa_kv_append", _torch()
+    dev, B, bf16 = cache.device, cache.B, torch.bfloat16
+    shape = _three(fn, "k_new", k_new)
+    rows, d = shape[0], cache.d_h
+    shape = (rows, cache.n_kv, d)
+    ks = _rows(fn, "k_new", k_new, bf16, shape, dev)
+    vs = _rows(fn, "v_new", v_new, bf16, shape, dev)
+    n_q = qs = rot = 0
+    q_at = q_out_at = inv_at = pos_at = None
+    if q is not None and q_out is not None:
+        n_q = _three(fn, "q", q)[1]
+        qs = _rows(fn, "q", q, bf16, (rows, n_q, d), dev)
+        _want(fn, "q_out", q_out, bf16, (rows, n_q, d), dev)
+        q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
+    elif q is not None or q_out is not None:
         _refuse(fn, "q and q_out must be set together")
-    if q is not None:
-        n_q = q.shape[1]
-        _want(fn, "q", q, "bfloat16", (rows, None, cache.d_h), dev, False)
-        _want(fn, "q_out", q_out, "bfloat16", (rows, n_q, cache.d_h), dev)
-        qs = _row_stride(fn, "q", q)
     style = ROPE.get(rope, -1)
-    if style < 0:
-        _refuse(fn, f"unknown rope {rope!r}")
-    rot = 0
-    if inv_freq is None:
+    if inv_freq is None and style >= 0:
         style = 0
-    else:
-        _want(fn, "inv_freq", inv_freq, "float32", (None,), dev)
+    elif style > 0:
         rot = 2 * inv_freq.shape[0]
+        _want(fn, "inv_freq", inv_freq, torch.float32, (rot // 2,), dev)
+        inv_at = inv_freq.data_ptr()
     if positions is not None:
-        _want(fn, "positions", positions, "int32", (rows,), dev)
-    off, offp = _offsets(fn, "new_offsets", new_offsets, new_offsets_host, B, rows, dev)
-    _launch(dev, fn, _kv_append,
-            (cache.ref, B, k_new.data_ptr(), _row_stride(fn, "k_new", k_new), v_new.data_ptr(),
-             _row_stride(fn, "v_new", v_new), _p(q), qs, _p(q_out), n_q, new_offsets.data_ptr(), offp, style, _p(inv_freq),
-             rot, _p(positions)), stream)
+        _want(fn, "positions", positions, torch.int32, (rows,), dev)
+        pos_at = positions.data_ptr()
+    host, host_at = _offsets(fn, "new_offsets", new_offsets, new_offsets_host, B, rows, dev)
+    _launch(dev, fn, _kv_append, (cache.ref, B, k_new.data_ptr(), ks, v_new.data_ptr(), vs, q_at, qs, q_out_at, n_q,
+                                  new_offsets.data_ptr(), host_at, style, inv_at, rot, pos_at), stream)
 
 
 def attend_workspace_size(cache, *, n_q, q_offsets_host, max_kv_len, window=0, sinks=0) -> int:
@@ -480,15 +503,22 @@ def attend_workspace_size(cache, *, n_q, q_offsets_host, max_kv_len, window=0, s
 
 
 def _attend_tensors(fn, cache, q, out, lse, workspace):
-    dev, rows = cache.device, q.shape[0]
-    _want(fn, "q", q, "bfloat16", (rows, None, cache.d_h), dev, False)
-    n_q = q.shape[1]
-    _want(fn, "out", out, "bfloat16", (rows, n_q, cache.d_h), dev, False)
+    torch, dev = _torch(), cache.device
+    shape = _three(fn, "q", q)
+    rows, n_q = shape[0], shape[1]
+    shape = (rows, n_q, cache.d_h)
+    qs = _rows(fn, "q", q, torch.bfloat16, shape, dev)
+    os_ = _rows(fn, "out", out, torch.bfloat16, shape, dev)
+    lse_at = ws_at = None
+    nbytes = 0
     if lse is not None:
-        _want(fn, "lse", lse, "float32", (rows, n_q), dev)
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-        _refuse(fn, f"workspace must be contiguous and on {dev}")
-    return n_q, _row_stride(fn, "q", q), _row_stride(fn, "out", out)
+        _want(fn, "lse", lse, torch.float32, (rows, n_q), dev)
+        lse_at = lse.data_ptr()
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse(fn, f"workspace must be contiguous and on device {dev}")
+        ws_at, nbytes = workspace.data_ptr(), workspace.nbytes
+    return rows, n_q, qs, os_, lse_at, ws_at, nbytes
 
 
 def attend(cache, q, *, q_offsets, q_offsets_host, max_kv_len, out, scale, window=0, sinks=0, lse=None, workspace=None,
@@ -497,11 +527,10 @@ def attend(cache, q, *, q_offsets, q_offsets_host, max_kv_len, out, scale, windo
     or None; q_offsets [B + 1] int64 on the device and on the host; workspace a tensor of at least
     attend_workspace_size(...) bytes for the same arguments."""
     fn = "lsa_attend"
-    n_q, qs, os_ = _attend_tensors(fn, cache, q, out, lse, workspace)
-    off, offp = _offsets(fn, "q_offsets", q_offsets, q_offsets_host, cache.B, q.shape[0], cache.device)
-    _launch(cache.device, fn, _attend,
-            (cache.ref, cache.B, q.data_ptr(), qs, n_q, q_offsets.data_ptr(), offp, max_kv_len, scale, window, sinks,
-             out.data_ptr(), os_, _p(lse), _p(workspace), _nbytes(workspace)), stream)
+    rows, n_q, qs, os_, lse_at, ws_at, nbytes = _attend_tensors(fn, cache, q, out, lse, workspace)
+    host, host_at = _offsets(fn, "q_offsets", q_offsets, q_offsets_host, cache.B, rows, cache.device)
+    _launch(cache.device, fn, _attend, (cache.ref, cache.B, q.data_ptr(), qs, n_q, q_offsets.data_ptr(), host_at, max_kv_len,
+                                        scale, window, sinks, out.data_ptr(), os_, lse_at, ws_at, nbytes), stream)
 
 
 def attend_topk_workspace_size(cache, *, n_q, k, entry_tokens=1, window=0, sinks=0) -> int:
@@ -513,12 +542,13 @@ def attend_topk(cache, q, *, idx, count, out, scale, entry_tokens=1, window=0, s
                 stream=None):
     """lsa_attend_topk: q and out [B, n_q, d_h] bfloat16, idx [B, k] and count [B] int32 as topk and topk_step
     write them, lse [B, n_q] float32 or None; workspace of at least attend_topk_workspace_size(...) bytes."""
-    fn = "lsa_attend_topk"
-    if q.shape[0] != cache.B:
-        _refuse(fn, f"q must have one row per sequence (got {q.shape[0]} for {cache.B})")
-    n_q, qs, os_ = _attend_tensors(fn, cache, q, out, lse, workspace)
-    _want(fn, "idx", idx, "int32", (cache.B, None), cache.device)
-    _want(fn, "count", count, "int32", (cache.B,), cache.device)
-    _launch(cache.device, fn, _attend_topk,
-            (cache.ref, cache.B, q.data_ptr(), qs, n_q, idx.data_ptr(), count.data_ptr(), idx.shape[1], entry_tokens, scale,
-             window, sinks, out.data_ptr(), os_, _p(lse), _p(workspace), _nbytes(workspace)), stream)
+    fn, torch, B = "lsa_attend_topk", _torch(), cache.B
+    rows, n_q, qs, os_, lse_at, ws_at, nbytes = _attend_tensors(fn, cache, q, out, lse, workspace)
+    if rows != B or idx.dim() != 2:
+        _refuse(fn, f"q must have one row per sequence and idx must be [B, k] (got {rows} rows for {B}, {list(idx.shape)})")
+    k = idx.shape[1]
+    _want(fn, "idx", idx, torch.int32, (B, k), cache.device)
+    _want(fn, "count", count, torch.int32, (B,), cache.device)
+    _launch(cache.device, fn, _attend_topk, (cache.ref, B, q.data_ptr(), qs, n_q, idx.data_ptr(), count.data_ptr(), k,
+                                             entry_tokens, scale, window, sinks, out.data_ptr(), os_, lse_at, ws_at, nbytes),
+            stream)
