@@ -27,65 +27,6 @@ namespace lsa {
 
 static constexpr int AT_WAVES = 4;
 static constexpr int AT_THREADS = 64 * AT_WAVES;
-static constexpr float LAZY = 8.0f;
-static constexpr float LOWEST = -3.402823466e38f;  // running maximum of a row that has seen nothing
-static constexpr float LN2 = 0.6931471805599453f;
-
-// One row block: rows r0 .. r0 + n - 1 of sequence b for key head h.
-struct Rows {
-  int32_t b, n, r0;
-  int32_t p0;          // position of the sequence's first query token (negative: it has fewer cached tokens)
-  int32_t p_lo, p_hi;  // positions of the block's first and last row
-  int64_t t0;          // row number of the sequence's first token in q
-  TileRange near;      // tiles seen by position
-  int32_t tiles;       // those and the listed ones
-};
-
-template <bool LISTED>
-__device__ __forceinline__ void set_block(const AttendArgs& a, int64_t n_tok, int64_t j, int M, Rows* w) {
-  const int64_t rows = n_tok * a.G;
-  w->r0 = (int32_t)(j * M);
-  w->n = (int32_t)min((int64_t)M, rows - j * M);
-  const int32_t len = min(max(a.c.kv_len[w->b], 0), a.max_kv_len);
-  w->p0 = (int32_t)(len - n_tok);
-  w->p_lo = w->p0 + w->r0 / a.G;
-  w->p_hi = w->p0 + (w->r0 + w->n - 1) / a.G;
-  if constexpr (LISTED) {
-    const int64_t some = (int64_t)min(max(a.count[w->b], 0), a.k) * a.r;
-    if (a.window > 0) {
-      w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks);
-    } else {
-      const int32_t end = w->p_hi < 0 ? 0 : w->p_hi / 32 + 1, s = a.sinks / 32 + (a.sinks % 32 != 0);
-      w->near.n_first = w->near.n = min(s, end);
-      w->near.first_b = 0;
-    }
-    w->tiles = w->p_hi < 0 ? 0 : w->near.n + (int32_t)((some + 31) / 32);
-  } else {
-    w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks);
-    w->tiles = w->near.n;
-  }
-}
-
-template <bool LISTED>
-__device__ __forceinline__ bool find_rows(const AttendArgs& a, int64_t block, int M, Rows* w) {
-  int64_t n_tok, j;
-  if constexpr (LISTED) {
-    const int per = (a.G + M - 1) / M;
-    w->b = (int)(block / per);
-    w->t0 = w->b;
-    n_tok = 1;
-    j = block % per;
-  } else {
-    auto slot_of = [&](int x) -> int64_t { return (a.off[x] - a.first_row) * a.G / M + x; };
-    w->b = wave_find(a.B, block, slot_of);
-    w->t0 = a.off[w->b];
-    n_tok = a.off[w->b + 1] - w->t0;
-    j = block - slot_of(w->b);
-    if (j * M >= n_tok * a.G) return false;
-  }
-  set_block<LISTED>(a, n_tok, j, M, w);
-  return true;
-}
 
 // One wave's tile of 32 keys in registers.
 template <bool FP8, int D>
@@ -198,7 +139,7 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
 
   // the block's queries: lane column = row
   bf16x8 q[RT][KS];
-  int32_t p_row[RT];
+  int32_t p_row[RT], w_row[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int r = rt * 16 + col;
@@ -206,6 +147,7 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
     const int row = w.r0 + (live ? r : w.n - 1);
     const int tok = row / a.G;
     p_row[rt] = w.p0 + tok;
+    w_row[rt] = window_start(a, p_row[rt]);
     const uint16_t* src = a.q + (w.t0 + tok) * a.q_stride + (int64_t)(h * a.G + (row - tok * a.G)) * D;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -219,7 +161,7 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
   float m[RT], l[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    m[rt] = LOWEST;
+    m[rt] = ATTEND_LOWEST;
     l[rt] = 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[rt][i] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -234,7 +176,7 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
       if constexpr (LISTED) {
         if (tile < w.near.n) {
           tok = (int64_t)w.near.tile(tile) * 32 + i % 32;
-          const bool seen = tok <= w.p_hi && ((a.window > 0 && tok > (int64_t)w.p_hi - a.window) || tok < a.sinks);
+          const bool seen = tok <= w.p_hi && ((a.window > 0 && tok > w.w_hi) || tok < a.sinks);
           tok = seen ? tok : -1;
         } else {
           const int64_t at = (int64_t)(tile - w.near.n) * 32 + i % 32;
@@ -243,14 +185,14 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
             const int32_t* list = a.idx + (int64_t)w.b * a.k;
             const int32_t entry = list[e];
             tok = (int64_t)entry * a.r + at % a.r;
-            const bool near = (a.window > 0 && tok > (int64_t)w.p_hi - a.window) || tok < a.sinks;
+            const bool near = (a.window > 0 && tok > w.w_hi) || tok < a.sinks;
             if (entry < 0 || tok > w.p_hi || near || (e > 0 && list[e - 1] == entry)) tok = -1;
           }
         }
       } else {
         tok = (int64_t)w.near.tile(tile) * 32 + (i % 2) * 16;
         // no row sees any of the 16: the page may not be the sequence's any more
-        if (tok > w.p_hi || (a.window > 0 && tok + 15 <= (int64_t)w.p_lo - a.window && tok >= a.sinks)) tok = -1;
+        if (tok > w.p_hi || (tok + 15 <= w.w_lo && tok >= a.sinks)) tok = -1;
       }
       int64_t row = -1;
       if (tok >= 0) {
@@ -335,7 +277,7 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
       const int t0 = w.near.tile(base + i) * 32;
       const bool here0 = uni(s_row[2 * i]) >= 0, here1 = uni(s_row[2 * i + 1]) >= 0;
       const bool whole = here0 && here1 && t0 + 31 <= w.p_lo &&
-                         (a.window == 0 || (int64_t)t0 > (int64_t)w.p_hi - a.window || t0 + 31 < a.sinks);
+                         (t0 > w.w_hi || t0 + 31 < a.sinks);
       if (!whole) {
         uint32_t odd = 0;
 #pragma unroll
@@ -343,11 +285,11 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
           const int tok = t0 + 16 * (j / 4) + 4 * g + j % 4;
           const bool here = j < 4 ? here0 : here1;
           const bool some = here && tok <= w.p_hi &&
-                            (a.window == 0 || (int64_t)tok > (int64_t)w.p_lo - a.window || tok < a.sinks);
+                            (tok > w.w_lo || tok < a.sinks);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             const bool seen = here && tok <= p_row[rt] &&
-                              (a.window == 0 || (int64_t)tok > (int64_t)p_row[rt] - a.window || tok < a.sinks);
+                              (tok > w_row[rt] || tok < a.sinks);
             x[rt][j] = seen ? x[rt][j] : -__builtin_inff();
           }
 #pragma unroll
@@ -374,7 +316,7 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
       float top = x[rt][0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) top = fmaxf(top, x[rt][j]);
-      if (__any(top > m[rt] + LAZY)) {
+      if (__any(top > m[rt] + ATTEND_LAZY)) {
         const float up = fmaxf(m[rt], max_column(top));
         const float f = __builtin_amdgcn_exp2f(m[rt] - up);
         m[rt] = up;
@@ -413,7 +355,7 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             const bool seen = tok <= p_row[rt] &&
-                              (a.window == 0 || (int64_t)tok > (int64_t)p_row[rt] - a.window || tok < a.sinks);
+                              (tok > w_row[rt] || tok < a.sinks);
 #pragma unroll
             for (int e = 0; e < VPL; ++e)
 #pragma unroll
@@ -519,13 +461,14 @@ __global__ __launch_bounds__(AT_THREADS) void attend_join_kernel(const AttendArg
     w.b = upper_seq(a.off, a.B, t + a.first_row);
     w.t0 = a.off[w.b];
     n_tok = a.off[w.b + 1] - w.t0;
+    if (!of_class(a, n_tok)) return;
   }
   const int64_t row = (t + a.first_row - w.t0) * a.G + head % a.G;
   set_block<LISTED>(a, n_tok, row / M, M, &w);
   const int parts = (w.tiles + a.run - 1) / a.run;
   if (parts <= 1) return;
   const int64_t step = a.T * a.n_q;
-  float top = LOWEST;
+  float top = ATTEND_LOWEST;
   for (int s = lane; s < parts; s += 64) top = fmaxf(top, a.part_ml[2 * (s * step + id)]);
 #pragma unroll
   for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
@@ -582,9 +525,8 @@ hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_til
   return listed ? launch_dim<true>(a, fp8, d, row_tiles, s) : launch_dim<false>(a, fp8, d, row_tiles, s);
 }
 
-hipError_t launch_attend_join(const AttendArgs& a, int d, int row_tiles, bool listed, hipStream_t s) {
+hipError_t launch_attend_join(const AttendArgs& a, int d, int M, bool listed, hipStream_t s) {
   const dim3 grid((unsigned)((a.T * a.n_q + AT_WAVES - 1) / AT_WAVES));
-  const int M = 16 * row_tiles;
   if (listed) {
     if (d == 64) attend_join_kernel<64, true><<<grid, AT_THREADS, 0, s>>>(a, M);
     else attend_join_kernel<128, true><<<grid, AT_THREADS, 0, s>>>(a, M);

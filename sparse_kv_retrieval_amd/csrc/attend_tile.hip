@@ -1,0 +1,332 @@
+// lsa_attend for many rows (prompts, chunks): the matrix cores bound it, so keys and values go
+// through LDS once per block and serve its 128 rows.
+//
+// Mathematics and precision are those of the split kernel (attend.hip): one pass with a lazily
+// raised maximum, S^T = K Q^T and O^T = V^T P^T, fp32 sums, probabilities rounded once to bf16.
+//
+// Layout. Four waves of 32 rows each; a row is one lane column of 32x32x16 MFMA results, so a
+// lane's 16 scores of a 32-key half tile belong to one row and become the second product's operand
+// where they are (half h holds keys 8a + 4h + 0..3). Tiles of 64 keys are double-buffered in LDS as
+// bf16 rows; 16-byte chunk c of row r lies at c ^ swizzle(r), so that neither the 16-byte reads of K
+// (8 rows, one chunk) nor the transposing 8-byte reads of V (4 rows, two chunks) meet in a bank. A
+// wave fetches 16 rows of K and V (one page each) to registers while the block works on the
+// tile before, and stores them to the other buffer: one barrier per tile.
+//
+// e4m3 codes are widened on the way to LDS, once per block. The power-of-two part of the page's scale
+// goes in there, exactly; what is left of a scale that is no power of two multiplies scores and
+// probabilities instead, on a path that caches written by lsa_kv_append never take.
+#include <type_traits>
+
+#include "kv.hpp"
+
+namespace lsa {
+
+static constexpr int TL_WAVES = 4;
+static constexpr int TL_THREADS = 64 * TL_WAVES;
+static constexpr int TL_M = ATTEND_TILE_ROWS, TL_N = ATTEND_TILE_KEYS;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Swizzle of 16-byte chunks (even, so a chunk pair stays a pair): rows that share a bank phase differ.
+template <int CPR>
+__device__ __forceinline__ int tile_swizzle(int r) {
+  return 2 * ((r * CPR / 16) % (CPR / 2));
+}
+
+// e4m3 to bf16 times a power of two.
+__device__ __forceinline__ u32x2 widen4(uint32_t four, float pow2) {
+  u32x2 r;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, pow2, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, pow2, true));
+  return r;
+}
+
+// A scale as a power of two within bf16's middle range, times what is left.
+__device__ __forceinline__ void split_scale(float s, float* pow2, float* rest) {
+  int e = (int)((__float_as_uint(s) >> 23) & 255) - 127;
+  e = e < -100 ? -100 : e > 100 ? 100 : e;
+  *pow2 = __uint_as_float((uint32_t)(e + 127) << 23);
+  *rest = s * __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+__device__ __forceinline__ uint32_t not_finite_bf16(uint32_t w) {
+  return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+template <bool FP8, int D>
+__global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const AttendArgs a) {
+  constexpr int CPR = D / 8;                  // 16-byte chunks of a row in LDS
+  constexpr int SRC = FP8 ? D / 16 : D / 8;   // and of a cached row
+  constexpr int LOADS = SRC / 4;              // 16-byte loads per lane of 16 rows
+  constexpr int ROWB = 2 * D;                 // bytes of a row in LDS
+  constexpr int KS = D / 16, DT = D / 32;
+  __shared__ __attribute__((aligned(16))) char s_k[2][TL_N * ROWB];
+  __shared__ __attribute__((aligned(16))) char s_v[2][TL_N * ROWB];
+  __shared__ float s_rest[2][2][TL_WAVES];  // what is left of the scales, [buffer][k, v][16 keys]
+  __shared__ __attribute__((aligned(16))) int32_t s_here[2][TL_WAVES];  // whether the 16 keys are there
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), col = lane & 31, h = lane >> 5;
+  const int64_t id = blockIdx.x;
+  const int kv = (int)(id % a.c.n_kv);
+  const int split = (int)((id / a.c.n_kv) % a.splits);
+  // the last row blocks see the most keys: they go first
+  Rows w;
+  if (!find_rows<false>(a, a.blocks - 1 - id / ((int64_t)a.c.n_kv * a.splits), TL_M, &w)) return;
+  const int parts = (w.tiles + a.run - 1) / a.run;
+  if (split > 0 && split >= parts) return;
+  const int first = split * a.run, count = min(a.run, w.tiles - first);
+
+  // scores in units of |scale|: its sign goes into the queries
+  const float c = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
+  const int r = wave * 32 + col;
+  const bool live = r < w.n;
+  const int row = w.r0 + (live ? r : w.n - 1), tok = row / a.G, head = kv * a.G + (row - tok * a.G);
+  const int p_row = w.p0 + tok, w_row = window_start(a, p_row);
+  bf16x8 q[KS];
+  {
+    const uint16_t* src = a.q + (w.t0 + tok) * a.q_stride + (int64_t)head * D + 8 * h;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) q[s] = as_bf16x8((*(const u32x4*)(src + 16 * s) & keep) ^ flip);
+  }
+
+  // The 16 tokens of tile i that this wave fetches: the cached row of the first, or -1.
+  auto place = [&](int i) -> int64_t {
+    if (i >= count) return -1;
+    const int t = w.near.tile(first + i) * TL_N + wave * 16;
+    if (t > w.p_hi || (t + 15 <= w.w_lo && t >= a.sinks)) return -1;
+    const int32_t page = uni(a.c.table[w.b * a.c.table_stride + (t >> a.c.pt_log2)]);
+    if (page < 0 || page >= a.c.n_pages) return -1;
+    return (((int64_t)page * a.c.n_kv + kv) << a.c.pt_log2) + (t & ((1 << a.c.pt_log2) - 1));
+  };
+
+  u32x4 kr[LOADS], vr[LOADS];
+  float ks = 1.f, vs = 1.f;
+  auto fetch = [&](int64_t at) {
+    const int64_t row0 = at < 0 ? 0 : at;  // nothing there: any row, its values are cleared below
+    const char* kb = a.c.k + row0 * (SRC * 16);
+    const char* vb = a.c.v + row0 * (SRC * 16);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      kr[i] = *(const u32x4*)(kb + (uint32_t)((i * 64 + lane) * 16));
+      vr[i] = *(const u32x4*)(vb + (uint32_t)((i * 64 + lane) * 16));
+    }
+    if constexpr (FP8) {
+      ks = a.c.k_scale[row0 >> a.c.pt_log2];
+      vs = a.c.v_scale[row0 >> a.c.pt_log2];
+    }
+  };
+  // Values that no row of the block sees become 0: a probability of 0 would not clear an infinity.
+  auto store = [&](int buf, int i, int64_t at) {
+    const int t0 = w.near.tile(first + i) * TL_N + wave * 16;
+    if (lane == 0) s_here[buf][wave] = at >= 0;
+    float kp = 1.f, vp = 1.f, kx = 1.f, vx = 1.f;
+    if constexpr (FP8) {
+      if (at >= 0) {
+        split_scale(ks, &kp, &kx);
+        split_scale(vs, &vp, &vx);
+      }
+      if (lane == 0) {
+        s_rest[buf][0][wave] = kx;
+        s_rest[buf][1][wave] = vx;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < LOADS; ++e) {
+      const int at_row = (e * 64 + lane) / SRC, ch = (e * 64 + lane) % SRC, rr = wave * 16 + at_row;
+      const int t = t0 + at_row;
+      const bool some = at >= 0 && t <= w.p_hi && (t > w.w_lo || t < a.sinks);
+      if (!some) vr[e] = (u32x4){0, 0, 0, 0};
+      char* kd = s_k[buf] + rr * ROWB;
+      char* vd = s_v[buf] + rr * ROWB;
+      const int sw = tile_swizzle<CPR>(rr);
+      if constexpr (FP8) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const u32x2 k0 = widen4(kr[e][2 * x], kp), k1 = widen4(kr[e][2 * x + 1], kp);
+          const u32x2 v0 = widen4(vr[e][2 * x], vp), v1 = widen4(vr[e][2 * x + 1], vp);
+          *(u32x4*)(kd + ((2 * ch + x) ^ sw) * 16) = (u32x4){k0[0], k0[1], k1[0], k1[1]};
+          *(u32x4*)(vd + ((2 * ch + x) ^ sw) * 16) = (u32x4){v0[0], v0[1], v1[0], v1[1]};
+        }
+      } else {
+        *(u32x4*)(kd + (ch ^ sw) * 16) = kr[e];
+        *(u32x4*)(vd + (ch ^ sw) * 16) = vr[e];
+      }
+    }
+  };
+
+  f32x16 acc[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) acc[i] = (f32x16)(0.f);
+  float m = ATTEND_LOWEST, l = 0.f;
+
+  // LDS addresses of the operands: K row `col`, chunk 2 s + h; V rows 4 h + (lane % 16) / 4, 8 bytes of
+  // the 32 that the lane's group of 16 reads per row
+  const int k_at = col * ROWB + (tile_swizzle<CPR>(col) + h) * 16;
+  const int vrow = 4 * h + (lane & 15) / 4;
+  const int v_at = vrow * ROWB + ((2 * ((lane >> 4) & 1) + (lane & 3) / 2) ^ tile_swizzle<CPR>(vrow)) * 16 + (lane & 1) * 8;
+
+  auto half = [&](int buf, int t0, int u, auto masked, bool here0, bool here1) {
+    constexpr bool MASKED = decltype(masked)::value;
+    f32x16 s = (f32x16)(0.f);
+    const char* kb = s_k[buf] + u * 32 * ROWB;
+#pragma unroll
+    for (int x = 0; x < KS; ++x)
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(*(const u32x4*)(kb + (k_at ^ (32 * x)))), q[x], s, 0, 0, 0);
+    if constexpr (FP8) {
+      const float r0 = s_rest[buf][0][2 * u], r1 = s_rest[buf][0][2 * u + 1];
+      if (uni(__float_as_int(r0)) != 0x3F800000 || uni(__float_as_int(r1)) != 0x3F800000) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] *= i < 8 ? r0 : r1;
+      }
+    }
+    if constexpr (MASKED) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int t = t0 + 32 * u + 8 * (i / 4) + 4 * h + i % 4;
+        const bool seen = (i < 8 ? here0 : here1) && t <= p_row && (t > w_row || t < a.sinks);
+        s[i] = seen ? s[i] : -__builtin_inff();
+      }
+    }
+    float top = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    if (__any(top * c > m + ATTEND_LAZY)) {
+      const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+      const float up = fmaxf(m, fmaxf(__uint_as_float(o[0]), __uint_as_float(o[1])) * c);
+      const float f = __builtin_amdgcn_exp2f(m - up);
+      m = up;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) acc[i] *= f;
+    }
+    float p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -m));
+      l += p[i];
+    }
+    if constexpr (FP8) {
+      const float r0 = s_rest[buf][1][2 * u], r1 = s_rest[buf][1][2 * u + 1];
+      if (uni(__float_as_int(r0)) != 0x3F800000 || uni(__float_as_int(r1)) != 0x3F800000) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] *= i < 8 ? r0 : r1;
+      }
+    }
+    uint32_t odd = 0;
+    const char* vb = s_v[buf] + u * 32 * ROWB;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const bf16x8 pp = as_bf16x8((u32x4){pack_bf16(p[8 * x], p[8 * x + 1]), pack_bf16(p[8 * x + 2], p[8 * x + 3]),
+                                         pack_bf16(p[8 * x + 4], p[8 * x + 5]), pack_bf16(p[8 * x + 6], p[8 * x + 7])});
+#pragma unroll
+      for (int e = 0; e < DT; ++e) {
+        u32x4 v;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+          const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(vb + (16 * x + 8 * y) * ROWB + (v_at ^ (64 * e))));
+          const u32x2 t2 = __builtin_bit_cast(u32x2, t);
+          v[2 * y] = t2[0];
+          v[2 * y + 1] = t2[1];
+        }
+        if constexpr (MASKED) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t bad = not_finite_bf16(v[y]);
+            odd |= bad;
+            v[y] &= ~bad;
+          }
+        }
+        acc[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(v), pp, acc[e], 0, 0, 0);
+      }
+    }
+    if constexpr (MASKED) {
+      // values that are not finite, taken out of the product above, reach the rows that see them
+      if (__any(odd != 0)) {
+#pragma unroll 1
+        for (int j = 0; j < 32; ++j) {
+          const int t = t0 + 32 * u + j, rr = 32 * u + j;
+          const bool seen = (j < 16 ? here0 : here1) && t <= p_row && (t > w_row || t < a.sinks);
+#pragma unroll
+          for (int e = 0; e < DT; ++e) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const int d = 32 * e + 2 * i + 4 * h;
+              const u32x2 y = *(const u32x2*)(s_v[buf] + rr * ROWB + ((d / 8) ^ tile_swizzle<CPR>(rr)) * 16 + (d % 8) * 2);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float z = __uint_as_float(x % 2 ? y[x / 2] & 0xFFFF0000u : y[x / 2] << 16);
+                if (seen && !(fabsf(z) < __builtin_inff())) acc[e][i + x] += z;
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);  // rare: keep its registers few
+          }
+        }
+      }
+    }
+  };
+
+  int64_t at = place(0);
+  if (count > 0) {
+    fetch(at);
+    store(0, 0, at);
+  }
+  int64_t next = place(1);
+  __syncthreads();
+  for (int i = 0; i < count; ++i) {
+    const int buf = i & 1;
+    at = next;
+    if (i + 1 < count) fetch(at);
+    next = place(i + 2);
+    const int t0 = w.near.tile(first + i) * TL_N;
+    const bool whole = t0 + TL_N - 1 <= w.p_lo && (t0 > w.w_hi || t0 + TL_N - 1 < a.sinks);
+    const u32x4 here = *(const u32x4*)s_here[buf];
+    const bool h0 = uni((int)here[0]), h1 = uni((int)here[1]), h2 = uni((int)here[2]), h3 = uni((int)here[3]);
+    if (whole && h0 && h1 && h2 && h3) {
+      half(buf, t0, 0, std::false_type{}, true, true);
+      half(buf, t0, 1, std::false_type{}, true, true);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) half(buf, t0, u, std::true_type{}, u ? h2 : h0, u ? h3 : h1);
+    }
+    if (i + 1 < count) store(buf ^ 1, i + 1, at);
+    __syncthreads();
+  }
+
+  const float sum = sum_halves(l);
+  if (!live) return;
+  if (parts <= 1) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t* dst = a.out + (w.t0 + tok) * a.out_stride + (int64_t)head * D + 4 * h;
+#pragma unroll
+    for (int e = 0; e < DT; ++e)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *(u32x2*)(dst + 32 * e + 2 * i) = (u32x2){pack_bf16(acc[e][i] * inv, acc[e][i + 1] * inv),
+                                                  pack_bf16(acc[e][i + 2] * inv, acc[e][i + 3] * inv)};
+    if (a.lse && h == 0) a.lse[(w.t0 + tok) * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (m + __log2f(sum)) * LN2;
+  } else {
+    const int64_t to = ((int64_t)split * a.T + (w.t0 - a.first_row + tok)) * a.n_q + head;
+#pragma unroll
+    for (int e = 0; e < DT; ++e)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *(f32x4*)(a.part_o + to * D + 4 * h + 32 * e + 2 * i) = (f32x4){acc[e][i], acc[e][i + 1], acc[e][i + 2], acc[e][i + 3]};
+    if (h == 0) *(f32x2*)(a.part_ml + 2 * to) = (f32x2){m, sum};
+  }
+}
+
+hipError_t launch_attend_tile(const AttendArgs& a, bool fp8, int d, hipStream_t s) {
+  const dim3 grid((unsigned)(a.blocks * a.splits * a.c.n_kv));
+  if (d == 64) {
+    if (fp8) attend_tile_kernel<true, 64><<<grid, TL_THREADS, 0, s>>>(a);
+    else attend_tile_kernel<false, 64><<<grid, TL_THREADS, 0, s>>>(a);
+  } else {
+    if (fp8) attend_tile_kernel<true, 128><<<grid, TL_THREADS, 0, s>>>(a);
+    else attend_tile_kernel<false, 128><<<grid, TL_THREADS, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace lsa

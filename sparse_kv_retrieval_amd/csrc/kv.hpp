@@ -41,8 +41,9 @@ inline int64_t append_page_slots(int64_t T, int32_t B, int32_t pt) { return T / 
 
 // Work of one attention launch. Rows of a sequence are its (new token, query head of the group)
 // pairs, row = token * G + head; a row block is M of them for one key head. The keys that a row
-// block sees are numbered in tiles of 32 (first tokens, then the window; listed entries last) and
-// split in runs of `run` tiles; partial results of several runs are joined by a second launch.
+// block sees are numbered in tiles (first tokens, then the window; listed entries last) and split in
+// runs of `run` tiles; partial results of several runs are joined by a second launch. A launch works
+// on the sequences with more than rows_above and at most rows_to rows.
 struct AttendArgs {
   KvView c;
   const uint16_t* q;
@@ -58,25 +59,27 @@ struct AttendArgs {
   int64_t blocks;         // row-block slots
   float scale_log2;       // softmax scale * log2(e)
   int32_t B, n_q, G, max_kv_len, window, sinks, k, r;
-  int32_t splits, run;
+  int32_t splits, run, tile;  // tile: keys per tile
+  int64_t rows_above, rows_to;
 };
 
-// Tiles of 32 tokens that the rows at positions p_lo..p_hi see. Tile i < n_first is tile i of the
+// Tiles of `tile` tokens that the rows at positions p_lo..p_hi see. Tile i < n_first is tile i of the
 // sequence, tile i >= n_first is tile first_b + i - n_first.
 struct TileRange {
   int32_t n_first, first_b, n;
   __device__ __forceinline__ int32_t tile(int32_t i) const { return i < n_first ? i : first_b + (i - n_first); }
 };
 
-__host__ __device__ __forceinline__ TileRange tile_range(int32_t p_lo, int32_t p_hi, int32_t window, int32_t sinks) {
+__host__ __device__ __forceinline__ TileRange tile_range(int32_t p_lo, int32_t p_hi, int32_t window, int32_t sinks,
+                                                         int32_t tile) {
   TileRange t{0, 0, 0};
   if (p_hi < 0) return t;
-  const int32_t end = p_hi / 32 + 1;
+  const int32_t end = p_hi / tile + 1;
   if (window > 0) {
-    const int32_t s = sinks / 32 + (sinks % 32 != 0);
+    const int32_t s = sinks / tile + (sinks % tile != 0);
     t.n_first = s < end ? s : end;
     const int32_t lo = p_lo - window + 1;  // p_lo >= -2^31 + window fits: both are at most 2^31 - 1
-    t.first_b = lo > 0 ? lo / 32 : 0;
+    t.first_b = lo > 0 ? lo / tile : 0;
     if (t.first_b < t.n_first) t.first_b = t.n_first;
   }
   t.n = t.n_first + (end > t.first_b ? end - t.first_b : 0);
@@ -88,7 +91,10 @@ constexpr int ATTEND_MAX_RUN_LISTED = 16;  // the same over listed keys, each wi
 
 hipError_t launch_kv_append(const AppendArgs& a, bool fp8, int d, int style, hipStream_t s);
 hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_tiles, bool listed, hipStream_t s);
-hipError_t launch_attend_join(const AttendArgs& a, int d, int row_tiles, bool listed, hipStream_t s);
+hipError_t launch_attend_join(const AttendArgs& a, int d, int rows, bool listed, hipStream_t s);
+hipError_t launch_attend_tile(const AttendArgs& a, bool fp8, int d, hipStream_t s);
+constexpr int ATTEND_TILE_ROWS = 128;  // rows of a block of attend_tile_kernel
+constexpr int ATTEND_TILE_KEYS = 64;   // keys of its tiles
 
 // Largest b in [0, B) with slot(b) <= x, for slot strictly increasing and slot(0) <= x: the lanes
 // of a wave try 64 places at a time.
@@ -105,6 +111,84 @@ __device__ __forceinline__ int wave_find(int B, int64_t x, F slot) {
     n = min(step, n - c * step);
   }
   return __builtin_amdgcn_readfirstlane(lo);
+}
+
+constexpr float ATTEND_LAZY = 8.0f;
+constexpr float ATTEND_LOWEST = -3.402823466e38f;  // running maximum of a row that has seen nothing
+constexpr float LN2 = 0.6931471805599453f;
+
+// One row block: rows r0 .. r0 + n - 1 of sequence b for key head h.
+struct Rows {
+  int32_t b, n, r0;
+  int32_t p0;          // position of the sequence's first query token (negative: it has fewer cached tokens)
+  int32_t p_lo, p_hi;  // positions of the block's first and last row
+  int32_t w_lo, w_hi;  // positions beyond these are in their windows
+  int64_t t0;          // row number of the sequence's first token in q
+  TileRange near;      // tiles seen by position
+  int32_t tiles;       // those and the listed ones
+};
+
+// The row at position p sees s <= p where s > window_start(a, p) or s < a.sinks.
+__device__ __forceinline__ int32_t window_start(const AttendArgs& a, int32_t p) {
+  return a.window > 0 && p >= a.window ? p - a.window : -1;
+}
+
+// Whether a launch works on sequences of n_tok new tokens.
+__device__ __forceinline__ bool of_class(const AttendArgs& a, int64_t n_tok) {
+  const int64_t rows = n_tok * a.G;
+  return rows > a.rows_above && rows <= a.rows_to;
+}
+
+template <bool LISTED>
+__device__ __forceinline__ void set_block(const AttendArgs& a, int64_t n_tok, int64_t j, int M, Rows* w) {
+  const int64_t rows = n_tok * a.G;
+  w->r0 = (int32_t)(j * M);
+  w->n = (int32_t)min((int64_t)M, rows - j * M);
+  const int32_t len = min(max(a.c.kv_len[w->b], 0), a.max_kv_len);
+  w->p0 = (int32_t)(len - n_tok);
+  w->p_lo = w->p0 + w->r0 / a.G;
+  w->p_hi = w->p0 + (w->r0 + w->n - 1) / a.G;
+  w->w_lo = window_start(a, w->p_lo);
+  w->w_hi = window_start(a, w->p_hi);
+  if constexpr (LISTED) {
+    const int64_t some = (int64_t)min(max(a.count[w->b], 0), a.k) * a.r;
+    if (a.window > 0) {
+      w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks, a.tile);
+    } else {
+      const int32_t end = w->p_hi < 0 ? 0 : w->p_hi / 32 + 1, s = a.sinks / 32 + (a.sinks % 32 != 0);
+      w->near.n_first = w->near.n = min(s, end);
+      w->near.first_b = 0;
+    }
+    w->tiles = w->p_hi < 0 ? 0 : w->near.n + (int32_t)((some + 31) / 32);
+  } else {
+    w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks, a.tile);
+    w->tiles = w->near.n;
+  }
+}
+
+template <bool LISTED>
+__device__ __forceinline__ bool find_rows(const AttendArgs& a, int64_t block, int M, Rows* w) {
+  int64_t n_tok, j;
+  if constexpr (LISTED) {
+    const int per = (a.G + M - 1) / M;
+    w->b = (int)(block / per);
+    w->t0 = w->b;
+    n_tok = 1;
+    j = block % per;
+  } else {
+    auto slot_of = [&](int x) -> int64_t { return (a.off[x] - a.first_row) * a.G / M + x; };
+    w->b = wave_find(a.B, block, slot_of);
+    w->t0 = a.off[w->b];
+    n_tok = a.off[w->b + 1] - w->t0;
+    j = block - slot_of(w->b);
+    if (j * M >= n_tok * a.G || !of_class(a, n_tok)) return false;
+  }
+  set_block<LISTED>(a, n_tok, j, M, w);
+  // the block agrees on all of it: scalar registers
+  w->n = uni(w->n); w->r0 = uni(w->r0); w->p0 = uni(w->p0); w->p_lo = uni(w->p_lo); w->p_hi = uni(w->p_hi);
+  w->w_lo = uni(w->w_lo); w->w_hi = uni(w->w_hi); w->t0 = uni(w->t0); w->tiles = uni(w->tiles);
+  w->near.n_first = uni(w->near.n_first); w->near.first_b = uni(w->near.first_b); w->near.n = uni(w->near.n);
+  return true;
 }
 
 // Maximum and sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48 (one column of a 16x16 tile).

@@ -693,72 +693,84 @@ lsa_status check_rows(int32_t B, const int64_t* off, const int64_t* off_host, in
   return LSA_OK;
 }
 
-// How an attention call is laid over the device; depends only on host arguments.
+// How one attention launch is laid over the device; depends only on host arguments.
 struct AttendPlan {
-  int32_t row_tiles, splits, run;
+  bool used;
+  int32_t rows;    // rows of a row block
+  int32_t splits, run;
   int64_t blocks;  // row-block slots
   size_t bytes;    // workspace
 };
 
-// Row blocks are as tall as the largest sequence needs, up to 64 rows. Keys are split in runs while
-// the row blocks alone do not fill the device (256 CUs, a few blocks each): to about 1024 blocks in
-// all, with runs of 4 tiles (one per wave) to `most` tiles, and not beyond kPartialBytes of partials.
-AttendPlan attend_plan(int64_t T, int32_t n_q, int32_t n_kv, int32_t d, int64_t max_tok, int64_t tiles, int32_t most,
-                       int64_t (*count)(const void*, int32_t, int64_t), const void* ctx) {
-  AttendPlan p{};
-  const int64_t G = n_q / n_kv, rows = max_tok * G;
-  p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  const int32_t M = 16 * p.row_tiles;
-  const int64_t filled = count(ctx, M, G) * n_kv;  // blocks with rows
+// Keys are split in runs while the row blocks with rows (`filled`) do not fill the device: to about
+// `want` blocks in all, with runs of `least` to `most` tiles, and not beyond kPartialBytes of partials.
+void split_keys(AttendPlan* p, int64_t filled, int64_t T, int32_t n_q, int32_t d, int64_t tiles, int64_t least, int64_t most,
+                int64_t want) {
   tiles = std::max<int64_t>(tiles, 1);
   int64_t run = tiles;
-  if (filled < 512) {
-    run = std::min<int64_t>(std::max<int64_t>((tiles * filled + 1023) / 1024, 4), most);
-    run = (run + 3) / 4 * 4;
+  if (filled < want / 2) {
+    run = std::min(std::max((tiles * filled + want - 1) / want, least), most);
+    run = (run + least - 1) / least * least;
     const size_t per = (size_t)std::max<int64_t>(T, 1) * n_q * (d + 2) * 4;
     const int64_t splits = std::max<int64_t>((int64_t)(kPartialBytes / per), 2);
     run = std::max(run, (tiles + splits - 1) / splits);
   }
-  p.run = (int32_t)std::min(run, tiles);
-  p.splits = (int32_t)((tiles + p.run - 1) / p.run);
-  p.bytes = p.splits > 1 ? (size_t)p.splits * T * n_q * (d + 2) * 4 : 0;
-  return p;
+  p->used = filled > 0;
+  p->run = (int32_t)std::min(run, tiles);
+  p->splits = (int32_t)((tiles + p->run - 1) / p->run);
+  p->bytes = p->used && p->splits > 1 ? (size_t)p->splits * T * n_q * (d + 2) * 4 : 0;
 }
 
-int64_t near_tiles(int64_t window, int64_t sinks) { return (sinks + 31) / 32 + (window > 0 ? (window + 30) / 32 + 1 : 0); }
+int64_t near_tiles(int64_t window, int64_t sinks, int64_t tile) {
+  return (sinks + tile - 1) / tile + (window > 0 ? (window + tile - 2) / tile + 1 : 0);
+}
 
-struct RaggedRows {
-  const int64_t* off;
-  int32_t B;
+// Sequences with at most this many rows (new tokens times query heads of a group) go to the split
+// kernel, whose waves share no keys, the others to the tile kernel.
+constexpr int64_t kSplitRows = 64;
+
+struct RaggedPlan {
+  AttendPlan few, many;
+  size_t bytes;
 };
 
-AttendPlan plan_ragged(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, const int64_t* off, int32_t max_kv_len,
+RaggedPlan plan_ragged(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, const int64_t* off, int32_t max_kv_len,
                        int32_t window, int32_t sinks) {
-  int64_t max_tok = 0;
-  for (int32_t b = 0; b < B; ++b) max_tok = std::max(max_tok, off[b + 1] - off[b]);
-  const int64_t T = off[B] - off[0], all = ((int64_t)max_kv_len + 31) / 32;
-  // a row block of several tokens sees that many more tiles; 64 rows are 64 tokens at most
-  const int64_t tiles = window > 0 ? std::min(all, near_tiles((int64_t)window + 63, sinks)) : all;
-  const RaggedRows ctx{off, B};
-  AttendPlan p = attend_plan(T, n_q, n_kv, d, max_tok, tiles, ATTEND_MAX_RUN,
-                             [](const void* c, int32_t M, int64_t G) {
-                               const RaggedRows& r = *static_cast<const RaggedRows*>(c);
-                               int64_t n = 0;
-                               for (int32_t b = 0; b < r.B; ++b) n += ((r.off[b + 1] - r.off[b]) * G + M - 1) / M;
-                               return n;
-                             }, &ctx);
-  p.blocks = T * (n_q / n_kv) / (16 * p.row_tiles) + B;
-  return p;
+  RaggedPlan r{};
+  const int64_t T = off[B] - off[0], G = n_q / n_kv;
+  int64_t most = 0, few = 0, many = 0;
+  for (int32_t b = 0; b < B; ++b) {
+    const int64_t rows = (off[b + 1] - off[b]) * G;
+    if (rows <= kSplitRows) most = std::max(most, rows);
+    else many += (rows + ATTEND_TILE_ROWS - 1) / ATTEND_TILE_ROWS;
+  }
+  r.few.rows = most <= 16 ? 16 : most <= 32 ? 32 : 64;
+  for (int32_t b = 0; b < B; ++b) {
+    const int64_t rows = (off[b + 1] - off[b]) * G;
+    if (rows <= kSplitRows) few += (rows + r.few.rows - 1) / r.few.rows;
+  }
+  r.few.blocks = T * G / r.few.rows + B;
+  r.many.rows = ATTEND_TILE_ROWS;
+  r.many.blocks = T * G / ATTEND_TILE_ROWS + B;
+  // a row block of several tokens sees that many more keys than its window
+  auto tiles = [&](int64_t rows, int64_t tile) {
+    const int64_t all = ((int64_t)max_kv_len + tile - 1) / tile;
+    return window > 0 ? std::min(all, near_tiles((int64_t)window + rows - 1, sinks, tile)) : all;
+  };
+  split_keys(&r.few, few * n_kv, T, n_q, d, tiles(r.few.rows, 32), 4, ATTEND_MAX_RUN, 1024);
+  split_keys(&r.many, many * n_kv, T, n_q, d, tiles(ATTEND_TILE_ROWS, ATTEND_TILE_KEYS), 4, INT32_MAX, 512);
+  r.bytes = std::max(r.few.bytes, r.many.bytes);
+  return r;
 }
 
 AttendPlan plan_listed(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t k, int32_t entry_tokens, int32_t window,
                        int32_t sinks) {
-  const int64_t tiles = near_tiles(window, sinks) + ((int64_t)k * entry_tokens + 31) / 32;
-  AttendPlan p = attend_plan(B, n_q, n_kv, d, 1, tiles, ATTEND_MAX_RUN_LISTED,
-                             [](const void* c, int32_t M, int64_t G) { return *static_cast<const int32_t*>(c) * ((G + M - 1) / M); },
-                             &B);
-  const int64_t M = 16 * p.row_tiles;
-  p.blocks = B * ((n_q / n_kv + M - 1) / M);
+  AttendPlan p{};
+  const int64_t G = n_q / n_kv;
+  p.rows = G <= 16 ? 16 : G <= 32 ? 32 : 64;
+  p.blocks = B * ((G + p.rows - 1) / p.rows);
+  const int64_t tiles = near_tiles(window, sinks, 32) + ((int64_t)k * entry_tokens + 31) / 32;
+  split_keys(&p, p.blocks * n_kv, B, n_q, d, tiles, 4, ATTEND_MAX_RUN_LISTED, 1024);
   return p;
 }
 
@@ -768,33 +780,43 @@ void clip_window(int32_t max_kv_len, int32_t* window, int32_t* sinks) {
   *sinks = *window > 0 ? std::min(*sinks, max_kv_len) : 0;
 }
 
-// The checks and launches that lsa_attend and lsa_attend_topk share. a.c, a.B, the rows and the keys are set.
-lsa_status attend_call(AttendArgs& a, const AttendPlan& p, bool fp8, int32_t d, bool listed, const void* q, int64_t q_stride,
-                       float softmax_scale, void* out, int64_t out_stride, float* lse, void* workspace,
-                       size_t workspace_bytes, hipStream_t stream) {
-  if (a.T == 0) return LSA_OK;  // no rows: q and out may be NULL
+// The checks that lsa_attend and lsa_attend_topk share, and what of the arguments follows from them.
+// a.c, a.T and a.n_q are set.
+lsa_status attend_args(AttendArgs* a, size_t bytes, int32_t d, const void* q, int64_t q_stride, float softmax_scale, void* out,
+                       int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes) {
   if (!q || !out) return fail(LSA_ERR_INVALID_ARG, "q and out must be set");
   if (!aligned16(q) || !aligned16(out)) return fail(LSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if (q == out) return fail(LSA_ERR_INVALID_ARG, "out must not overlap q");
-  const int64_t row = (int64_t)a.n_q * d;
+  const int64_t row = (int64_t)a->n_q * d;
   if (q_stride < row || out_stride < row || !multiple8(q_stride) || !multiple8(out_stride))
     return fail(LSA_ERR_INVALID_ARG, "q_stride and out_stride must be multiples of 8, at least n_q * d_h = %lld", (long long)row);
   if (!std::isfinite(softmax_scale)) return fail(LSA_ERR_INVALID_ARG, "softmax_scale must be finite");
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(LSA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
-  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
-    return fail(LSA_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", p.bytes, workspace_bytes);
-  if (p.bytes > 0 && !aligned16(workspace)) return fail(LSA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-  if (p.blocks * p.splits * a.c.n_kv > kMaxBlocks || a.T * a.n_q > kMaxBlocks * 4)
-    return fail(LSA_ERR_UNSUPPORTED, "too many rows for one call");
-  a.q = (const uint16_t*)q; a.q_stride = q_stride; a.out = (uint16_t*)out; a.out_stride = out_stride; a.lse = lse;
-  a.G = a.n_q / a.c.n_kv;
-  a.blocks = p.blocks; a.splits = p.splits; a.run = p.run;
-  a.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
-  a.part_o = (float*)workspace;
-  a.part_ml = a.part_o + (p.bytes ? (size_t)p.splits * a.T * a.n_q * d : 0);
-  hipError_t e = launch_attend_split(a, fp8, d, p.row_tiles, listed, stream);
-  if (e == hipSuccess && p.splits > 1) e = launch_attend_join(a, d, p.row_tiles, listed, stream);
-  return e == hipSuccess ? LSA_OK : hip_fail(listed ? "lsa_attend_topk launch" : "lsa_attend launch", e);
+  if (bytes > 0 && (!workspace || workspace_bytes < bytes))
+    return fail(LSA_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", bytes, workspace_bytes);
+  if (bytes > 0 && !aligned16(workspace)) return fail(LSA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  a->q = (const uint16_t*)q; a->q_stride = q_stride; a->out = (uint16_t*)out; a->out_stride = out_stride; a->lse = lse;
+  a->G = a->n_q / a->c.n_kv;
+  a->scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+  a->part_o = (float*)workspace;
+  return LSA_OK;
+}
+
+bool plan_fits(const AttendPlan& p, const AttendArgs& a) {
+  return !p.used || (p.blocks * p.splits * a.c.n_kv <= kMaxBlocks && a.T * a.n_q <= kMaxBlocks * 4);
+}
+
+// One attention launch over the sequences with more than `above` and at most `to` rows.
+hipError_t launch_plan(AttendArgs a, const AttendPlan& p, bool fp8, int32_t d, bool tiled, int64_t above, int64_t to,
+                       hipStream_t stream) {
+  if (!p.used) return hipSuccess;
+  const bool listed = a.idx != nullptr;
+  a.blocks = p.blocks; a.splits = p.splits; a.run = p.run; a.tile = tiled ? ATTEND_TILE_KEYS : 32;
+  a.rows_above = above; a.rows_to = to;
+  a.part_ml = a.part_o + (p.splits > 1 ? (size_t)p.splits * a.T * a.n_q * d : 0);
+  hipError_t e = tiled ? launch_attend_tile(a, fp8, d, stream) : launch_attend_split(a, fp8, d, p.rows / 16, listed, stream);
+  if (e == hipSuccess && p.splits > 1) e = launch_attend_join(a, d, p.rows, listed, stream);
+  return e;
 }
 
 bool plan_sizes_ok(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h, int32_t window, int32_t sinks) {
@@ -872,9 +894,16 @@ lsa_status lsa_attend(const lsa_kv_cache* cache, int32_t B, const void* q, int64
   clip_window(max_kv_len, &window, &sinks);
   a.off = q_offsets; a.first_row = q_offsets_host[0]; a.T = q_offsets_host[B] - q_offsets_host[0];
   a.B = B; a.n_q = n_q; a.max_kv_len = max_kv_len; a.window = window; a.sinks = sinks; a.r = 1;
-  const AttendPlan p = plan_ragged(B, n_q, a.c.n_kv, cache->d_h, q_offsets_host, max_kv_len, window, sinks);
-  return attend_call(a, p, fp8, cache->d_h, false, q, q_stride, softmax_scale, out, out_stride, lse, workspace,
-                     workspace_bytes, stream);
+  if (a.T == 0) return LSA_OK;  // no rows: q and out may be NULL
+  const int32_t d = cache->d_h;
+  const RaggedPlan p = plan_ragged(B, n_q, a.c.n_kv, d, q_offsets_host, max_kv_len, window, sinks);
+  if ((s = attend_args(&a, p.bytes, d, q, q_stride, softmax_scale, out, out_stride, lse, workspace, workspace_bytes)) != LSA_OK)
+    return s;
+  if (!plan_fits(p.few, a) || !plan_fits(p.many, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows for one call");
+  // the two launches and their joins use the workspace one after the other
+  hipError_t e = launch_plan(a, p.few, fp8, d, false, 0, kSplitRows, stream);
+  if (e == hipSuccess) e = launch_plan(a, p.many, fp8, d, true, kSplitRows, INT64_MAX, stream);
+  return e == hipSuccess ? LSA_OK : hip_fail("lsa_attend launch", e);
 }
 
 size_t lsa_attend_topk_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h, int32_t k,
@@ -902,8 +931,12 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, 
   a.first_row = 0; a.T = B; a.B = B; a.n_q = n_q;
   const AttendPlan p = plan_listed(B, n_q, a.c.n_kv, cache->d_h, k, entry_tokens, window, sinks);
   a.window = std::min(window, a.max_kv_len); a.sinks = std::min(sinks, a.max_kv_len);
-  return attend_call(a, p, fp8, cache->d_h, true, q, q_stride, softmax_scale, out, out_stride, lse, workspace,
-                     workspace_bytes, stream);
+  if ((s = attend_args(&a, p.bytes, cache->d_h, q, q_stride, softmax_scale, out, out_stride, lse, workspace,
+                       workspace_bytes)) != LSA_OK)
+    return s;
+  if (!plan_fits(p, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows for one call");
+  const hipError_t e = launch_plan(a, p, fp8, cache->d_h, false, -1, INT64_MAX, stream);
+  return e == hipSuccess ? LSA_OK : hip_fail("lsa_attend_topk launch", e);
 }
 
 }  // extern "C"
