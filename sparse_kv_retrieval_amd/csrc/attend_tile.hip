@@ -90,13 +90,19 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     for (int s = 0; s < KS; ++s) q[s] = as_bf16x8((*(const u32x4*)(src + 16 * s) & keep) ^ flip);
   }
 
-  // The 16 tokens of tile i that this wave fetches: the cached row of the first, or -1.
-  auto place = [&](int i) -> int64_t {
+  // The 16 tokens of tile i that this wave fetches: the first one's position, or -1 where no row sees
+  // any of them, and the page that holds them. The page is asked for one tile ahead of its use, so
+  // that reading it never waits for the tile's own loads.
+  auto tokens = [&](int i) -> int {
     if (i >= count) return -1;
     const int t = w.near.tile(first + i) * TL_N + wave * 16;
-    if (t > w.p_hi || (t + 15 <= w.w_lo && t >= a.sinks)) return -1;
-    const int32_t page = uni(a.c.table[w.b * a.c.table_stride + (t >> a.c.pt_log2)]);
-    if (page < 0 || page >= a.c.n_pages) return -1;
+    return t > w.p_hi || (t + 15 <= w.w_lo && t >= a.sinks) ? -1 : t;
+  };
+  const int32_t* table = a.c.table + w.b * a.c.table_stride;
+  auto page_of = [&](int t) -> int32_t { return table[max(t, 0) >> a.c.pt_log2]; };
+  auto place = [&](int t, int32_t page) -> int64_t {
+    page = uni(page);
+    if (t < 0 || page < 0 || page >= a.c.n_pages) return -1;
     return (((int64_t)page * a.c.n_kv + kv) << a.c.pt_log2) + (t & ((1 << a.c.pt_log2) - 1));
   };
 
@@ -267,18 +273,22 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     }
   };
 
-  int64_t at = place(0);
+  int t_next = tokens(0);
+  int32_t page = page_of(t_next);
+  int64_t at = place(t_next, page);
+  t_next = tokens(1);
+  page = page_of(t_next);
   if (count > 0) {
     fetch(at);
     store(0, 0, at);
   }
-  int64_t next = place(1);
   __syncthreads();
   for (int i = 0; i < count; ++i) {
     const int buf = i & 1;
-    at = next;
+    at = place(t_next, page);
+    t_next = tokens(i + 2);
+    page = page_of(t_next);
     if (i + 1 < count) fetch(at);
-    next = place(i + 2);
     const int t0 = w.near.tile(first + i) * TL_N;
     const bool whole = t0 + TL_N - 1 <= w.p_lo && (t0 > w.w_hi || t0 + TL_N - 1 < a.sinks);
     const u32x4 here = *(const u32x4*)s_here[buf];
