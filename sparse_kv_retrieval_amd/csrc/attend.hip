@@ -96,26 +96,6 @@ __device__ __forceinline__ bf16x8 v_operand(const Tile<FP8, D>& t, int i) {
   }
 }
 
-// The elements of a dword that are not finite, as a mask over its bits.
-template <bool FP8>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  if constexpr (FP8) {
-    const uint32_t hit = (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;  // code 7F or FF
-    return hit * 0xFFu;
-  } else {
-    return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-  }
-}
-
-template <bool FP8>
-__device__ __forceinline__ float element(const char* row, int d) {
-  if constexpr (FP8) {
-    return __builtin_amdgcn_cvt_f32_fp8((int)*(const uint8_t*)(row + d), 0);
-  } else {
-    return bf16_bits_to_f32(*(const uint16_t*)(row + 2 * d));
-  }
-}
-
 template <bool FP8, int D, int RT, bool LISTED>
 __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendArgs a) {
   using TileT = Tile<FP8, D>;
@@ -360,7 +340,7 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
             for (int e = 0; e < VPL; ++e)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const float y = element<FP8>(src, VPL * (4 * g + c) + e);
+                const float y = cached_value<FP8>(src, VPL * (4 * g + c) + e);
                 if (seen && !(fabsf(y) < __builtin_inff())) acc[rt][e][c] += y;
               }
           }

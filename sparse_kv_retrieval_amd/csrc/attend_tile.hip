@@ -15,15 +15,17 @@
 // e4m3 codes are widened on the way to LDS, once per block. The power-of-two part of the page's scale
 // goes in there, exactly; what is left of a scale that is no power of two multiplies scores and
 // probabilities instead, on a path that caches written by lsa_kv_append never take.
-#include <type_traits>
-
 #include "kv.hpp"
 
 namespace lsa {
 
-static constexpr int TL_WAVES = 4;
+static constexpr int TL_WAVES = 8;
 static constexpr int TL_THREADS = 64 * TL_WAVES;
 static constexpr int TL_M = ATTEND_TILE_ROWS, TL_N = ATTEND_TILE_KEYS;
+static_assert(TL_M == 32 * TL_WAVES, "a wave has 32 rows");
+static constexpr int TL_BUFS = 3;
+static constexpr int TL_SUBS = TL_N / 16;
+static_assert(TL_WAVES == 2 * TL_SUBS, "one wave fetches 16 rows of K or of V");
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -49,10 +51,6 @@ __device__ __forceinline__ void split_scale(float s, float* pow2, float* rest) {
   *rest = s * __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
-__device__ __forceinline__ uint32_t not_finite_bf16(uint32_t w) {
-  return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-}
-
 template <bool FP8, int D>
 __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const AttendArgs a) {
   constexpr int CPR = D / 8;                  // 16-byte chunks of a row in LDS
@@ -60,12 +58,15 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   constexpr int LOADS = SRC / 4;              // 16-byte loads per lane of 16 rows
   constexpr int ROWB = 2 * D;                 // bytes of a row in LDS
   constexpr int KS = D / 16, DT = D / 32;
-  __shared__ __attribute__((aligned(16))) char s_k[2][TL_N * ROWB];
-  __shared__ __attribute__((aligned(16))) char s_v[2][TL_N * ROWB];
-  __shared__ float s_rest[2][2][TL_WAVES];  // what is left of the scales, [buffer][k, v][16 keys]
-  __shared__ __attribute__((aligned(16))) int32_t s_here[2][TL_WAVES];  // whether the 16 keys are there
+  __shared__ __attribute__((aligned(16))) char s_k[TL_BUFS][TL_N * ROWB];
+  __shared__ __attribute__((aligned(16))) char s_v[TL_BUFS][TL_N * ROWB];
+  __shared__ float s_rest[TL_BUFS][2][TL_SUBS];  // what is left of the scales, [buffer][k, v][16 keys]
+  __shared__ __attribute__((aligned(16))) int32_t s_here[TL_BUFS][TL_SUBS];  // whether the 16 keys are there
+  __shared__ __attribute__((aligned(16))) int32_t s_odd[TL_BUFS][TL_SUBS];   // whether values were taken out
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), col = lane & 31, h = lane >> 5;
+  const int sub = wave % TL_SUBS;        // the wave fetches this 16 tokens' keys, or values
+  const bool is_v = wave >= TL_SUBS;
   const int64_t id = blockIdx.x;
   const int kv = (int)(id % a.c.n_kv);
   const int split = (int)((id / a.c.n_kv) % a.splits);
@@ -80,14 +81,13 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   const float c = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
   const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
   const int r = wave * 32 + col;
-  const bool live = r < w.n;
-  const int row = w.r0 + (live ? r : w.n - 1), tok = row / a.G, head = kv * a.G + (row - tok * a.G);
+  const int row = w.r0 + min(r, w.n - 1), tok = row / a.G, head = kv * a.G + (row - tok * a.G);
   const int p_row = w.p0 + tok, w_row = window_start(a, p_row);
   bf16x8 q[KS];
   {
-    const uint16_t* src = a.q + (w.t0 + tok) * a.q_stride + (int64_t)head * D + 8 * h;
+    const uint16_t* from = a.q + (w.t0 + tok) * a.q_stride + (int64_t)head * D + 8 * h;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) q[s] = as_bf16x8((*(const u32x4*)(src + 16 * s) & keep) ^ flip);
+    for (int s = 0; s < KS; ++s) q[s] = as_bf16x8((*(const u32x4*)(from + 16 * s) & keep) ^ flip);
   }
 
   // The 16 tokens of tile i that this wave fetches: the first one's position, or -1 where no row sees
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   // that reading it never waits for the tile's own loads.
   auto tokens = [&](int i) -> int {
     if (i >= count) return -1;
-    const int t = w.near.tile(first + i) * TL_N + wave * 16;
+    const int t = w.near.tile(first + i) * TL_N + sub * 16;
     return t > w.p_hi || (t + 15 <= w.w_lo && t >= a.sinks) ? -1 : t;
   };
   const int32_t* table = a.c.table + w.b * a.c.table_stride;
@@ -106,58 +106,60 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     return (((int64_t)page * a.c.n_kv + kv) << a.c.pt_log2) + (t & ((1 << a.c.pt_log2) - 1));
   };
 
-  u32x4 kr[LOADS], vr[LOADS];
-  float ks = 1.f, vs = 1.f;
+  u32x4 in[LOADS];
+  float in_scale = 1.f;
+  const char* src = is_v ? a.c.v : a.c.k;
+  const float* src_scale = is_v ? a.c.v_scale : a.c.k_scale;
   auto fetch = [&](int64_t at) {
     const int64_t row0 = at < 0 ? 0 : at;  // nothing there: any row, its values are cleared below
-    const char* kb = a.c.k + row0 * (SRC * 16);
-    const char* vb = a.c.v + row0 * (SRC * 16);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      kr[i] = *(const u32x4*)(kb + (uint32_t)((i * 64 + lane) * 16));
-      vr[i] = *(const u32x4*)(vb + (uint32_t)((i * 64 + lane) * 16));
-    }
-    if constexpr (FP8) {
-      ks = a.c.k_scale[row0 >> a.c.pt_log2];
-      vs = a.c.v_scale[row0 >> a.c.pt_log2];
-    }
+    for (int i = 0; i < LOADS; ++i) in[i] = *(const u32x4*)(src + row0 * (SRC * 16) + (uint32_t)((i * 64 + lane) * 16));
+    if constexpr (FP8) in_scale = src_scale[row0 >> a.c.pt_log2];
   };
-  // Values that no row of the block sees become 0: a probability of 0 would not clear an infinity.
+  auto whole_tile = [&](int t0) { return t0 + TL_N - 1 <= w.p_lo && (t0 > w.w_hi || t0 + TL_N - 1 < a.sinks); };
+  // Values that no row of the block sees become 0: a probability of 0 would not clear an infinity. (Keys
+  // may stay, their scores are masked.) Where some rows see a value and others do not, one that is not
+  // finite becomes 0 as well, and the tile is marked: rescue() brings it to the rows that see it.
   auto store = [&](int buf, int i, int64_t at) {
-    const int t0 = w.near.tile(first + i) * TL_N + wave * 16;
-    if (lane == 0) s_here[buf][wave] = at >= 0;
-    float kp = 1.f, vp = 1.f, kx = 1.f, vx = 1.f;
+    const int t0 = w.near.tile(first + i) * TL_N + sub * 16;
+    const bool whole = whole_tile(t0 - sub * 16);
+    uint32_t odd = 0;
+    if (lane == 0 && !is_v) s_here[buf][sub] = at >= 0;
+    float pow2 = 1.f, rest = 1.f;
     if constexpr (FP8) {
-      if (at >= 0) {
-        split_scale(ks, &kp, &kx);
-        split_scale(vs, &vp, &vx);
-      }
-      if (lane == 0) {
-        s_rest[buf][0][wave] = kx;
-        s_rest[buf][1][wave] = vx;
-      }
+      if (at >= 0) split_scale(in_scale, &pow2, &rest);
+      if (lane == 0) s_rest[buf][is_v][sub] = rest;
     }
+    char* dst = is_v ? s_v[buf] : s_k[buf];
 #pragma unroll
     for (int e = 0; e < LOADS; ++e) {
-      const int at_row = (e * 64 + lane) / SRC, ch = (e * 64 + lane) % SRC, rr = wave * 16 + at_row;
+      const int at_row = (e * 64 + lane) / SRC, ch = (e * 64 + lane) % SRC, rr = sub * 16 + at_row;
       const int t = t0 + at_row;
       const bool some = at >= 0 && t <= w.p_hi && (t > w.w_lo || t < a.sinks);
-      if (!some) vr[e] = (u32x4){0, 0, 0, 0};
-      char* kd = s_k[buf] + rr * ROWB;
-      char* vd = s_v[buf] + rr * ROWB;
+      if (!some) in[e] = (u32x4){0, 0, 0, 0};
+      if (!whole) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const uint32_t bad = not_finite<FP8>(in[e][z]);
+          odd |= bad;
+          if (is_v) in[e][z] &= ~bad;
+        }
+      }
+      char* d = dst + rr * ROWB;
       const int sw = tile_swizzle<CPR>(rr);
       if constexpr (FP8) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const u32x2 k0 = widen4(kr[e][2 * x], kp), k1 = widen4(kr[e][2 * x + 1], kp);
-          const u32x2 v0 = widen4(vr[e][2 * x], vp), v1 = widen4(vr[e][2 * x + 1], vp);
-          *(u32x4*)(kd + ((2 * ch + x) ^ sw) * 16) = (u32x4){k0[0], k0[1], k1[0], k1[1]};
-          *(u32x4*)(vd + ((2 * ch + x) ^ sw) * 16) = (u32x4){v0[0], v0[1], v1[0], v1[1]};
+          const u32x2 lo = widen4(in[e][2 * x], pow2), hi = widen4(in[e][2 * x + 1], pow2);
+          *(u32x4*)(d + ((2 * ch + x) ^ sw) * 16) = (u32x4){lo[0], lo[1], hi[0], hi[1]};
         }
       } else {
-        *(u32x4*)(kd + (ch ^ sw) * 16) = kr[e];
-        *(u32x4*)(vd + (ch ^ sw) * 16) = vr[e];
+        *(u32x4*)(d + (ch ^ sw) * 16) = in[e];
       }
+    }
+    if (is_v) {
+      const bool any = __any(odd != 0);
+      if (lane == 0) s_odd[buf][sub] = any;
     }
   };
 
@@ -171,14 +173,25 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   const int k_at = col * ROWB + (tile_swizzle<CPR>(col) + h) * 16;
   const int vrow = 4 * h + (lane & 15) / 4;
   const int v_at = vrow * ROWB + ((2 * ((lane >> 4) & 1) + (lane & 3) / 2) ^ tile_swizzle<CPR>(vrow)) * 16 + (lane & 1) * 8;
-
-  auto half = [&](int buf, int t0, int u, auto masked, bool here0, bool here1) {
-    constexpr bool MASKED = decltype(masked)::value;
-    f32x16 s = (f32x16)(0.f);
-    const char* kb = s_k[buf] + u * 32 * ROWB;
+  auto k_operand = [&](int buf, int u, int x) { return *(const u32x4*)(s_k[buf] + u * 32 * ROWB + (k_at ^ (32 * x))); };
+  // operand e of key step x: dimensions 32 e + lane % 32, keys 16 x + 8 z + 4 h + 0..3 for z = 0, 1
+  auto v_operand = [&](int buf, int u, int x, int e) {
+    typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+    u32x4 v;
 #pragma unroll
-    for (int x = 0; x < KS; ++x)
-      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(*(const u32x4*)(kb + (k_at ^ (32 * x)))), q[x], s, 0, 0, 0);
+    for (int z = 0; z < 2; ++z) {
+      const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s_v[buf] + (u * 32 + 16 * x + 8 * z) * ROWB + (v_at ^ (64 * e))));
+      const u32x2 t2 = __builtin_bit_cast(u32x2, t);
+      v[2 * z] = t2[0];
+      v[2 * z + 1] = t2[1];
+    }
+    return v;
+  };
+  auto seen = [&](int t) { return t <= p_row && (t > w_row || t < a.sinks); };
+
+  // Scores of 32 keys before their softmax: register i of a lane is key 8 (i / 4) + 4 h + i % 4. Applies what is
+  // left of the page scales and the mask, and raises the maximum.
+  auto settle = [&](int buf, int t0, int u, bool whole, bool here0, bool here1, f32x16& s) {
     if constexpr (FP8) {
       const float r0 = s_rest[buf][0][2 * u], r1 = s_rest[buf][0][2 * u + 1];
       if (uni(__float_as_int(r0)) != 0x3F800000 || uni(__float_as_int(r1)) != 0x3F800000) {
@@ -186,12 +199,12 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
         for (int i = 0; i < 16; ++i) s[i] *= i < 8 ? r0 : r1;
       }
     }
-    if constexpr (MASKED) {
+    if (!whole) {
+      const int base = t0 + 32 * u + 4 * h, hi = p_row - base, lo = w_row - base, few = a.sinks - base;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int t = t0 + 32 * u + 8 * (i / 4) + 4 * h + i % 4;
-        const bool seen = (i < 8 ? here0 : here1) && t <= p_row && (t > w_row || t < a.sinks);
-        s[i] = seen ? s[i] : -__builtin_inff();
+        const int x = 8 * (i / 4) + i % 4;  // key base + x
+        s[i] = (i < 8 ? here0 : here1) && x <= hi && (x > lo || x < few) ? s[i] : -__builtin_inff();
       }
     }
     float top = s[0];
@@ -199,76 +212,84 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
     if (__any(top * c > m + ATTEND_LAZY)) {
       const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-      const float up = fmaxf(m, fmaxf(__uint_as_float(o[0]), __uint_as_float(o[1])) * c);
-      const float f = __builtin_amdgcn_exp2f(m - up);
-      m = up;
+      const float high = fmaxf(m, fmaxf(__uint_as_float(o[0]), __uint_as_float(o[1])) * c);
+      const float f = __builtin_amdgcn_exp2f(m - high);
+      m = high;
       l *= f;
 #pragma unroll
       for (int i = 0; i < DT; ++i) acc[i] *= f;
     }
-    float p[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -m));
-      l += p[i];
-    }
+  };
+
+  // One step over 32 keys: the next step's scores beside this one's probabilities, then the second
+  // product. The order is fixed group by group: one matrix instruction, the LDS reads of the one after
+  // the next, and a share of the exponentials, so that neither waits long for the other and no more
+  // than three operands are held.
+  auto step = [&](int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next) {
+    float r0 = 1.f, r1 = 1.f;
+    bool rest = false;
     if constexpr (FP8) {
-      const float r0 = s_rest[buf][1][2 * u], r1 = s_rest[buf][1][2 * u + 1];
-      if (uni(__float_as_int(r0)) != 0x3F800000 || uni(__float_as_int(r1)) != 0x3F800000) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] *= i < 8 ? r0 : r1;
-      }
+      r0 = s_rest[buf][1][2 * u];
+      r1 = s_rest[buf][1][2 * u + 1];
+      rest = uni(__float_as_int(r0)) != 0x3F800000 || uni(__float_as_int(r1)) != 0x3F800000;
     }
-    uint32_t odd = 0;
-    const char* vb = s_v[buf] + u * 32 * ROWB;
+    float e[8];
+    auto probability = [&](int i) {
+      e[i % 8] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -m));
+      l += e[i % 8];
+    };
+    auto packed = [&](float left) {
+      if constexpr (FP8) {
+        if (rest) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const bf16x8 pp = as_bf16x8((u32x4){pack_bf16(p[8 * x], p[8 * x + 1]), pack_bf16(p[8 * x + 2], p[8 * x + 3]),
-                                         pack_bf16(p[8 * x + 4], p[8 * x + 5]), pack_bf16(p[8 * x + 6], p[8 * x + 7])});
+          for (int i = 0; i < 8; ++i) e[i] *= left;
+        }
+      }
+      return as_bf16x8((u32x4){pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])});
+    };
+    u32x4 f[3];
+    f[0] = k_operand(next_buf, next_u, 0);
+    f[1] = k_operand(next_buf, next_u, 1);
+    s_next = (f32x16)(0.f);
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      f[(x + 2) % 3] = x + 2 < KS ? k_operand(next_buf, next_u, x + 2) : v_operand(buf, u, 0, x + 2 - KS);
+      s_next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f[x % 3]), q[x], s_next, 0, 0, 0);
+#pragma unroll
+      for (int i = 8 / KS * x; i < 8 / KS * (x + 1); ++i) probability(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    bf16x8 p = packed(r0);
+#pragma unroll
+    for (int x = 0; x < 2 * DT; ++x) {
+      if (x + 2 < 2 * DT) f[(KS + x + 2) % 3] = v_operand(buf, u, (x + 2) / DT, (x + 2) % DT);
+      acc[x % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f[(KS + x) % 3]), p, acc[x % DT], 0, 0, 0);
+      if (x < DT) {
+#pragma unroll
+        for (int i = 8 + 8 / DT * x; i < 8 + 8 / DT * (x + 1); ++i) probability(i);
+        if (x == DT - 1) p = packed(r1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Values that are not finite, taken out of a tile on its way to LDS, reach the rows that see them.
+  auto rescue = [&](int t0) {
+#pragma unroll 1
+    for (int j = 0; j < TL_N; ++j) {
+      const int t = t0 + j;
+      if (t > w.p_hi || !(t > w.w_lo || t < a.sinks)) continue;
+      const int64_t row = place(t, page_of(t));
+      if (row < 0) continue;
+      const char* from = a.c.v + row * (SRC * 16);
+      const bool sees = seen(t);
 #pragma unroll
       for (int e = 0; e < DT; ++e) {
-        u32x4 v;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
-          const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(vb + (16 * x + 8 * y) * ROWB + (v_at ^ (64 * e))));
-          const u32x2 t2 = __builtin_bit_cast(u32x2, t);
-          v[2 * y] = t2[0];
-          v[2 * y + 1] = t2[1];
+        for (int i = 0; i < 16; ++i) {
+          const float z = cached_value<FP8>(from, 32 * e + 8 * (i / 4) + 4 * h + i % 4);
+          if (sees && !(fabsf(z) < __builtin_inff())) acc[e][i] += z;
         }
-        if constexpr (MASKED) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t bad = not_finite_bf16(v[y]);
-            odd |= bad;
-            v[y] &= ~bad;
-          }
-        }
-        acc[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(v), pp, acc[e], 0, 0, 0);
-      }
-    }
-    if constexpr (MASKED) {
-      // values that are not finite, taken out of the product above, reach the rows that see them
-      if (__any(odd != 0)) {
-#pragma unroll 1
-        for (int j = 0; j < 32; ++j) {
-          const int t = t0 + 32 * u + j, rr = 32 * u + j;
-          const bool seen = (j < 16 ? here0 : here1) && t <= p_row && (t > w_row || t < a.sinks);
-#pragma unroll
-          for (int e = 0; e < DT; ++e) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const int d = 32 * e + 2 * i + 4 * h;
-              const u32x2 y = *(const u32x2*)(s_v[buf] + rr * ROWB + ((d / 8) ^ tile_swizzle<CPR>(rr)) * 16 + (d % 8) * 2);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float z = __uint_as_float(x % 2 ? y[x / 2] & 0xFFFF0000u : y[x / 2] << 16);
-                if (seen && !(fabsf(z) < __builtin_inff())) acc[e][i + x] += z;
-              }
-            }
-            __builtin_amdgcn_sched_barrier(0);  // rare: keep its registers few
-          }
-        }
+        __builtin_amdgcn_sched_barrier(0);  // rare: keep its registers few
       }
     }
   };
@@ -278,34 +299,48 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   int64_t at = place(t_next, page);
   t_next = tokens(1);
   page = page_of(t_next);
+  f32x16 s0 = (f32x16)(0.f), s1;
   if (count > 0) {
     fetch(at);
     store(0, 0, at);
-  }
-  __syncthreads();
-  for (int i = 0; i < count; ++i) {
-    const int buf = i & 1;
     at = place(t_next, page);
-    t_next = tokens(i + 2);
+    t_next = tokens(2);
     page = page_of(t_next);
-    if (i + 1 < count) fetch(at);
+    fetch(at);  // beyond the run: row 0, not used
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < KS; ++x) s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(k_operand(0, 0, x)), q[x], s0, 0, 0, 0);
+  }
+  int buf = 0;
+  for (int i = 0; i < count; ++i) {
+    const int nb = buf + 1 == TL_BUFS ? 0 : buf + 1;
     const int t0 = w.near.tile(first + i) * TL_N;
-    const bool whole = t0 + TL_N - 1 <= w.p_lo && (t0 > w.w_hi || t0 + TL_N - 1 < a.sinks);
     const u32x4 here = *(const u32x4*)s_here[buf];
     const bool h0 = uni((int)here[0]), h1 = uni((int)here[1]), h2 = uni((int)here[2]), h3 = uni((int)here[3]);
-    if (whole && h0 && h1 && h2 && h3) {
-      half(buf, t0, 0, std::false_type{}, true, true);
-      half(buf, t0, 1, std::false_type{}, true, true);
-    } else {
-#pragma unroll 1
-      for (int u = 0; u < 2; ++u) half(buf, t0, u, std::true_type{}, u ? h2 : h0, u ? h3 : h1);
+    const bool whole = h0 && h1 && h2 && h3 && whole_tile(t0);
+    settle(buf, t0, 0, whole, h0, h1, s0);
+    step(buf, 0, s0, buf, 1, s1);
+    // The next tile: its buffer was last read two barriers ago.
+    if (i + 1 < count) {
+      store(nb, i + 1, at);
+      at = place(t_next, page);
+      t_next = tokens(i + 3);
+      page = page_of(t_next);
+      fetch(at);
     }
-    if (i + 1 < count) store(buf ^ 1, i + 1, at);
     __syncthreads();
+    settle(buf, t0, 1, whole, h2, h3, s1);
+    // after the last tile the next scores are those of an old buffer, and not used
+    step(buf, 1, s1, nb, 0, s0);
+    if (!whole) {
+      const u32x4 odd = *(const u32x4*)s_odd[buf];
+      if (uni((int)(odd[0] | odd[1] | odd[2] | odd[3]))) rescue(t0);
+    }
+    buf = nb;
   }
 
   const float sum = sum_halves(l);
-  if (!live) return;
+  if (r >= w.n) return;
   if (parts <= 1) {
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint16_t* dst = a.out + (w.t0 + tok) * a.out_stride + (int64_t)head * D + 4 * h;

@@ -93,7 +93,7 @@ hipError_t launch_kv_append(const AppendArgs& a, bool fp8, int d, int style, hip
 hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_tiles, bool listed, hipStream_t s);
 hipError_t launch_attend_join(const AttendArgs& a, int d, int rows, bool listed, hipStream_t s);
 hipError_t launch_attend_tile(const AttendArgs& a, bool fp8, int d, hipStream_t s);
-constexpr int ATTEND_TILE_ROWS = 128;  // rows of a block of attend_tile_kernel
+constexpr int ATTEND_TILE_ROWS = 256;  // rows of a block of attend_tile_kernel
 constexpr int ATTEND_TILE_KEYS = 64;   // keys of its tiles
 
 // Largest b in [0, B) with slot(b) <= x, for slot strictly increasing and slot(0) <= x: the lanes
@@ -189,6 +189,27 @@ __device__ __forceinline__ bool find_rows(const AttendArgs& a, int64_t block, in
   w->w_lo = uni(w->w_lo); w->w_hi = uni(w->w_hi); w->t0 = uni(w->t0); w->tiles = uni(w->tiles);
   w->near.n_first = uni(w->near.n_first); w->near.first_b = uni(w->near.first_b); w->near.n = uni(w->near.n);
   return true;
+}
+
+// The elements of a dword that are not finite, as a mask over its bits.
+template <bool FP8>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  if constexpr (FP8) {
+    const uint32_t hit = (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;  // code 7F or FF
+    return hit * 0xFFu;
+  } else {
+    return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+  }
+}
+
+// Dimension d of a cached row, in units of its scale.
+template <bool FP8>
+__device__ __forceinline__ float cached_value(const char* row, int d) {
+  if constexpr (FP8) {
+    return __builtin_amdgcn_cvt_f32_fp8((int)*(const uint8_t*)(row + d), 0);
+  } else {
+    return bf16_bits_to_f32(*(const uint16_t*)(row + 2 * d));
+  }
 }
 
 // Maximum and sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48 (one column of a 16x16 tile).
