@@ -29,10 +29,15 @@ static_assert(TL_WAVES == 2 * TL_SUBS, "one wave fetches 16 rows of K or of V");
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// Swizzle of 16-byte chunks (even, so a chunk pair stays a pair): rows that share a bank phase differ.
+// Swizzles of 16-byte chunks. A read of K takes one chunk of consecutive rows: 16 of them (or 8 rows of two
+// lines) meet all banks once. A transposing read of V takes four chunks of four rows.
 template <int CPR>
-__device__ __forceinline__ int tile_swizzle(int r) {
-  return 2 * ((r * CPR / 16) % (CPR / 2));
+__device__ __forceinline__ int k_swizzle(int r) {
+  return (r * CPR / 16) % CPR;
+}
+template <int CPR>
+__device__ __forceinline__ int v_swizzle(int r) {
+  return 4 * ((r * CPR / 16) % (CPR / 4));
 }
 
 // e4m3 to bf16 times a power of two.
@@ -58,8 +63,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   constexpr int LOADS = SRC / 4;              // 16-byte loads per lane of 16 rows
   constexpr int ROWB = 2 * D;                 // bytes of a row in LDS
   constexpr int KS = D / 16, DT = D / 32;
-  __shared__ __attribute__((aligned(16))) char s_k[TL_BUFS][TL_N * ROWB];
-  __shared__ __attribute__((aligned(16))) char s_v[TL_BUFS][TL_N * ROWB];
+  __shared__ __attribute__((aligned(16))) char s_k[TL_BUFS][TL_N * ROWB], s_v[TL_BUFS][TL_N * ROWB];
   __shared__ float s_rest[TL_BUFS][2][TL_SUBS];  // what is left of the scales, [buffer][k, v][16 keys]
   __shared__ __attribute__((aligned(16))) int32_t s_here[TL_BUFS][TL_SUBS];  // whether the 16 keys are there
   __shared__ __attribute__((aligned(16))) int32_t s_odd[TL_BUFS][TL_SUBS];   // whether values were taken out
@@ -122,9 +126,26 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   // finite becomes 0 as well, and the tile is marked: rescue() brings it to the rows that see it.
   auto store = [&](int buf, int i, int64_t at) {
     const int t0 = w.near.tile(first + i) * TL_N + sub * 16;
-    const bool whole = whole_tile(t0 - sub * 16);
-    uint32_t odd = 0;
-    if (lane == 0 && !is_v) s_here[buf][sub] = at >= 0;
+    if (is_v) {
+      uint32_t odd = 0;
+      if (at < 0 || !whole_tile(t0 - sub * 16)) {
+#pragma unroll
+        for (int e = 0; e < LOADS; ++e) {
+          const int t = t0 + (e * 64 + lane) / SRC;
+          const bool some = at >= 0 && t <= w.p_hi && (t > w.w_lo || t < a.sinks);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const uint32_t x = some ? in[e][z] : 0u, bad = not_finite<FP8>(x);
+            odd |= bad;
+            in[e][z] = x & ~bad;
+          }
+        }
+      }
+      const bool any = __any(odd != 0);
+      if (lane == 0) s_odd[buf][sub] = any;
+    } else if (lane == 0) {
+      s_here[buf][sub] = at >= 0;
+    }
     float pow2 = 1.f, rest = 1.f;
     if constexpr (FP8) {
       if (at >= 0) split_scale(in_scale, &pow2, &rest);
@@ -134,19 +155,8 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
 #pragma unroll
     for (int e = 0; e < LOADS; ++e) {
       const int at_row = (e * 64 + lane) / SRC, ch = (e * 64 + lane) % SRC, rr = sub * 16 + at_row;
-      const int t = t0 + at_row;
-      const bool some = at >= 0 && t <= w.p_hi && (t > w.w_lo || t < a.sinks);
-      if (!some) in[e] = (u32x4){0, 0, 0, 0};
-      if (!whole) {
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const uint32_t bad = not_finite<FP8>(in[e][z]);
-          odd |= bad;
-          if (is_v) in[e][z] &= ~bad;
-        }
-      }
       char* d = dst + rr * ROWB;
-      const int sw = tile_swizzle<CPR>(rr);
+      const int sw = is_v ? v_swizzle<CPR>(rr) : k_swizzle<CPR>(rr);
       if constexpr (FP8) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -157,10 +167,6 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
         *(u32x4*)(d + (ch ^ sw) * 16) = in[e];
       }
     }
-    if (is_v) {
-      const bool any = __any(odd != 0);
-      if (lane == 0) s_odd[buf][sub] = any;
-    }
   };
 
   f32x16 acc[DT];
@@ -170,9 +176,9 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
 
   // LDS addresses of the operands: K row `col`, chunk 2 s + h; V rows 4 h + (lane % 16) / 4, 8 bytes of
   // the 32 that the lane's group of 16 reads per row
-  const int k_at = col * ROWB + (tile_swizzle<CPR>(col) + h) * 16;
+  const int k_at = col * ROWB + (k_swizzle<CPR>(col) ^ h) * 16;
   const int vrow = 4 * h + (lane & 15) / 4;
-  const int v_at = vrow * ROWB + ((2 * ((lane >> 4) & 1) + (lane & 3) / 2) ^ tile_swizzle<CPR>(vrow)) * 16 + (lane & 1) * 8;
+  const int v_at = vrow * ROWB + ((2 * ((lane >> 4) & 1) + (lane & 3) / 2) ^ v_swizzle<CPR>(vrow)) * 16 + (lane & 1) * 8;
   auto k_operand = [&](int buf, int u, int x) { return *(const u32x4*)(s_k[buf] + u * 32 * ROWB + (k_at ^ (32 * x))); };
   // operand e of key step x: dimensions 32 e + lane % 32, keys 16 x + 8 z + 4 h + 0..3 for z = 0, 1
   auto v_operand = [&](int buf, int u, int x, int e) {
