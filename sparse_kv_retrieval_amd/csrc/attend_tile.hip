@@ -48,7 +48,7 @@ __device__ __forceinline__ u32x2 widen4(uint32_t four, float pow2) {
   return r;
 }
 
-// A scale as a power of two within bf16's middle range, times what is left.
+// A scale as a power of two within bf16's middle range, times what is left (1, or beyond that range).
 __device__ __forceinline__ void split_scale(float s, float* pow2, float* rest) {
   int e = (int)((__float_as_uint(s) >> 23) & 255) - 127;
   e = e < -100 ? -100 : e > 100 ? 100 : e;
@@ -64,7 +64,8 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   constexpr int ROWB = 2 * D;                 // bytes of a row in LDS
   constexpr int KS = D / 16, DT = D / 32;
   __shared__ __attribute__((aligned(16))) char s_k[TL_BUFS][TL_N * ROWB], s_v[TL_BUFS][TL_N * ROWB];
-  __shared__ float s_rest[TL_BUFS][2][TL_SUBS];  // what is left of the scales, [buffer][k, v][16 keys]
+  // what is left of the scales of 16 keys: of K times c, of V as log2 and reciprocal
+  __shared__ __attribute__((aligned(16))) float s_kc[TL_BUFS][TL_SUBS], s_vlog[TL_BUFS][TL_SUBS], s_vinv[TL_BUFS][TL_SUBS];
   __shared__ __attribute__((aligned(16))) int32_t s_here[TL_BUFS][TL_SUBS];  // whether the 16 keys are there
   __shared__ __attribute__((aligned(16))) int32_t s_odd[TL_BUFS][TL_SUBS];   // whether values were taken out
 
@@ -149,7 +150,14 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     float pow2 = 1.f, rest = 1.f;
     if constexpr (FP8) {
       if (at >= 0) split_scale(in_scale, &pow2, &rest);
-      if (lane == 0) s_rest[buf][is_v][sub] = rest;
+      if (lane == 0) {
+        if (is_v) {
+          s_vlog[buf][sub] = __log2f(rest);
+          s_vinv[buf][sub] = 1.f / rest;
+        } else {
+          s_kc[buf][sub] = rest * c;
+        }
+      }
     }
     char* dst = is_v ? s_v[buf] : s_k[buf];
 #pragma unroll
@@ -195,16 +203,9 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   };
   auto seen = [&](int t) { return t <= p_row && (t > w_row || t < a.sinks); };
 
-  // Scores of 32 keys before their softmax: register i of a lane is key 8 (i / 4) + 4 h + i % 4. Applies what is
-  // left of the page scales and the mask, and raises the maximum.
-  auto settle = [&](int buf, int t0, int u, bool whole, bool here0, bool here1, f32x16& s) {
-    if constexpr (FP8) {
-      const float r0 = s_rest[buf][0][2 * u], r1 = s_rest[buf][0][2 * u + 1];
-      if (uni(__float_as_int(r0)) != 0x3F800000 || uni(__float_as_int(r1)) != 0x3F800000) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] *= i < 8 ? r0 : r1;
-      }
-    }
+  // Scores of 32 keys before their softmax: register i of a lane is key 8 (i / 4) + 4 h + i % 4. Applies the mask and
+  // raises the maximum; returns whether it rose for some row of the wave, and then what to scale by in `fall`.
+  auto settle = [&](int buf, int t0, int u, bool whole, bool here0, bool here1, f32x16& s, float& fall) -> bool {
     if (!whole) {
       const int base = t0 + 32 * u + 4 * h, hi = p_row - base, lo = w_row - base, few = a.sinks - base;
 #pragma unroll
@@ -213,70 +214,78 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
         s[i] = (i < 8 ? here0 : here1) && x <= hi && (x > lo || x < few) ? s[i] : -__builtin_inff();
       }
     }
-    float top = s[0];
+    float top = s[0], top1 = s[8];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-    if (__any(top * c > m + ATTEND_LAZY)) {
-      const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-      const float high = fmaxf(m, fmaxf(__uint_as_float(o[0]), __uint_as_float(o[1])) * c);
-      const float f = __builtin_amdgcn_exp2f(m - high);
-      m = high;
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) acc[i] *= f;
+    for (int i = 1; i < 8; ++i) {
+      top = fmaxf(top, s[i]);
+      top1 = fmaxf(top1, s[8 + i]);
     }
+    top = FP8 ? fmaxf(top * s_kc[buf][2 * u], top1 * s_kc[buf][2 * u + 1]) : fmaxf(top, top1) * c;
+    if (!__any(top > m + ATTEND_LAZY)) return false;
+    const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+    const float high = fmaxf(m, fmaxf(__uint_as_float(o[0]), __uint_as_float(o[1])));
+    fall = __builtin_amdgcn_exp2f(m - high);
+    m = high;
+    l *= fall;
+    return true;
   };
 
-  // One step over 32 keys: the next step's scores beside this one's probabilities, then the second
-  // product. The order is fixed group by group: one matrix instruction, the LDS reads of the one after
-  // the next, and a share of the exponentials, so that neither waits long for the other and no more
-  // than three operands are held.
-  auto step = [&](int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next) {
-    float r0 = 1.f, r1 = 1.f;
-    bool rest = false;
+  // One step over 32 keys (buf, u) does three things side by side: the scores of the next 32 keys, this
+  // one's probabilities, and the second product of the ones before. The order is fixed group by group: one matrix
+  // instruction of each product (they do not wait for each other), the LDS reads of the group after the
+  // next, and a share of the exponentials. What is left of V's scale rides in the exponent, and leaves
+  // the sum again by its reciprocal.
+  bf16x8 p[2] = {as_bf16x8((u32x4){0, 0, 0, 0}), as_bf16x8((u32x4){0, 0, 0, 0})};
+  auto step = [&](int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next, int old_buf, int old_u) {
+    constexpr int E = 16 / KS;  // exponentials of a group
+    static_assert(KS == 2 * DT, "as many key steps as value operands");
+    float c2[2] = {c, c}, add[2] = {-m, -m}, inv[2] = {1.f, 1.f};
     if constexpr (FP8) {
-      r0 = s_rest[buf][1][2 * u];
-      r1 = s_rest[buf][1][2 * u + 1];
-      rest = uni(__float_as_int(r0)) != 0x3F800000 || uni(__float_as_int(r1)) != 0x3F800000;
-    }
-    float e[8];
-    auto probability = [&](int i) {
-      e[i % 8] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -m));
-      l += e[i % 8];
-    };
-    auto packed = [&](float left) {
-      if constexpr (FP8) {
-        if (rest) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] *= left;
-        }
+      for (int x = 0; x < 2; ++x) {
+        c2[x] = s_kc[buf][2 * u + x];
+        add[x] = s_vlog[buf][2 * u + x] - m;
+        inv[x] = s_vinv[buf][2 * u + x];
       }
-      return as_bf16x8((u32x4){pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])});
-    };
-    u32x4 f[3];
-    f[0] = k_operand(next_buf, next_u, 0);
-    f[1] = k_operand(next_buf, next_u, 1);
+    }
+    uint32_t packed[8];
+    u32x4 kf[3], vf[3];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      kf[x] = k_operand(next_buf, next_u, x);
+      vf[x] = v_operand(old_buf, old_u, x / DT, x % DT);
+    }
     s_next = (f32x16)(0.f);
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
-      f[(x + 2) % 3] = x + 2 < KS ? k_operand(next_buf, next_u, x + 2) : v_operand(buf, u, 0, x + 2 - KS);
-      s_next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f[x % 3]), q[x], s_next, 0, 0, 0);
+      if (x + 2 < KS) {
+        kf[(x + 2) % 3] = k_operand(next_buf, next_u, x + 2);
+        vf[(x + 2) % 3] = v_operand(old_buf, old_u, (x + 2) / DT, (x + 2) % DT);
+      }
+      s_next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf[x % 3]), q[x], s_next, 0, 0, 0);
+      acc[x % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vf[x % 3]), p[x / DT], acc[x % DT], 0, 0, 0);
 #pragma unroll
-      for (int i = 8 / KS * x; i < 8 / KS * (x + 1); ++i) probability(i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    bf16x8 p = packed(r0);
-#pragma unroll
-    for (int x = 0; x < 2 * DT; ++x) {
-      if (x + 2 < 2 * DT) f[(KS + x + 2) % 3] = v_operand(buf, u, (x + 2) / DT, (x + 2) % DT);
-      acc[x % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f[(KS + x) % 3]), p, acc[x % DT], 0, 0, 0);
-      if (x < DT) {
-#pragma unroll
-        for (int i = 8 + 8 / DT * x; i < 8 + 8 / DT * (x + 1); ++i) probability(i);
-        if (x == DT - 1) p = packed(r1);
+      for (int i = E * x; i < E * (x + 1); i += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c2[i / 8], add[i / 8]));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 1], c2[i / 8], add[i / 8]));
+        if constexpr (FP8) {
+          l = __builtin_fmaf(e0, inv[i / 8], l);
+          l = __builtin_fmaf(e1, inv[i / 8], l);
+        } else {
+          l += e0;
+          l += e1;
+        }
+        packed[i / 2] = pack_bf16(e0, e1);
+        asm volatile("" : "+v"(packed[i / 2]), "+v"(l));  // here, and not sunk to where they are used
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) p[x] = as_bf16x8((u32x4){packed[4 * x], packed[4 * x + 1], packed[4 * x + 2], packed[4 * x + 3]});
+  };
+  auto scale_out = [&](float f) {
+#pragma unroll
+    for (int i = 0; i < DT; ++i) acc[i] *= f;
   };
   // Values that are not finite, taken out of a tile on its way to LDS, reach the rows that see them.
   auto rescue = [&](int t0) {
@@ -306,6 +315,8 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   t_next = tokens(1);
   page = page_of(t_next);
   f32x16 s0 = (f32x16)(0.f), s1;
+  float fall = 1.f;
+  int buf = 0, old = TL_BUFS - 1;
   if (count > 0) {
     fetch(at);
     store(0, 0, at);
@@ -313,19 +324,22 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     t_next = tokens(2);
     page = page_of(t_next);
     fetch(at);  // beyond the run: row 0, not used
+    // the first step's second product is of no probabilities and these values
+    for (int i = tid; i < TL_N * ROWB / 16; i += TL_THREADS) *(u32x4*)(s_v[old] + 16 * i) = (u32x4){0, 0, 0, 0};
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < KS; ++x) s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(k_operand(0, 0, x)), q[x], s0, 0, 0, 0);
   }
-  int buf = 0;
   for (int i = 0; i < count; ++i) {
     const int nb = buf + 1 == TL_BUFS ? 0 : buf + 1;
     const int t0 = w.near.tile(first + i) * TL_N;
     const u32x4 here = *(const u32x4*)s_here[buf];
     const bool h0 = uni((int)here[0]), h1 = uni((int)here[1]), h2 = uni((int)here[2]), h3 = uni((int)here[3]);
     const bool whole = h0 && h1 && h2 && h3 && whole_tile(t0);
-    settle(buf, t0, 0, whole, h0, h1, s0);
-    step(buf, 0, s0, buf, 1, s1);
+    // The probabilities before this step's belong to the maximum before it: the output is scaled after them.
+    bool rose = settle(buf, t0, 0, whole, h0, h1, s0, fall);
+    step(buf, 0, s0, buf, 1, s1, old, 1);
+    if (rose) scale_out(fall);
     // The next tile: its buffer was last read two barriers ago.
     if (i + 1 < count) {
       store(nb, i + 1, at);
@@ -335,14 +349,21 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       fetch(at);
     }
     __syncthreads();
-    settle(buf, t0, 1, whole, h2, h3, s1);
+    rose = settle(buf, t0, 1, whole, h2, h3, s1, fall);
     // after the last tile the next scores are those of an old buffer, and not used
-    step(buf, 1, s1, nb, 0, s0);
+    step(buf, 1, s1, nb, 0, s0, buf, 0);
+    if (rose) scale_out(fall);
     if (!whole) {
       const u32x4 odd = *(const u32x4*)s_odd[buf];
       if (uni((int)(odd[0] | odd[1] | odd[2] | odd[3]))) rescue(t0);
     }
+    old = buf;
     buf = nb;
+  }
+  if (count > 0) {
+#pragma unroll
+    for (int x = 0; x < KS; ++x)
+      acc[x % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(v_operand(old, 1, x / DT, x % DT)), p[x / DT], acc[x % DT], 0, 0, 0);
   }
 
   const float sum = sum_halves(l);
