@@ -37,6 +37,8 @@ struct Tile {
   static constexpr int VB = VPL * (FP8 ? 1 : 2);           // bytes of them
   u32x4 k[2][KL];
   uint32_t v[8][VB / 4];
+  // FP8, the scales: of the two 16 keys of K and of V; LISTED, of key lane % 32, of K in lanes 0-31 and of V above
+  float scale[FP8 ? 4 : 1];
 };
 
 template <int N>
@@ -97,25 +99,93 @@ __device__ __forceinline__ bf16x8 v_operand(const Tile<FP8, D>& t, int i) {
 }
 
 template <bool FP8, int D, int RT, bool LISTED>
-__global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendArgs a) {
+__global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1) void attend_split_kernel(const AttendArgs a) {
   using TileT = Tile<FP8, D>;
   constexpr int KS = D / 32, VPL = TileT::VPL, ROW = TileT::ROW, M = 16 * RT;
-  constexpr int RUN = LISTED ? ATTEND_MAX_RUN_LISTED : ATTEND_MAX_RUN;
+  constexpr int RUN = LISTED ? ATTEND_RESOLVED_LISTED : ATTEND_RESOLVED;
+  constexpr int DEPTH = (FP8 || D == 64) && RT <= 2 && !LISTED ? 3 : 2;
   constexpr int PLACES = LISTED ? 32 : 2;  // places resolved per tile: single keys, or 16 in a row
   __shared__ int64_t s_row[RUN * PLACES];  // cached row of the place, or -1: nothing there
-  __shared__ float s_ks[FP8 ? RUN * PLACES : 1], s_vs[FP8 ? RUN * PLACES : 1];
   __shared__ float s_o[AT_WAVES][16][D + 4];
   __shared__ float s_m[AT_WAVES][16], s_l[AT_WAVES][16];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), col = lane & 15, g = lane >> 4;
-  const int64_t id = blockIdx.x;
-  const int h = (int)(id % a.c.n_kv);
-  const int split = (int)((id / a.c.n_kv) % a.splits);
+  const int h = (int)(blockIdx.x % a.c.n_kv);
+  const int worker = (int)(blockIdx.x / a.c.n_kv);
+
+  // The worker's share [at, end) of all tiles. 64 row blocks are looked at at a time: `upto` is the sum of
+  // the tiles of row blocks chunk .. chunk + lane, `before` that of the ones before the chunk. A row block with rows
+  // counts at least one tile, so that someone writes the rows that see nothing.
+  int chunk = 0;
+  int64_t upto = 0, before = 0, at = 0, end = 0, share = 0;
+  Seq mine{0, 0, 0, 0};  // row block chunk + lane
+  auto look = [&]() {
+    const int e = chunk + lane;
+    int64_t n = 0;
+    if (e < a.entries && entry_seq<LISTED>(a, e, &mine)) {
+      Rows w;
+      set_entry<LISTED>(a, e, mine, M, &w);
+      n = max(w.tiles, 1);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t x = __shfl_up(n, o);
+      n += lane >= o ? x : 0;
+    }
+    upto = n;
+  };
+  if (a.workers > 0) {
+    int64_t total = 0;
+    for (chunk = 0; chunk < a.entries; chunk += 64) {
+      look();
+      total += __shfl(upto, 63);
+    }
+    if (a.entries > 64) {
+      chunk = 0;
+      look();
+    } else {
+      chunk = 0;  // looked at already
+    }
+    share = max((total + a.workers - 1) / a.workers, (int64_t)AT_WAVES);
+    share = uni((share + AT_WAVES - 1) / AT_WAVES * AT_WAVES);
+    at = worker * share;
+    end = uni(min(at + share, total));
+  }
+
+  for (bool again = false;; again = true) {
   Rows w;
-  if (!find_rows<LISTED>(a, id / ((int64_t)a.c.n_kv * a.splits), M, &w)) return;
-  const int parts = (w.tiles + a.run - 1) / a.run;
-  if (split > 0 && split >= parts) return;
-  const int first = split * a.run, count = min(a.run, w.tiles - first);  // count is 0 where nothing is seen
+  int first = 0, count, parts = 1, entry = worker;
+  if (a.workers > 0) {
+    if (at >= end) return;
+    while (at >= before + uni(__shfl(upto, 63))) {
+      before += uni(__shfl(upto, 63));
+      chunk += 64;
+      look();
+    }
+    const int which = __ffsll((unsigned long long)__ballot(before + upto > at)) - 1;
+    entry = uni(chunk + which);
+    const Seq s = {__builtin_amdgcn_readlane(mine.n_tok, which), __builtin_amdgcn_readlane(mine.len, which),
+                   __builtin_amdgcn_readlane(mine.listed, which), __builtin_amdgcn_readlane(mine.row, which)};
+    set_entry<LISTED>(a, entry, s, M, &w);
+    pin_rows(&w);
+    const int64_t begins = before + uni(__shfl(upto, which)) - max(w.tiles, 1);
+    first = (int)(at - begins);
+    count = (int)min(end - at, (int64_t)max(w.tiles, 1) - first);
+    parts = (int)((begins + max(w.tiles, 1) - 1) / share - begins / share) + 1;
+    at += count;
+    if (first == 0 && tid == 0) {
+      a.joins[2 * (entry * a.c.n_kv + h)] = worker;
+      a.joins[2 * (entry * a.c.n_kv + h) + 1] = parts > 1 ? parts : 0;
+    }
+    count = min(count, w.tiles - first);  // 0 where nothing is seen
+  } else {
+    Seq s;
+    if (again || !entry_seq<LISTED>(a, entry, &s)) return;
+    set_entry<LISTED>(a, entry, s, M, &w);
+    pin_rows(&w);
+    count = w.tiles;
+  }
+  if (again) __syncthreads();
 
   // the block's queries: lane column = row
   bf16x8 q[RT][KS];
@@ -180,13 +250,8 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
         if (page >= 0 && page < a.c.n_pages) {
           const int64_t t = (int64_t)page * a.c.n_kv + h;
           row = (t << a.c.pt_log2) + (tok & ((1 << a.c.pt_log2) - 1));
-          if constexpr (FP8) {
-            s_ks[i] = a.c.k_scale[t] * a.scale_log2;
-            s_vs[i] = a.c.v_scale[t];
-          }
         }
       }
-      if (FP8 && row < 0) s_ks[i] = s_vs[i] = 0.f;
       s_row[i] = row;
     }
   };
@@ -205,6 +270,10 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
         const int64_t row = max(s_row[32 * i + 16 * (j / 4) + 4 * g + j % 4], (int64_t)0);
         load_words(a.c.v + row * ROW + col * TileT::VB, t.v[j]);
       }
+      if constexpr (FP8) {
+        const int64_t row = max(s_row[32 * i + lane % 32], (int64_t)0);
+        t.scale[0] = (lane < 32 ? a.c.k_scale : a.c.v_scale)[row >> a.c.pt_log2];
+      }
     } else {
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
@@ -215,11 +284,23 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
         for (int c = 0; c < TileT::KL; ++c) t.k[sub][c] = *(const u32x4*)(kb + (uint32_t)(col * ROW + 64 * c + 16 * g));
 #pragma unroll
         for (int j = 0; j < 4; ++j) load_words(vb + (uint32_t)((4 * g + j) * ROW + col * TileT::VB), t.v[4 * sub + j]);
+        if constexpr (FP8) {
+          t.scale[sub] = a.c.k_scale[row >> a.c.pt_log2];
+          t.scale[2 + sub] = a.c.v_scale[row >> a.c.pt_log2];
+        }
       }
     }
   };
 
   auto compute = [&](int i, TileT& t) {
+    float ks[FP8 && LISTED ? 8 : 1], vs[FP8 && LISTED ? 8 : 1];
+    if constexpr (FP8 && LISTED) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ks[j] = __shfl(t.scale[0], 16 * (j / 4) + 4 * g + j % 4);
+        vs[j] = __shfl(t.scale[0], 32 + 16 * (j / 4) + 4 * g + j % 4);
+      }
+    }
     // x[rt][j]: score, base 2, of key 16 (j / 4) + 4 g + j % 4
     float x[RT][8];
 #pragma unroll
@@ -238,7 +319,7 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float f = a.scale_log2;
-          if constexpr (FP8) f = LISTED ? s_ks[32 * i + 16 * sub + 4 * g + j] : s_ks[2 * i + sub];
+          if constexpr (FP8) f *= LISTED ? ks[4 * sub + j] : t.scale[sub];
           x[rt][4 * sub + j] = s[rt][j] * f;
         }
     }
@@ -310,9 +391,10 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
         float y0 = __builtin_amdgcn_exp2f(x[rt][j] - m[rt]), y1 = __builtin_amdgcn_exp2f(x[rt][j + 1] - m[rt]);
         l[rt] += y0 + y1;
         if constexpr (FP8) {
-          const int at = LISTED ? 32 * i + 16 * (j / 4) + 4 * g + j % 4 : 2 * i + j / 4;
-          y0 *= s_vs[at];
-          y1 *= s_vs[LISTED ? at + 1 : at];
+          // where nothing is seen the scale may be anything: 0 stays 0
+          const float v0 = LISTED ? vs[j] : t.scale[2 + j / 4], v1 = LISTED ? vs[j + 1] : v0;
+          y0 = y0 == 0.f ? 0.f : y0 * v0;
+          y1 = y1 == 0.f ? 0.f : y1 * v1;
         }
         packed[j / 2] = pack_bf16(y0, y1);
       }
@@ -327,22 +409,22 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
     if constexpr (!LISTED) {
       if (rescue) {
         const int t0 = w.near.tile(base + i) * 32;
+#pragma unroll 1
         for (int j = 0; j < 32; ++j) {
           const int64_t row = uni(s_row[2 * i + j / 16]);
           if (row < 0) continue;
           const char* src = a.c.v + (row + j % 16) * ROW;
           const int tok = t0 + j;
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const bool seen = tok <= p_row[rt] &&
-                              (tok > w_row[rt] || tok < a.sinks);
+          for (int e = 0; e < VPL; ++e) {
 #pragma unroll
-            for (int e = 0; e < VPL; ++e)
+            for (int c = 0; c < 4; ++c) {
+              const float y = cached_value<FP8>(src, VPL * (4 * g + c) + e);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float y = cached_value<FP8>(src, VPL * (4 * g + c) + e);
-                if (seen && !(fabsf(y) < __builtin_inff())) acc[rt][e][c] += y;
-              }
+              for (int rt = 0; rt < RT; ++rt)
+                if (tok <= p_row[rt] && (tok > w_row[rt] || tok < a.sinks) && !(fabsf(y) < __builtin_inff())) acc[rt][e][c] += y;
+            }
+            __builtin_amdgcn_sched_barrier(0);  // rare: keep its registers few
           }
         }
       }
@@ -356,19 +438,18 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
     resolve(base, n);
     __syncthreads();
     if (wave >= n) continue;
-    // two tiles in registers: the loads of the next one are in flight while one is worked on
-    TileT t0, t1;
-    int i = wave;
-    load(i, t0);
-    for (;;) {
-      const int j = i + AT_WAVES;
-      if (j < n) load(j, t1);
-      compute(i, t0);
-      if (j >= n) break;
-      i = j + AT_WAVES;
-      if (i < n) load(i, t0);
-      compute(j, t1);
-      if (i >= n) break;
+    // DEPTH tiles in registers: the loads of the next ones are in flight while one is worked on
+    TileT t[DEPTH];
+#pragma unroll
+    for (int x = 0; x < DEPTH - 1; ++x)
+      if (wave + x * AT_WAVES < n) load(wave + x * AT_WAVES, t[x]);
+    for (int i = wave; i < n; i += DEPTH * AT_WAVES) {
+#pragma unroll
+      for (int x = 0; x < DEPTH; ++x) {
+        const int now = i + x * AT_WAVES, then = now + (DEPTH - 1) * AT_WAVES;
+        if (then < n) load(then, t[(x + DEPTH - 1) % DEPTH]);
+        if (now < n) compute(now, t[x]);
+      }
     }
   }
 
@@ -414,81 +495,99 @@ __global__ __launch_bounds__(AT_THREADS) void attend_split_kernel(const AttendAr
         if (a.lse && tid % 16 == 0)
           a.lse[(w.t0 + tok) * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (top + __log2f(sum)) * LN2;
       } else {
-        const int64_t at = ((int64_t)split * a.T + (w.t0 - a.first_row + tok)) * a.n_q + head;
+        const int64_t to = (((int64_t)worker + entry) * a.c.n_kv + h) * M + rt * 16 + r;
 #pragma unroll
-        for (int e = 0; e < VPL; e += 4) *(f32x4*)(a.part_o + at * D + d0 + e) = (f32x4){o[e], o[e + 1], o[e + 2], o[e + 3]};
-        if (tid % 16 == 0) *(f32x2*)(a.part_ml + 2 * at) = (f32x2){top, sum};
+        for (int e = 0; e < VPL; e += 4) *(f32x4*)(a.part_o + to * D + d0 + e) = (f32x4){o[e], o[e + 1], o[e + 2], o[e + 3]};
+        if (tid % 16 == 0) *(f32x2*)(a.part_ml + 2 * to) = (f32x2){top, sum};
       }
     }
   }
+  }
 }
 
-// Joins the partial results of rows whose keys were split: one wave per row.
+// Joins `parts` partial results of one row, at first, first + step, ...: one wave per row.
+template <int D>
+__device__ __forceinline__ void join_row(const AttendArgs& a, int64_t first, int64_t step, int parts, int64_t row, int head) {
+  constexpr int LP = D / 4, GP = 64 / LP, UN = 4;  // lanes of a part, parts at once, and of those in flight
+  const int lane = threadIdx.x & 63, d0 = lane % LP * 4;
+  float top = ATTEND_LOWEST;
+  for (int s = lane; s < parts; s += 64) top = fmaxf(top, a.part_ml[2 * (first + s * step)]);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  float sum = 0.f;
+  f32x4 acc = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < parts; s0 += 64) {
+    const int n = min(64, parts - s0);
+    float f = 0.f;
+    if (lane < n) {
+      const f32x2 ml = *(const f32x2*)(a.part_ml + 2 * (first + (s0 + lane) * step));
+      f = __builtin_amdgcn_exp2f(ml[0] - top);
+      sum += ml[1] * f;
+    }
+    for (int s = 0; s < n; s += GP * UN) {
+      f32x4 o[UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u)
+        o[u] = *(const f32x4*)(a.part_o + (first + (s0 + min(s + u * GP + lane / LP, n - 1)) * step) * D + d0);
+#pragma unroll
+      for (int u = 0; u < UN; ++u) acc += o[u] * __shfl(f, s + u * GP + lane / LP);  // lanes from n on hold a factor of 0
+    }
+  }
+#pragma unroll
+  for (int o = LP; o < 64; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], o);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (lane < LP)
+    *(u32x2*)(a.out + row * a.out_stride + (int64_t)head * D + d0) =
+        (u32x2){pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
+  if (a.lse && lane == 0) a.lse[row * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (top + __log2f(sum)) * LN2;
+}
+
 template <int D, bool LISTED>
-__global__ __launch_bounds__(AT_THREADS) void attend_join_kernel(const AttendArgs a, int M) {
-  const int lane = threadIdx.x & 63;
+__global__ __launch_bounds__(AT_THREADS) void split_join_kernel(const AttendArgs a, int M) {
+  const int64_t id = (int64_t)blockIdx.x * AT_WAVES + (threadIdx.x >> 6);
+  if (id >= a.T * a.n_q) return;
+  const int64_t t = id / a.n_q;
+  const int head = (int)(id - t * a.n_q), h = head / a.G;
+  int entry, r = head - h * a.G;
+  if constexpr (LISTED) {
+    entry = (int)t * a.per + r / M;
+    r %= M;
+  } else {
+    if (t + a.first_row >= a.off[a.B]) return;
+    entry = upper_seq(a.off, a.B, t + a.first_row);
+    if (!of_class(a, a.off[entry + 1] - a.off[entry])) return;
+    r += (int)(t + a.first_row - a.off[entry]) * a.G;
+  }
+  const int worker = a.joins[2 * ((int64_t)entry * a.c.n_kv + h)], parts = a.joins[2 * ((int64_t)entry * a.c.n_kv + h) + 1];
+  if (parts == 0) return;
+  join_row<D>(a, (((int64_t)worker + entry) * a.c.n_kv + h) * M + r, (int64_t)a.c.n_kv * M, parts, t + a.first_row, head);
+}
+
+template <int D>
+__global__ __launch_bounds__(AT_THREADS) void tile_join_kernel(const AttendArgs a) {
   const int64_t id = (int64_t)blockIdx.x * AT_WAVES + (threadIdx.x >> 6);
   if (id >= a.T * a.n_q) return;
   const int64_t t = id / a.n_q;
   const int head = (int)(id - t * a.n_q);
+  if (t + a.first_row >= a.off[a.B]) return;
   Rows w;
-  int64_t n_tok = 1;
-  if constexpr (LISTED) {
-    w.b = (int)t;
-    w.t0 = t;
-  } else {
-    if (t + a.first_row >= a.off[a.B]) return;
-    w.b = upper_seq(a.off, a.B, t + a.first_row);
-    w.t0 = a.off[w.b];
-    n_tok = a.off[w.b + 1] - w.t0;
-    if (!of_class(a, n_tok)) return;
-  }
+  w.b = upper_seq(a.off, a.B, t + a.first_row);
+  w.t0 = a.off[w.b];
+  const int64_t n_tok = a.off[w.b + 1] - w.t0;
+  if (!of_class(a, n_tok)) return;
   const int64_t row = (t + a.first_row - w.t0) * a.G + head % a.G;
-  set_block<LISTED>(a, n_tok, row / M, M, &w);
+  set_block<false>(a, seq_of<false>(a, w.b, w.t0, n_tok), (int32_t)(row / ATTEND_TILE_ROWS), ATTEND_TILE_ROWS, &w);
   const int parts = (w.tiles + a.run - 1) / a.run;
-  if (parts <= 1) return;
-  const int64_t step = a.T * a.n_q;
-  float top = ATTEND_LOWEST;
-  for (int s = lane; s < parts; s += 64) top = fmaxf(top, a.part_ml[2 * (s * step + id)]);
-#pragma unroll
-  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  constexpr int W = D / 64;
-  float sum = 0.f, acc[W] = {};
-  for (int s0 = 0; s0 < parts; s0 += 64) {
-    const int n = min(64, parts - s0);
-    float f = 0.f, part = 0.f;
-    if (lane < n) {
-      const f32x2 ml = *(const f32x2*)(a.part_ml + 2 * ((s0 + lane) * step + id));
-      f = __builtin_amdgcn_exp2f(ml[0] - top);
-      part = ml[1] * f;
-    }
-    sum += part;
-    for (int s = 0; s < n; s += 4) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {  // lanes from n on hold a factor of 0
-        const float x = __shfl(f, s + u);
-        const float* src = a.part_o + ((s0 + min(s + u, n - 1)) * step + id) * D + lane * W;
-#pragma unroll
-        for (int e = 0; e < W; ++e) acc[e] += src[e] * x;
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t* dst = a.out + (t + a.first_row) * a.out_stride + (int64_t)head * D + lane * W;
-  if constexpr (W == 2) {
-    *(uint32_t*)dst = pack_bf16(acc[0] * inv, acc[1] * inv);
-  } else {
-    *dst = (uint16_t)pack_bf16(acc[0] * inv, 0.f);
-  }
-  if (a.lse && lane == 0)
-    a.lse[(t + a.first_row) * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (top + __log2f(sum)) * LN2;
+  if (parts > 1) join_row<D>(a, id, a.T * a.n_q, parts, t + a.first_row, head);
 }
 
 template <bool FP8, int D, bool LISTED>
 static hipError_t launch_rows(const AttendArgs& a, int row_tiles, hipStream_t s) {
-  const dim3 grid((unsigned)(a.blocks * a.splits * a.c.n_kv));
+  const dim3 grid((unsigned)((a.workers > 0 ? a.workers : a.entries) * (int64_t)a.c.n_kv));
   if (row_tiles == 1) attend_split_kernel<FP8, D, 1, LISTED><<<grid, AT_THREADS, 0, s>>>(a);
   else if (row_tiles == 2) attend_split_kernel<FP8, D, 2, LISTED><<<grid, AT_THREADS, 0, s>>>(a);
   else attend_split_kernel<FP8, D, 4, LISTED><<<grid, AT_THREADS, 0, s>>>(a);
@@ -505,15 +604,22 @@ hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_til
   return listed ? launch_dim<true>(a, fp8, d, row_tiles, s) : launch_dim<false>(a, fp8, d, row_tiles, s);
 }
 
-hipError_t launch_attend_join(const AttendArgs& a, int d, int M, bool listed, hipStream_t s) {
-  const dim3 grid((unsigned)((a.T * a.n_q + AT_WAVES - 1) / AT_WAVES));
+static dim3 join_grid(const AttendArgs& a) { return dim3((unsigned)((a.T * a.n_q + AT_WAVES - 1) / AT_WAVES)); }
+
+hipError_t launch_attend_split_join(const AttendArgs& a, int d, int M, bool listed, hipStream_t s) {
   if (listed) {
-    if (d == 64) attend_join_kernel<64, true><<<grid, AT_THREADS, 0, s>>>(a, M);
-    else attend_join_kernel<128, true><<<grid, AT_THREADS, 0, s>>>(a, M);
+    if (d == 64) split_join_kernel<64, true><<<join_grid(a), AT_THREADS, 0, s>>>(a, M);
+    else split_join_kernel<128, true><<<join_grid(a), AT_THREADS, 0, s>>>(a, M);
   } else {
-    if (d == 64) attend_join_kernel<64, false><<<grid, AT_THREADS, 0, s>>>(a, M);
-    else attend_join_kernel<128, false><<<grid, AT_THREADS, 0, s>>>(a, M);
+    if (d == 64) split_join_kernel<64, false><<<join_grid(a), AT_THREADS, 0, s>>>(a, M);
+    else split_join_kernel<128, false><<<join_grid(a), AT_THREADS, 0, s>>>(a, M);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_attend_tile_join(const AttendArgs& a, int d, hipStream_t s) {
+  if (d == 64) tile_join_kernel<64><<<join_grid(a), AT_THREADS, 0, s>>>(a);
+  else tile_join_kernel<128><<<join_grid(a), AT_THREADS, 0, s>>>(a);
   return hipGetLastError();
 }
 

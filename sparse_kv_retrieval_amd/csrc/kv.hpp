@@ -40,9 +40,8 @@ struct AppendArgs {
 inline int64_t append_page_slots(int64_t T, int32_t B, int32_t pt) { return T / pt + 2 * (int64_t)B; }
 
 // Work of one attention launch. Rows of a sequence are its (new token, query head of the group)
-// pairs, row = token * G + head; a row block is M of them for one key head. The keys that a row
-// block sees are numbered in tiles (first tokens, then the window; listed entries last) and split in
-// runs of `run` tiles; partial results of several runs are joined by a second launch. A launch works
+// pairs, row = token * G + head; a row block is up to M of them for one key head. The keys that a row
+// block sees are numbered in tiles (first tokens, then the window; listed entries last). A launch works
 // on the sequences with more than rows_above and at most rows_to rows.
 struct AttendArgs {
   KvView c;
@@ -53,14 +52,23 @@ struct AttendArgs {
   const int64_t* off;     // [B+1], or null: one row each (lsa_attend_topk)
   const int32_t* idx;     // [B][k] listed entries, or null
   const int32_t* count;   // [B]
-  float* part_o;          // [splits][T][n_q][D]
-  float* part_ml;         // [splits][T][n_q][2]: running maximum (base 2) and sum
   int64_t first_row, T;
-  int64_t blocks;         // row-block slots
   float scale_log2;       // softmax scale * log2(e)
   int32_t B, n_q, G, max_kv_len, window, sinks, k, r;
-  int32_t splits, run, tile;  // tile: keys per tile
+  int32_t tile;           // keys per tile
   int64_t rows_above, rows_to;
+  float* part_o;          // partial results of row blocks whose keys are split
+  float* part_ml;         // and their running maximum (base 2) and sum
+  // Tile kernel: a row block's keys are split in runs of `run` tiles; partials [splits][T][n_q][D].
+  int64_t blocks;         // row-block slots
+  int32_t splits, run;
+  // Split kernel: the tiles of all row blocks of a key head, one after the other, are shared evenly by
+  // `workers` blocks (0: each row block has a worker of its own). A worker's part of a row block goes to
+  // partials [worker + row block][n_kv][M][D], a number that no two parts have, and
+  // joins[row block][n_kv] says which workers took part.
+  int32_t entries, per;   // row blocks, and how many of them a sequence has (LISTED)
+  int32_t workers;
+  int32_t* joins;         // pairs: first worker, number of parts (0: written whole)
 };
 
 // Tiles of `tile` tokens that the rows at positions p_lo..p_hi see. Tile i < n_first is tile i of the
@@ -86,12 +94,13 @@ __host__ __device__ __forceinline__ TileRange tile_range(int32_t p_lo, int32_t p
   return t;
 }
 
-constexpr int ATTEND_MAX_RUN = 64;         // tiles of one split
-constexpr int ATTEND_MAX_RUN_LISTED = 16;  // the same over listed keys, each with a place of its own in LDS
+constexpr int ATTEND_RESOLVED = 64;         // tiles whose places a block of the split kernel holds at once
+constexpr int ATTEND_RESOLVED_LISTED = 16;  // the same over listed keys, each with a place of its own
 
 hipError_t launch_kv_append(const AppendArgs& a, bool fp8, int d, int style, hipStream_t s);
 hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_tiles, bool listed, hipStream_t s);
-hipError_t launch_attend_join(const AttendArgs& a, int d, int rows, bool listed, hipStream_t s);
+hipError_t launch_attend_split_join(const AttendArgs& a, int d, int rows, bool listed, hipStream_t s);
+hipError_t launch_attend_tile_join(const AttendArgs& a, int d, hipStream_t s);
 hipError_t launch_attend_tile(const AttendArgs& a, bool fp8, int d, hipStream_t s);
 constexpr int ATTEND_TILE_ROWS = 256;  // rows of a block of attend_tile_kernel
 constexpr int ATTEND_TILE_KEYS = 64;   // keys of its tiles
@@ -139,56 +148,76 @@ __device__ __forceinline__ bool of_class(const AttendArgs& a, int64_t n_tok) {
   return rows > a.rows_above && rows <= a.rows_to;
 }
 
+// What a row block's sequence brings: its new tokens, its cached tokens and (LISTED) its listed entries.
+struct Seq {
+  int32_t n_tok, len, listed;
+  int32_t row;  // its first row, after first_row
+};
+
 template <bool LISTED>
-__device__ __forceinline__ void set_block(const AttendArgs& a, int64_t n_tok, int64_t j, int M, Rows* w) {
-  const int64_t rows = n_tok * a.G;
-  w->r0 = (int32_t)(j * M);
-  w->n = (int32_t)min((int64_t)M, rows - j * M);
-  const int32_t len = min(max(a.c.kv_len[w->b], 0), a.max_kv_len);
-  w->p0 = (int32_t)(len - n_tok);
+__device__ __forceinline__ Seq seq_of(const AttendArgs& a, int b, int64_t row, int64_t n_tok) {
+  return {(int32_t)n_tok, min(max(a.c.kv_len[b], 0), a.max_kv_len), LISTED ? min(max(a.count[b], 0), a.k) : 0,
+          (int32_t)(row - a.first_row)};
+}
+
+template <bool LISTED>
+__device__ __forceinline__ void set_block(const AttendArgs& a, Seq s, int32_t j, int M, Rows* w) {
+  w->r0 = j * M;
+  w->n = min(M, s.n_tok * a.G - j * M);
+  w->p0 = s.len - s.n_tok;
   w->p_lo = w->p0 + w->r0 / a.G;
   w->p_hi = w->p0 + (w->r0 + w->n - 1) / a.G;
   w->w_lo = window_start(a, w->p_lo);
   w->w_hi = window_start(a, w->p_hi);
   if constexpr (LISTED) {
-    const int64_t some = (int64_t)min(max(a.count[w->b], 0), a.k) * a.r;
     if (a.window > 0) {
       w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks, a.tile);
     } else {
-      const int32_t end = w->p_hi < 0 ? 0 : w->p_hi / 32 + 1, s = a.sinks / 32 + (a.sinks % 32 != 0);
-      w->near.n_first = w->near.n = min(s, end);
+      const int32_t end = w->p_hi < 0 ? 0 : w->p_hi / 32 + 1, first = a.sinks / 32 + (a.sinks % 32 != 0);
+      w->near.n_first = w->near.n = min(first, end);
       w->near.first_b = 0;
     }
-    w->tiles = w->p_hi < 0 ? 0 : w->near.n + (int32_t)((some + 31) / 32);
+    w->tiles = w->p_hi < 0 ? 0 : w->near.n + (int32_t)(((int64_t)s.listed * a.r + 31) / 32);
   } else {
     w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks, a.tile);
     w->tiles = w->near.n;
   }
 }
 
-template <bool LISTED>
-__device__ __forceinline__ bool find_rows(const AttendArgs& a, int64_t block, int M, Rows* w) {
-  int64_t n_tok, j;
-  if constexpr (LISTED) {
-    const int per = (a.G + M - 1) / M;
-    w->b = (int)(block / per);
-    w->t0 = w->b;
-    n_tok = 1;
-    j = block % per;
-  } else {
-    auto slot_of = [&](int x) -> int64_t { return (a.off[x] - a.first_row) * a.G / M + x; };
-    w->b = wave_find(a.B, block, slot_of);
-    w->t0 = a.off[w->b];
-    n_tok = a.off[w->b + 1] - w->t0;
-    j = block - slot_of(w->b);
-    if (j * M >= n_tok * a.G || !of_class(a, n_tok)) return false;
-  }
-  set_block<LISTED>(a, n_tok, j, M, w);
-  // the block agrees on all of it: scalar registers
-  w->n = uni(w->n); w->r0 = uni(w->r0); w->p0 = uni(w->p0); w->p_lo = uni(w->p_lo); w->p_hi = uni(w->p_hi);
+// The fields that a block agrees on, in scalar registers.
+__device__ __forceinline__ void pin_rows(Rows* w) {
+  w->b = uni(w->b); w->n = uni(w->n); w->r0 = uni(w->r0); w->p0 = uni(w->p0); w->p_lo = uni(w->p_lo); w->p_hi = uni(w->p_hi);
   w->w_lo = uni(w->w_lo); w->w_hi = uni(w->w_hi); w->t0 = uni(w->t0); w->tiles = uni(w->tiles);
   w->near.n_first = uni(w->near.n_first); w->near.first_b = uni(w->near.first_b); w->near.n = uni(w->near.n);
+}
+
+// Tile kernel: the row block of a slot (see AttendArgs::blocks), if it has rows.
+__device__ __forceinline__ bool find_rows(const AttendArgs& a, int64_t block, int M, Rows* w) {
+  auto slot_of = [&](int x) -> int64_t { return (a.off[x] - a.first_row) * a.G / M + x; };
+  w->b = wave_find(a.B, block, slot_of);
+  w->t0 = a.off[w->b];
+  const int64_t n_tok = a.off[w->b + 1] - w->t0, j = block - slot_of(w->b);
+  if (j * M >= n_tok * a.G || !of_class(a, n_tok)) return false;
+  set_block<false>(a, seq_of<false>(a, w->b, w->t0, n_tok), (int32_t)j, M, w);
+  pin_rows(w);
   return true;
+}
+
+// Split kernel: row block e is block e % per of sequence e / per (only LISTED sequences have several).
+// Whether it has rows; its sequence.
+template <bool LISTED>
+__device__ __forceinline__ bool entry_seq(const AttendArgs& a, int e, Seq* s) {
+  const int b = LISTED ? e / a.per : e;
+  const int64_t row = LISTED ? b : a.off[b], n_tok = LISTED ? 1 : a.off[b + 1] - row;
+  *s = seq_of<LISTED>(a, b, row, n_tok);
+  if (!LISTED && !of_class(a, n_tok)) return false;
+  return true;
+}
+template <bool LISTED>
+__device__ __forceinline__ void set_entry(const AttendArgs& a, int e, Seq s, int M, Rows* w) {
+  w->b = LISTED ? e / a.per : e;
+  w->t0 = a.first_row + s.row;
+  set_block<LISTED>(a, s, LISTED ? e - w->b * a.per : 0, M, w);
 }
 
 // The elements of a dword that are not finite, as a mask over its bits.

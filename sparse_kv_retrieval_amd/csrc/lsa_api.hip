@@ -693,24 +693,52 @@ lsa_status check_rows(int32_t B, const int64_t* off, const int64_t* off_host, in
   return LSA_OK;
 }
 
-// How one attention launch is laid over the device; depends only on host arguments.
-struct AttendPlan {
-  bool used;
-  int32_t rows;    // rows of a row block
-  int32_t splits, run;
-  int64_t blocks;  // row-block slots
-  size_t bytes;    // workspace
+int64_t near_tiles(int64_t window, int64_t sinks, int64_t tile) {
+  return (sinks + tile - 1) / tile + (window > 0 ? (window + tile - 2) / tile + 1 : 0);
+}
+
+// How one launch of the split kernel is laid over the device; depends only on host arguments.
+struct SplitPlan {
+  int32_t rows = 16;         // rows of a row block
+  int32_t entries = 0;       // row blocks of a key head (0: no launch)
+  int32_t per = 1;           // of them, a sequence's
+  int32_t workers = 0;       // blocks of a key head that share its tiles; 0: one per row block, none shared
+  size_t joins = 0, ml = 0;  // where the joins and the partials' statistics begin in the workspace
+  size_t bytes = 0;
 };
 
-// Keys are split in runs while the row blocks with rows (`filled`) do not fill the device: to about
-// `want` blocks in all, with runs of `least` to `most` tiles, and not beyond kPartialBytes of partials.
-void split_keys(AttendPlan* p, int64_t filled, int64_t T, int32_t n_q, int32_t d, int64_t tiles, int64_t least, int64_t most,
-                int64_t want) {
+// The blocks that share the tiles are as many as the device holds at once: one a CU where the rows' and a tile's
+// registers are many (four row tiles, or two of bf16, at d_h 128), two otherwise. More were slower on every
+// size tried (32 ragged sequences in e4m3: 401 us with 512, 407 with 1024, 416 with 2048; their windows of 1024:
+// 28.4, 32.9 and 37.1 us): they add partial results and a second round. Row blocks of at most four tiles, one
+// a wave, are not worth sharing. The workspace's size does not depend on the cache's dtype.
+void share_tiles(SplitPlan* p, int32_t n_kv, int32_t d, bool fp8, int64_t tiles) {
+  if (p->entries == 0 || tiles <= 4) return;
+  // no worker has fewer than four tiles
+  auto workers = [&](int64_t blocks) {
+    return (int32_t)std::min<int64_t>(std::max<int64_t>(blocks / n_kv, 1), (p->entries * tiles + 3) / 4);
+  };
+  p->workers = workers(p->rows * d * (fp8 ? 1 : 2) >= 64 * 128 ? 256 : 512);
+  const size_t rows = (size_t)(workers(512) + p->entries) * n_kv * p->rows;
+  p->ml = rows * d * 4;
+  p->joins = p->ml + rows * 8;
+  p->bytes = p->joins + (size_t)p->entries * n_kv * 8;
+}
+
+// The same for the tile kernel: keys are split in runs while the row blocks do not fill the device.
+struct TilePlan {
+  bool used = false;
+  int32_t splits = 1, run = 1;
+  int64_t blocks = 0;  // row-block slots
+  size_t ml = 0, bytes = 0;
+};
+
+void split_keys(TilePlan* p, int64_t filled, int64_t T, int32_t n_q, int32_t d, int64_t tiles) {
+  constexpr int64_t want = 512, least = 4;  // blocks in all, and tiles of a run
   tiles = std::max<int64_t>(tiles, 1);
   int64_t run = tiles;
   if (filled < want / 2) {
-    run = std::min(std::max((tiles * filled + want - 1) / want, least), most);
-    run = (run + least - 1) / least * least;
+    run = std::max((tiles * filled + want - 1) / want, least);
     const size_t per = (size_t)std::max<int64_t>(T, 1) * n_q * (d + 2) * 4;
     const int64_t splits = std::max<int64_t>((int64_t)(kPartialBytes / per), 2);
     run = std::max(run, (tiles + splits - 1) / splits);
@@ -718,11 +746,10 @@ void split_keys(AttendPlan* p, int64_t filled, int64_t T, int32_t n_q, int32_t d
   p->used = filled > 0;
   p->run = (int32_t)std::min(run, tiles);
   p->splits = (int32_t)((tiles + p->run - 1) / p->run);
-  p->bytes = p->used && p->splits > 1 ? (size_t)p->splits * T * n_q * (d + 2) * 4 : 0;
-}
-
-int64_t near_tiles(int64_t window, int64_t sinks, int64_t tile) {
-  return (sinks + tile - 1) / tile + (window > 0 ? (window + tile - 2) / tile + 1 : 0);
+  if (p->used && p->splits > 1) {
+    p->ml = (size_t)p->splits * T * n_q * d * 4;
+    p->bytes = p->ml + (size_t)p->splits * T * n_q * 8;
+  }
 }
 
 // Sequences with at most this many rows (new tokens times query heads of a group) go to the split
@@ -730,47 +757,43 @@ int64_t near_tiles(int64_t window, int64_t sinks, int64_t tile) {
 constexpr int64_t kSplitRows = 64;
 
 struct RaggedPlan {
-  AttendPlan few, many;
-  size_t bytes;
+  SplitPlan few;
+  TilePlan many;
+  size_t bytes = 0;
 };
 
 RaggedPlan plan_ragged(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, const int64_t* off, int32_t max_kv_len,
-                       int32_t window, int32_t sinks) {
-  RaggedPlan r{};
+                       int32_t window, int32_t sinks, bool fp8 = false) {
+  RaggedPlan r;
   const int64_t T = off[B] - off[0], G = n_q / n_kv;
-  int64_t most = 0, few = 0, many = 0;
+  int64_t most = 0, many = 0;
   for (int32_t b = 0; b < B; ++b) {
     const int64_t rows = (off[b + 1] - off[b]) * G;
     if (rows <= kSplitRows) most = std::max(most, rows);
     else many += (rows + ATTEND_TILE_ROWS - 1) / ATTEND_TILE_ROWS;
   }
   r.few.rows = most <= 16 ? 16 : most <= 32 ? 32 : 64;
-  for (int32_t b = 0; b < B; ++b) {
-    const int64_t rows = (off[b + 1] - off[b]) * G;
-    if (rows <= kSplitRows) few += (rows + r.few.rows - 1) / r.few.rows;
-  }
-  r.few.blocks = T * G / r.few.rows + B;
-  r.many.rows = ATTEND_TILE_ROWS;
+  r.few.entries = most > 0 ? B : 0;
   r.many.blocks = T * G / ATTEND_TILE_ROWS + B;
   // a row block of several tokens sees that many more keys than its window
   auto tiles = [&](int64_t rows, int64_t tile) {
     const int64_t all = ((int64_t)max_kv_len + tile - 1) / tile;
     return window > 0 ? std::min(all, near_tiles((int64_t)window + rows - 1, sinks, tile)) : all;
   };
-  split_keys(&r.few, few * n_kv, T, n_q, d, tiles(r.few.rows, 32), 4, ATTEND_MAX_RUN, 1024);
-  split_keys(&r.many, many * n_kv, T, n_q, d, tiles(ATTEND_TILE_ROWS, ATTEND_TILE_KEYS), 4, INT32_MAX, 512);
+  share_tiles(&r.few, n_kv, d, fp8, tiles(r.few.rows, 32));
+  split_keys(&r.many, many * n_kv, T, n_q, d, tiles(ATTEND_TILE_ROWS, ATTEND_TILE_KEYS));
   r.bytes = std::max(r.few.bytes, r.many.bytes);
   return r;
 }
 
-AttendPlan plan_listed(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t k, int32_t entry_tokens, int32_t window,
-                       int32_t sinks) {
-  AttendPlan p{};
-  const int64_t G = n_q / n_kv;
+SplitPlan plan_listed(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t k, int32_t entry_tokens, int32_t window,
+                      int32_t sinks, bool fp8 = false) {
+  SplitPlan p;
+  const int32_t G = n_q / n_kv;
   p.rows = G <= 16 ? 16 : G <= 32 ? 32 : 64;
-  p.blocks = B * ((G + p.rows - 1) / p.rows);
-  const int64_t tiles = near_tiles(window, sinks, 32) + ((int64_t)k * entry_tokens + 31) / 32;
-  split_keys(&p, p.blocks * n_kv, B, n_q, d, tiles, 4, ATTEND_MAX_RUN_LISTED, 1024);
+  p.per = (G + p.rows - 1) / p.rows;
+  p.entries = B * p.per;
+  share_tiles(&p, n_kv, d, fp8, near_tiles(window, sinks, 32) + ((int64_t)k * entry_tokens + 31) / 32);
   return p;
 }
 
@@ -802,20 +825,32 @@ lsa_status attend_args(AttendArgs* a, size_t bytes, int32_t d, const void* q, in
   return LSA_OK;
 }
 
-bool plan_fits(const AttendPlan& p, const AttendArgs& a) {
+bool plan_fits(const SplitPlan& p, const AttendArgs& a) {
+  return (int64_t)std::max(p.workers, p.entries) * a.c.n_kv <= kMaxBlocks && a.T * a.n_q <= kMaxBlocks * 4;
+}
+bool plan_fits(const TilePlan& p, const AttendArgs& a) {
   return !p.used || (p.blocks * p.splits * a.c.n_kv <= kMaxBlocks && a.T * a.n_q <= kMaxBlocks * 4);
 }
 
-// One attention launch over the sequences with more than `above` and at most `to` rows.
-hipError_t launch_plan(AttendArgs a, const AttendPlan& p, bool fp8, int32_t d, bool tiled, int64_t above, int64_t to,
-                       hipStream_t stream) {
-  if (!p.used) return hipSuccess;
+hipError_t launch_plan(AttendArgs a, const SplitPlan& p, bool fp8, int32_t d, hipStream_t stream) {
+  if (p.entries == 0) return hipSuccess;
   const bool listed = a.idx != nullptr;
-  a.blocks = p.blocks; a.splits = p.splits; a.run = p.run; a.tile = tiled ? ATTEND_TILE_KEYS : 32;
-  a.rows_above = above; a.rows_to = to;
-  a.part_ml = a.part_o + (p.splits > 1 ? (size_t)p.splits * a.T * a.n_q * d : 0);
-  hipError_t e = tiled ? launch_attend_tile(a, fp8, d, stream) : launch_attend_split(a, fp8, d, p.rows / 16, listed, stream);
-  if (e == hipSuccess && p.splits > 1) e = launch_attend_join(a, d, p.rows, listed, stream);
+  a.entries = p.entries; a.per = p.per; a.workers = p.workers; a.tile = 32;
+  a.rows_above = 0; a.rows_to = listed ? INT64_MAX : kSplitRows;
+  a.part_ml = (float*)((char*)a.part_o + p.ml);
+  a.joins = (int32_t*)((char*)a.part_o + p.joins);
+  hipError_t e = launch_attend_split(a, fp8, d, p.rows / 16, listed, stream);
+  if (e == hipSuccess && p.workers > 0) e = launch_attend_split_join(a, d, p.rows, listed, stream);
+  return e;
+}
+
+hipError_t launch_plan(AttendArgs a, const TilePlan& p, bool fp8, int32_t d, hipStream_t stream) {
+  if (!p.used) return hipSuccess;
+  a.blocks = p.blocks; a.splits = p.splits; a.run = p.run; a.tile = ATTEND_TILE_KEYS;
+  a.rows_above = kSplitRows; a.rows_to = INT64_MAX;
+  a.part_ml = (float*)((char*)a.part_o + p.ml);
+  hipError_t e = launch_attend_tile(a, fp8, d, stream);
+  if (e == hipSuccess && p.splits > 1) e = launch_attend_tile_join(a, d, stream);
   return e;
 }
 
@@ -896,13 +931,13 @@ lsa_status lsa_attend(const lsa_kv_cache* cache, int32_t B, const void* q, int64
   a.B = B; a.n_q = n_q; a.max_kv_len = max_kv_len; a.window = window; a.sinks = sinks; a.r = 1;
   if (a.T == 0) return LSA_OK;  // no rows: q and out may be NULL
   const int32_t d = cache->d_h;
-  const RaggedPlan p = plan_ragged(B, n_q, a.c.n_kv, d, q_offsets_host, max_kv_len, window, sinks);
+  const RaggedPlan p = plan_ragged(B, n_q, a.c.n_kv, d, q_offsets_host, max_kv_len, window, sinks, fp8);
   if ((s = attend_args(&a, p.bytes, d, q, q_stride, softmax_scale, out, out_stride, lse, workspace, workspace_bytes)) != LSA_OK)
     return s;
   if (!plan_fits(p.few, a) || !plan_fits(p.many, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows for one call");
   // the two launches and their joins use the workspace one after the other
-  hipError_t e = launch_plan(a, p.few, fp8, d, false, 0, kSplitRows, stream);
-  if (e == hipSuccess) e = launch_plan(a, p.many, fp8, d, true, kSplitRows, INT64_MAX, stream);
+  hipError_t e = launch_plan(a, p.few, fp8, d, stream);
+  if (e == hipSuccess) e = launch_plan(a, p.many, fp8, d, stream);
   return e == hipSuccess ? LSA_OK : hip_fail("lsa_attend launch", e);
 }
 
@@ -929,13 +964,13 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, 
   a.max_kv_len = (int32_t)std::min<int64_t>(cache->table_stride * cache->page_tokens, INT32_MAX - 64);
   a.idx = idx; a.count = count; a.k = k; a.r = entry_tokens;
   a.first_row = 0; a.T = B; a.B = B; a.n_q = n_q;
-  const AttendPlan p = plan_listed(B, n_q, a.c.n_kv, cache->d_h, k, entry_tokens, window, sinks);
+  const SplitPlan p = plan_listed(B, n_q, a.c.n_kv, cache->d_h, k, entry_tokens, window, sinks, fp8);
   a.window = std::min(window, a.max_kv_len); a.sinks = std::min(sinks, a.max_kv_len);
   if ((s = attend_args(&a, p.bytes, cache->d_h, q, q_stride, softmax_scale, out, out_stride, lse, workspace,
                        workspace_bytes)) != LSA_OK)
     return s;
   if (!plan_fits(p, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows for one call");
-  const hipError_t e = launch_plan(a, p, fp8, cache->d_h, false, -1, INT64_MAX, stream);
+  const hipError_t e = launch_plan(a, p, fp8, cache->d_h, stream);
   return e == hipSuccess ? LSA_OK : hip_fail("lsa_attend_topk launch", e);
 }
 

@@ -139,9 +139,11 @@ def test_no_rows_is_fine(lsa):
 
 
 def test_workspace_sizes(lsa):
-    # a split call holds one fp32 row, its maximum and its sum per split; none where the rows fill the device
+    # decode: one fp32 row block, its maxima and sums per worker and sequence (2 * 32 tiles of 32 keys make 16
+    # workers of four), and a pair of integers per sequence and key head; none where the rows of a prompt fill the device
     size = lsa._attend_ws(2, 8, 2, 64, off(1, 1).ctypes.data, 1000, 0, 0)
-    assert size > 0 and size % (2 * 8 * 66 * 4) == 0
+    assert size == (16 + 2) * 2 * 16 * 66 * 4 + 2 * 2 * 8
+    assert lsa._attend_ws(2, 8, 2, 64, off(1, 1).ctypes.data, 128, 0, 0) == 0  # four tiles: nothing to share
     assert lsa._attend_ws(1, 64, 8, 128, off(20000).ctypes.data, 20000, 0, 0) == 0
     assert lsa._attend_ws(2, 8, 2, 64, off(1, 1).ctypes.data, 1000, 16, 4) <= size
     assert lsa._attend_ws(2, 7, 2, 64, off(1, 1).ctypes.data, 1000, 0, 0) == 0
