@@ -620,8 +620,9 @@ lsa_status lsa_kv_append(const lsa_kv_cache* cache /* host */, int32_t B, const 
  * not matter. Calls that may overlap in time need workspaces of their own; so do
  * two captured graphs that may.
  * Supported: 1 <= B <= 4096; n_q a multiple of n_kv, n_q <= 1024 * n_kv; at most
- * 2^31 - 1 query rows times heads; strides multiples of 8; q and out 16-byte
- * aligned; out must not overlap q.
+ * 2^31 - 1 query rows times heads, and B times the tiles of 32 keys that one
+ * sequence may see; strides multiples of 8; q and out 16-byte aligned; out must
+ * not overlap q.
  * ---------------------------------------------------------------------- */
 size_t lsa_attend_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h,
                                  const int64_t* q_offsets_host /* host [B+1] */, int32_t max_kv_len,

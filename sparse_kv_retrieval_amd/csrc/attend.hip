@@ -113,43 +113,44 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
   const int h = (int)(blockIdx.x % a.c.n_kv);
   const int worker = (int)(blockIdx.x / a.c.n_kv);
 
-  // The worker's share [at, end) of all tiles. 64 row blocks are looked at at a time: `upto` is the sum of
-  // the tiles of row blocks chunk .. chunk + lane, `before` that of the ones before the chunk. A row block with rows
-  // counts at least one tile, so that someone writes the rows that see nothing.
-  int chunk = 0;
-  int64_t upto = 0, before = 0, at = 0, end = 0, share = 0;
+  // The worker's share. The tiles of all row blocks are cut into `workers` equal runs of `share`; where it
+  // takes no more workers, no run crosses into another row block, and each row block's runs are equal instead
+  // (whole: units are runs, otherwise tiles). 64 row blocks are looked at at a time: `upto` is the sum of the units of
+  // row blocks chunk .. chunk + lane, `before` that of the ones before the chunk. A row block with rows counts at
+  // least one tile, so that someone writes the rows that see nothing.
+  int chunk = 0, upto = 0, before = 0, at = 0, end = 0, share = 1, mine_tiles = 0;
+  bool whole = false;
   Seq mine{0, 0, 0, 0};  // row block chunk + lane
   auto look = [&]() {
     const int e = chunk + lane;
-    int64_t n = 0;
+    mine_tiles = 0;
     if (e < a.entries && entry_seq<LISTED>(a, e, &mine)) {
       Rows w;
       set_entry<LISTED>(a, e, mine, M, &w);
-      n = max(w.tiles, 1);
+      mine_tiles = max(w.tiles, 1);
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t x = __shfl_up(n, o);
-      n += lane >= o ? x : 0;
-    }
-    upto = n;
   };
+  auto units = [&]() { return whole ? (mine_tiles + share - 1) / share : mine_tiles; };
   if (a.workers > 0) {
-    int64_t total = 0;
-    for (chunk = 0; chunk < a.entries; chunk += 64) {
+    // several chunks are gone through three times; one is looked at once
+    const bool one = a.entries <= 64;
+    int total = 0, runs = 0;
+    for (; chunk < a.entries; chunk += 64) {
       look();
-      total += __shfl(upto, 63);
+      total += wave_last(wave_scan(mine_tiles));
     }
-    if (a.entries > 64) {
-      chunk = 0;
-      look();
-    } else {
-      chunk = 0;  // looked at already
+    share = max((total - 1) / a.workers + 1, AT_WAVES);
+    if (!one) chunk = 0;
+    for (whole = true; one ? runs == 0 && total > 0 : chunk < a.entries; chunk += 64) {
+      if (!one) look();
+      runs += wave_last(wave_scan(units()));
     }
-    share = max((total + a.workers - 1) / a.workers, (int64_t)AT_WAVES);
-    share = uni((share + AT_WAVES - 1) / AT_WAVES * AT_WAVES);
-    at = worker * share;
-    end = uni(min(at + share, total));
+    whole = runs <= a.workers;
+    chunk = 0;
+    if (!one) look();
+    upto = wave_scan(units());
+    at = whole ? worker : (int)min((int64_t)worker * share, (int64_t)total);
+    end = whole ? min(worker + 1, runs) : (int)min((int64_t)at + share, (int64_t)total);
   }
 
   for (bool again = false;; again = true) {
@@ -157,10 +158,11 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
   int first = 0, count, parts = 1, entry = worker;
   if (a.workers > 0) {
     if (at >= end) return;
-    while (at >= before + uni(__shfl(upto, 63))) {
-      before += uni(__shfl(upto, 63));
+    while (at >= before + wave_last(upto)) {
+      before += wave_last(upto);
       chunk += 64;
       look();
+      upto = wave_scan(units());
     }
     const int which = __ffsll((unsigned long long)__ballot(before + upto > at)) - 1;
     entry = uni(chunk + which);
@@ -168,12 +170,24 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
                    __builtin_amdgcn_readlane(mine.listed, which), __builtin_amdgcn_readlane(mine.row, which)};
     set_entry<LISTED>(a, entry, s, M, &w);
     pin_rows(&w);
-    const int64_t begins = before + uni(__shfl(upto, which)) - max(w.tiles, 1);
-    first = (int)(at - begins);
-    count = (int)min(end - at, (int64_t)max(w.tiles, 1) - first);
-    parts = (int)((begins + max(w.tiles, 1) - 1) / share - begins / share) + 1;
-    at += count;
-    if (first == 0 && tid == 0) {
+    const int last = before + __builtin_amdgcn_readlane(upto, which), n = max(w.tiles, 1);
+    int owner;  // the worker that begins this row block
+    if (whole) {
+      parts = (n + share - 1) / share;
+      owner = last - parts;
+      const int per = (n + parts - 1) / parts;
+      first = (at - owner) * per;
+      count = min(per, n - first);
+      at = end;
+    } else {
+      const int begins = last - n;
+      owner = begins / share;
+      parts = (last - 1) / share - owner + 1;
+      first = at - begins;
+      count = min(end - at, n - first);
+      at += count;
+    }
+    if (owner == worker && tid == 0) {
       a.joins[2 * (entry * a.c.n_kv + h)] = worker;
       a.joins[2 * (entry * a.c.n_kv + h) + 1] = parts > 1 ? parts : 0;
     }

@@ -122,6 +122,18 @@ __device__ __forceinline__ int wave_find(int B, int64_t x, F slot) {
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// Inclusive sum over the lanes of a wave (DPP: within rows of 16, then across them), and its last lane's.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast 15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast 31 into rows 2 and 3
+  return x;
+}
+__device__ __forceinline__ int wave_last(int x) { return __builtin_amdgcn_readlane(x, 63); }
+
 constexpr float ATTEND_LAZY = 8.0f;
 constexpr float ATTEND_LOWEST = -3.402823466e38f;  // running maximum of a row that has seen nothing
 constexpr float LN2 = 0.6931471805599453f;

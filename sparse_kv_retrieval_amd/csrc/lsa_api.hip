@@ -703,6 +703,7 @@ struct SplitPlan {
   int32_t entries = 0;       // row blocks of a key head (0: no launch)
   int32_t per = 1;           // of them, a sequence's
   int32_t workers = 0;       // blocks of a key head that share its tiles; 0: one per row block, none shared
+  int64_t tiles = 0;         // most tiles of a row block
   size_t joins = 0, ml = 0;  // where the joins and the partials' statistics begin in the workspace
   size_t bytes = 0;
 };
@@ -713,6 +714,7 @@ struct SplitPlan {
 // 28.4, 32.9 and 37.1 us): they add partial results and a second round. Row blocks of at most four tiles, one
 // a wave, are not worth sharing. The workspace's size does not depend on the cache's dtype.
 void share_tiles(SplitPlan* p, int32_t n_kv, int32_t d, bool fp8, int64_t tiles) {
+  p->tiles = tiles;
   if (p->entries == 0 || tiles <= 4) return;
   // no worker has fewer than four tiles
   auto workers = [&](int64_t blocks) {
@@ -826,7 +828,8 @@ lsa_status attend_args(AttendArgs* a, size_t bytes, int32_t d, const void* q, in
 }
 
 bool plan_fits(const SplitPlan& p, const AttendArgs& a) {
-  return (int64_t)std::max(p.workers, p.entries) * a.c.n_kv <= kMaxBlocks && a.T * a.n_q <= kMaxBlocks * 4;
+  // the split kernel counts tiles (with at least one a row block) in int32
+  return p.entries * std::max<int64_t>(p.tiles, 1) <= INT32_MAX && (int64_t)std::max(p.workers, p.entries) * a.c.n_kv <= kMaxBlocks && a.T * a.n_q <= kMaxBlocks * 4;
 }
 bool plan_fits(const TilePlan& p, const AttendArgs& a) {
   return !p.used || (p.blocks * p.splits * a.c.n_kv <= kMaxBlocks && a.T * a.n_q <= kMaxBlocks * 4);
@@ -934,7 +937,7 @@ lsa_status lsa_attend(const lsa_kv_cache* cache, int32_t B, const void* q, int64
   const RaggedPlan p = plan_ragged(B, n_q, a.c.n_kv, d, q_offsets_host, max_kv_len, window, sinks, fp8);
   if ((s = attend_args(&a, p.bytes, d, q, q_stride, softmax_scale, out, out_stride, lse, workspace, workspace_bytes)) != LSA_OK)
     return s;
-  if (!plan_fits(p.few, a) || !plan_fits(p.many, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows for one call");
+  if (!plan_fits(p.few, a) || !plan_fits(p.many, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows or keys for one call");
   // the two launches and their joins use the workspace one after the other
   hipError_t e = launch_plan(a, p.few, fp8, d, stream);
   if (e == hipSuccess) e = launch_plan(a, p.many, fp8, d, stream);
@@ -969,7 +972,7 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, 
   if ((s = attend_args(&a, p.bytes, cache->d_h, q, q_stride, softmax_scale, out, out_stride, lse, workspace,
                        workspace_bytes)) != LSA_OK)
     return s;
-  if (!plan_fits(p, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows for one call");
+  if (!plan_fits(p, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows or keys for one call");
   const hipError_t e = launch_plan(a, p, fp8, cache->d_h, stream);
   return e == hipSuccess ? LSA_OK : hip_fail("lsa_attend_topk launch", e);
 }

@@ -162,6 +162,10 @@ ATTEND = [
     ("window_one", "fp8", 4, 1, 128, 16, [(1, 90), (3, 64)], 1, 0),
     ("window_prompt", "bf16", 4, 2, 128, 32, [(190, 190), (65, 300)], 50, 3),
     ("window_prompt_fp8", "fp8", 4, 2, 128, 16, [(190, 190), (65, 300)], 33, 33),
+    ("many_sequences", "fp8", 4, 2, 64, 16, [(i % 3 != 1, 1 + (i * 197) % 900) for i in range(150)], 0, 0),
+    ("many_equal", "bf16", 4, 4, 64, 16, [(1, 400)] * 70, 0, 0),
+    ("one_long_of_many", "fp8", 2, 1, 64, 64, [(1, 3)] * 66 + [(2, 9000), (1, 40)], 0, 0),
+    ("window_many", "bf16", 2, 1, 64, 16, [(1, 300)] * 65, 200, 7),
     ("window_longer", "bf16", 4, 2, 64, 16, [(20, 60), (1, 9)], 500, 5),
 ]
 
@@ -292,6 +296,8 @@ TOPK = [
     ("mqa", "bf16", 64, 1, 128, 64, [1000, 700], 200, 2, 128, 4),
     ("mqa_fp8", "fp8", 40, 1, 64, 128, [1000, 700], 300, 1, 1, 0),
     ("many", "fp8", 16, 2, 128, 64, [3001, 2000, 64, 0], 700, 1, 100, 4),
+    ("many_sequences", "fp8", 16, 8, 64, 16, [1 + (i * 131) % 500 for i in range(90)], 150, 1, 20, 2),
+    ("heads_beyond_a_block", "bf16", 100, 1, 64, 16, [300, 77, 0], 120, 1, 20, 2),
     ("window_over_all", "bf16", 4, 1, 64, 16, [50], 20, 1, 1000, 1000),
 ]
 
