@@ -15,6 +15,8 @@
 // e4m3 codes are widened on the way to LDS, once per block. The power-of-two part of the page's scale
 // goes in there, exactly; what is left of a scale that is no power of two multiplies scores and
 // probabilities instead, on a path that caches written by lsa_kv_append never take.
+#include <type_traits>
+
 #include "kv.hpp"
 
 namespace lsa {
@@ -47,6 +49,9 @@ __device__ __forceinline__ u32x2 widen4(uint32_t four, float pow2) {
   r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, pow2, true));
   return r;
 }
+
+// The lowest n bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 // A scale as a power of two within bf16's middle range, times what is left (1, or beyond that range).
 __device__ __forceinline__ void split_scale(float s, float* pow2, float* rest) {
@@ -98,14 +103,14 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   // The 16 tokens of tile i that this wave fetches: the first one's position, or -1 where no row sees
   // any of them, and the page that holds them. The page is asked for one tile ahead of its use, so
   // that reading it never waits for the tile's own loads.
-  auto tokens = [&](int i) -> int {
+  auto tokens = [&](int i) __attribute__((always_inline)) -> int {
     if (i >= count) return -1;
     const int t = w.near.tile(first + i) * TL_N + sub * 16;
     return t > w.p_hi || (t + 15 <= w.w_lo && t >= a.sinks) ? -1 : t;
   };
   const int32_t* table = a.c.table + w.b * a.c.table_stride;
-  auto page_of = [&](int t) -> int32_t { return table[max(t, 0) >> a.c.pt_log2]; };
-  auto place = [&](int t, int32_t page) -> int64_t {
+  auto page_of = [&](int t) __attribute__((always_inline)) -> int32_t { return table[max(t, 0) >> a.c.pt_log2]; };
+  auto place = [&](int t, int32_t page) __attribute__((always_inline)) -> int64_t {
     page = uni(page);
     if (t < 0 || page < 0 || page >= a.c.n_pages) return -1;
     return (((int64_t)page * a.c.n_kv + kv) << a.c.pt_log2) + (t & ((1 << a.c.pt_log2) - 1));
@@ -115,17 +120,17 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   float in_scale = 1.f;
   const char* src = is_v ? a.c.v : a.c.k;
   const float* src_scale = is_v ? a.c.v_scale : a.c.k_scale;
-  auto fetch = [&](int64_t at) {
+  auto fetch = [&](int64_t at) __attribute__((always_inline)) {
     const int64_t row0 = at < 0 ? 0 : at;  // nothing there: any row, its values are cleared below
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) in[i] = *(const u32x4*)(src + row0 * (SRC * 16) + (uint32_t)((i * 64 + lane) * 16));
     if constexpr (FP8) in_scale = src_scale[row0 >> a.c.pt_log2];
   };
-  auto whole_tile = [&](int t0) { return t0 + TL_N - 1 <= w.p_lo && (t0 > w.w_hi || t0 + TL_N - 1 < a.sinks); };
+  auto whole_tile = [&](int t0) __attribute__((always_inline)) { return t0 + TL_N - 1 <= w.p_lo && (t0 > w.w_hi || t0 + TL_N - 1 < a.sinks); };
   // Values that no row of the block sees become 0: a probability of 0 would not clear an infinity. (Keys
   // may stay, their scores are masked.) Where some rows see a value and others do not, one that is not
   // finite becomes 0 as well, and the tile is marked: rescue() brings it to the rows that see it.
-  auto store = [&](int buf, int i, int64_t at) {
+  auto store = [&](int buf, int i, int64_t at) __attribute__((always_inline)) {
     const int t0 = w.near.tile(first + i) * TL_N + sub * 16;
     if (is_v) {
       uint32_t odd = 0;
@@ -187,9 +192,9 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   const int k_at = col * ROWB + (k_swizzle<CPR>(col) ^ h) * 16;
   const int vrow = 4 * h + (lane & 15) / 4;
   const int v_at = vrow * ROWB + ((2 * ((lane >> 4) & 1) + (lane & 3) / 2) ^ v_swizzle<CPR>(vrow)) * 16 + (lane & 1) * 8;
-  auto k_operand = [&](int buf, int u, int x) { return *(const u32x4*)(s_k[buf] + u * 32 * ROWB + (k_at ^ (32 * x))); };
+  auto k_operand = [&](int buf, int u, int x) __attribute__((always_inline)) { return *(const u32x4*)(s_k[buf] + u * 32 * ROWB + (k_at ^ (32 * x))); };
   // operand e of key step x: dimensions 32 e + lane % 32, keys 16 x + 8 z + 4 h + 0..3 for z = 0, 1
-  auto v_operand = [&](int buf, int u, int x, int e) {
+  auto v_operand = [&](int buf, int u, int x, int e) __attribute__((always_inline)) {
     typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
     u32x4 v;
 #pragma unroll
@@ -201,17 +206,20 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     }
     return v;
   };
-  auto seen = [&](int t) { return t <= p_row && (t > w_row || t < a.sinks); };
+  auto seen = [&](int t) __attribute__((always_inline)) { return t <= p_row && (t > w_row || t < a.sinks); };
 
   // Scores of 32 keys before their softmax: register i of a lane is key 8 (i / 4) + 4 h + i % 4. Applies the mask and
   // raises the maximum; returns whether it rose for some row of the wave, and then what to scale by in `fall`.
-  auto settle = [&](int buf, int t0, int u, bool whole, bool here0, bool here1, f32x16& s, float& fall) -> bool {
+  auto settle = [&](int buf, int t0, int u, bool whole, bool here0, bool here1, f32x16& s, float& fall) __attribute__((always_inline)) -> bool {
     if (!whole) {
-      const int base = t0 + 32 * u + 4 * h, hi = p_row - base, lo = w_row - base, few = a.sinks - base;
+      // a bit for each of the 32 keys from the lane's first on: x <= hi, and x > lo or x < few
+      const int base = t0 + 32 * u + 4 * h;
+      const uint32_t in = low_bits(p_row - base + 1) & (~low_bits(w_row - base + 1) | low_bits(a.sinks - base)) &
+                          ((here0 ? 0x0000FFFFu : 0u) | (here1 ? 0xFFFF0000u : 0u));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int x = 8 * (i / 4) + i % 4;  // key base + x
-        s[i] = (i < 8 ? here0 : here1) && x <= hi && (x > lo || x < few) ? s[i] : -__builtin_inff();
+        const uint32_t see = __builtin_amdgcn_sbfe((int)in, 8 * (i / 4) + i % 4, 1);  // all ones or none
+        s[i] = __uint_as_float((__float_as_uint(s[i]) & see) | (0xFF800000u & ~see));
       }
     }
     float top = s[0], top1 = s[8];
@@ -236,7 +244,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   // next, and a share of the exponentials. What is left of V's scale rides in the exponent, and leaves
   // the sum again by its reciprocal.
   bf16x8 p[2] = {as_bf16x8((u32x4){0, 0, 0, 0}), as_bf16x8((u32x4){0, 0, 0, 0})};
-  auto step = [&](int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next, int old_buf, int old_u) {
+  auto step = [&](int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next, int old_buf, int old_u) __attribute__((always_inline)) {
     constexpr int E = 16 / KS;  // exponentials of a group
     static_assert(KS == 2 * DT, "as many key steps as value operands");
     float c2[2] = {c, c}, add[2] = {-m, -m}, inv[2] = {1.f, 1.f};
@@ -283,12 +291,12 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
 #pragma unroll
     for (int x = 0; x < 2; ++x) p[x] = as_bf16x8((u32x4){packed[4 * x], packed[4 * x + 1], packed[4 * x + 2], packed[4 * x + 3]});
   };
-  auto scale_out = [&](float f) {
+  auto scale_out = [&](float f) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < DT; ++i) acc[i] *= f;
   };
   // Values that are not finite, taken out of a tile on its way to LDS, reach the rows that see them.
-  auto rescue = [&](int t0) {
+  auto rescue = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll 1
     for (int j = 0; j < TL_N; ++j) {
       const int t = t0 + j;
@@ -316,7 +324,6 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   page = page_of(t_next);
   f32x16 s0 = (f32x16)(0.f), s1;
   float fall = 1.f;
-  int buf = 0, old = TL_BUFS - 1;
   if (count > 0) {
     fetch(at);
     store(0, 0, at);
@@ -325,13 +332,14 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     page = page_of(t_next);
     fetch(at);  // beyond the run: row 0, not used
     // the first step's second product is of no probabilities and these values
-    for (int i = tid; i < TL_N * ROWB / 16; i += TL_THREADS) *(u32x4*)(s_v[old] + 16 * i) = (u32x4){0, 0, 0, 0};
+    for (int i = tid; i < TL_N * ROWB / 16; i += TL_THREADS) *(u32x4*)(s_v[TL_BUFS - 1] + 16 * i) = (u32x4){0, 0, 0, 0};
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < KS; ++x) s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(k_operand(0, 0, x)), q[x], s0, 0, 0, 0);
   }
-  for (int i = 0; i < count; ++i) {
-    const int nb = buf + 1 == TL_BUFS ? 0 : buf + 1;
+  // tile i, in a buffer known when compiled: its operands' LDS addresses are constants beside the lane's
+  auto tile = [&](int i, auto which) __attribute__((always_inline)) {
+    constexpr int buf = decltype(which)::value, nb = (buf + 1) % TL_BUFS, old = (buf + TL_BUFS - 1) % TL_BUFS;
     const int t0 = w.near.tile(first + i) * TL_N;
     const u32x4 here = *(const u32x4*)s_here[buf];
     const bool h0 = uni((int)here[0]), h1 = uni((int)here[1]), h2 = uni((int)here[2]), h3 = uni((int)here[3]);
@@ -348,7 +356,10 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       page = page_of(t_next);
       fetch(at);
     }
-    __syncthreads();
+    // as __syncthreads(), but the loads of the tile after next stay in flight: only LDS is shared
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
     rose = settle(buf, t0, 1, whole, h2, h3, s1, fall);
     // after the last tile the next scores are those of an old buffer, and not used
     step(buf, 1, s1, nb, 0, s0, buf, 0);
@@ -357,13 +368,26 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       const u32x4 odd = *(const u32x4*)s_odd[buf];
       if (uni((int)(odd[0] | odd[1] | odd[2] | odd[3]))) rescue(t0);
     }
-    old = buf;
-    buf = nb;
-  }
-  if (count > 0) {
+  };
+  auto last = [&](auto which) __attribute__((always_inline)) {
+    constexpr int buf = decltype(which)::value;
 #pragma unroll
     for (int x = 0; x < KS; ++x)
-      acc[x % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(v_operand(old, 1, x / DT, x % DT)), p[x / DT], acc[x % DT], 0, 0, 0);
+      acc[x % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(v_operand(buf, 1, x / DT, x % DT)), p[x / DT], acc[x % DT], 0, 0, 0);
+  };
+  static_assert(TL_BUFS == 3, "the loop goes through the buffers");
+  typedef std::integral_constant<int, 0> B0;
+  typedef std::integral_constant<int, 1> B1;
+  typedef std::integral_constant<int, 2> B2;
+  for (int i = 0; i < count; i += 3) {
+    tile(i, B0{});
+    if (i + 1 < count) tile(i + 1, B1{});
+    if (i + 2 < count) tile(i + 2, B2{});
+  }
+  if (count > 0) {
+    if (count % 3 == 1) last(B0{});
+    else if (count % 3 == 2) last(B1{});
+    else last(B2{});
   }
 
   const float sum = sum_halves(l);
