@@ -832,7 +832,8 @@ bool plan_fits(const SplitPlan& p, const AttendArgs& a) {
   return p.entries * std::max<int64_t>(p.tiles, 1) <= INT32_MAX && (int64_t)std::max(p.workers, p.entries) * a.c.n_kv <= kMaxBlocks && a.T * a.n_q <= kMaxBlocks * 4;
 }
 bool plan_fits(const TilePlan& p, const AttendArgs& a) {
-  return !p.used || (p.blocks * p.splits * a.c.n_kv <= kMaxBlocks && a.T * a.n_q <= kMaxBlocks * 4);
+  // its blocks have 512 threads
+  return !p.used || (p.blocks * p.splits * a.c.n_kv <= kMaxBlocks / 2 && a.T * a.n_q <= kMaxBlocks * 4);
 }
 
 hipError_t launch_plan(AttendArgs a, const SplitPlan& p, bool fp8, int32_t d, hipStream_t stream) {

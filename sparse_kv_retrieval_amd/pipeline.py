@@ -21,6 +21,11 @@ After a trigger, alloc_steps() / pack_subset_keys() / step() run the decode step
 layer's union rows of keys are packed once (lsa_gather), and every step projects its own
 native query and calls lsa_topk_step over them.
 
+With alloc_attention(), the steps go on to the core attention of every layer over what was selected:
+append_prompt() stores the prompt's keys and values in a paged cache, and attend_step() stores a step's
+own (lsa_kv_append) and attends over the step's top-k entries, the sliding window and the first tokens
+(lsa_attend_topk).
+
 This module only wires buffers. All arithmetic happens in the HIP kernels.
 """
 from __future__ import annotations
@@ -326,6 +331,81 @@ class Pipeline:
         lsa.topk_step(tl, B=w.B, key_offsets=self.key_off, key_offsets_host=self.key_off_h, idx=self.idx,
                       count=self.count, n_h=w.n_h, d_h=w.d_h, key_dtype=w.key_dtype, k=w.k,
                       topk_count_out=self.step_count, workspace=self.workspace, stream=stream)
+
+    # ------------------------------------------------------------- core attention of the decode steps
+    def alloc_attention(self, *, n_q, n_kv, d_h=128, dtype="bf16", page_tokens=64, entry_tokens=4, window=128, sinks=4,
+                        max_steps=64, rot_dim=None, theta=10000.0):
+        """A paged cache per layer for every sequence's N_b * entry_tokens prompt tokens and max_steps more, and the
+        buffers of attend_step. `window` is at least the steps between triggers, so that tokens newer than the
+        last selection are seen."""
+        w, L, B = self.w, self.w.L, self.w.B
+        bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+        self.entry_tokens, self.window, self.sinks, self.n_q, self.n_kv = entry_tokens, window, sinks, n_q, n_kv
+        self.prompt_len = np.diff(self.key_off_h) * entry_tokens
+        pages = -(-(self.prompt_len + max_steps) // page_tokens)
+        self.capacity = self.prompt_len + max_steps
+        first = np.concatenate([[0], np.cumsum(pages)])
+        table = np.full((B, int(pages.max())), -1, np.int32)
+        for b in range(B):
+            table[b, :pages[b]] = np.arange(first[b], first[b + 1])
+        self.page_table = _dev(table, self.device)
+        self.len_h = np.zeros(B, np.int64)
+        self.kv_len = torch.zeros(B, dtype=i32, device=self.device)
+        shape = (int(first[-1]), n_kv, page_tokens, d_h)
+        self.caches = []
+        for _ in range(L):
+            if dtype == "fp8":
+                kv = [self._out(shape, torch.uint8).view(torch.float8_e4m3fn) for _ in range(2)]
+                scale = [self._out(shape[:2], f32) for _ in range(2)]
+            else:
+                kv, scale = [self._out(shape, bf16) for _ in range(2)], (None, None)
+            self.caches.append(lsa.KvCache(k=kv[0], v=kv[1], k_scale=scale[0], v_scale=scale[1],
+                                           page_table=self.page_table, kv_len=self.kv_len))
+        rot = d_h if rot_dim is None else rot_dim
+        self.inv_freq = _dev((theta ** (-np.arange(rot // 2) * 2.0 / rot)).astype(np.float32), self.device)
+        self.prompt_off_h = np.concatenate([[0], np.cumsum(self.prompt_len)]).astype(np.int64)
+        self.prompt_off = _dev(self.prompt_off_h, self.device)
+        self.one_off_h = np.arange(B + 1, dtype=np.int64)
+        self.one_off = _dev(self.one_off_h, self.device)
+        self.q_rot = [self._out((B, n_q, d_h), bf16) for _ in range(L)]
+        self.attn_out = [self._out((B, n_q, d_h), bf16) for _ in range(L)]
+        self.attn_lse = [self._out((B, n_q), f32) for _ in range(L)]
+        size = lsa.attend_topk_workspace_size(self.caches[0], n_q=n_q, k=w.k, entry_tokens=entry_tokens, window=window,
+                                              sinks=sinks)
+        self.attn_workspace = self._out((max(size, 16),), torch.uint8)
+
+    def _grow(self, by, stream):
+        """Every sequence gets `by` tokens more, in the order of `stream`."""
+        if (self.len_h + by > self.capacity).any():
+            raise ValueError("the cache is full: alloc_attention(max_steps=...) bounds the steps")
+        self.len_h += by
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        with torch.cuda.stream(stream):  # None: the current one
+            self.kv_len.copy_(torch.from_numpy(self.len_h.astype(np.int32)))
+
+    def append_prompt(self, k, v, stream=None):
+        """Once: the prompt's keys and values, [layer] -> [sum of N_b * entry_tokens, n_kv, d_h] bfloat16, before the
+        rotation, sequence after sequence."""
+        self._grow(self.prompt_len, stream)
+        for l in range(self.w.L):
+            lsa.kv_append(self.caches[l], k[l], v[l], new_offsets=self.prompt_off, new_offsets_host=self.prompt_off_h,
+                          inv_freq=self.inv_freq, stream=stream)
+
+    def attend_step(self, qkv, stream=None):
+        """The step's core attention, after step(): qkv [layer] -> [B, n_q + 2 n_kv, d_h] bfloat16, the step's queries, keys
+        and values before the rotation. Writes attn_out and attn_lse."""
+        self._grow(1, stream)
+        n_q, n_kv = self.n_q, self.n_kv
+        for l in range(self.w.L):
+            x = qkv[l]
+            lsa.kv_append(self.caches[l], x[:, n_q:n_q + n_kv], x[:, n_q + n_kv:], new_offsets=self.one_off,
+                          new_offsets_host=self.one_off_h, q=x[:, :n_q], q_out=self.q_rot[l], inv_freq=self.inv_freq,
+                          stream=stream)
+            lsa.attend_topk(self.caches[l], self.q_rot[l], idx=self.step_idx[l], count=self.step_count[l],
+                            entry_tokens=self.entry_tokens, scale=self.q_rot[l].shape[2] ** -0.5, window=self.window,
+                            sinks=self.sinks, out=self.attn_out[l], lse=self.attn_lse[l], workspace=self.attn_workspace,
+                            stream=stream)
 
     def load(self, stream=None):
         """The load step: from the host pool when there is one, else from HBM."""

@@ -162,6 +162,9 @@ ATTEND = [
     ("window_one", "fp8", 4, 1, 128, 16, [(1, 90), (3, 64)], 1, 0),
     ("window_prompt", "bf16", 4, 2, 128, 32, [(190, 190), (65, 300)], 50, 3),
     ("window_prompt_fp8", "fp8", 4, 2, 128, 16, [(190, 190), (65, 300)], 33, 33),
+    ("many_chunks", "bf16", 8, 1, 64, 16, [(9 + i % 3 if i % 4 else 0, 20 + i % 60) for i in range(70)], 0, 0),
+    ("group_beyond_a_block", "fp8", 300, 1, 64, 16, [(2, 70), (1, 33)], 0, 0),
+    ("one_token_many_heads", "bf16", 100, 1, 128, 64, [(1, 500), (1, 1)], 0, 0),
     ("many_sequences", "fp8", 4, 2, 64, 16, [(i % 3 != 1, 1 + (i * 197) % 900) for i in range(150)], 0, 0),
     ("many_equal", "bf16", 4, 4, 64, 16, [(1, 400)] * 70, 0, 0),
     ("one_long_of_many", "fp8", 2, 1, 64, 64, [(1, 3)] * 66 + [(2, 9000), (1, 40)], 0, 0),
@@ -271,8 +274,9 @@ def test_attend_length_beyond_the_bound(torch, lsa):
     assert bool((out[1] == 0).all()) and bool(torch.isneginf(lse[1]).all())
 
 
+@pytest.mark.parametrize("n", [2, 200])
 @pytest.mark.parametrize("scale", [0.0, 30.0, -1.0])
-def test_attend_scores_far_apart(torch, lsa, scale):
+def test_attend_scores_far_apart(torch, lsa, scale, n):
     # scores that grow along the keys by far more than the lazy maximum's slack, and the reverse
     say(f"[attend] far scores {scale}")
     s = Setup(torch, lsa, [333], dtype="bf16", n_kv=1, d=64, pt=32, seed=5)
@@ -280,11 +284,89 @@ def test_attend_scores_far_apart(torch, lsa, scale):
     for p in range(333):
         s.parts["k"][int(s.table[0, p // 32]), 0, p % 32] = ramp[p].to(torch.bfloat16)
     s.decode()
-    q = torch.ones((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.ones((n, 2, 64), dtype=torch.bfloat16, device="cuda")
     q[:, 1] = -1
-    out, lse = run_attend(torch, lsa, s, q, offsets([2]), scale=scale)
+    out, lse = run_attend(torch, lsa, s, q, offsets([n]), scale=scale)
     torch.cuda.synchronize()
-    check_rows(s, q, out, lse, [(0, 0, 331), (1, 0, 332)], scale, n_q=2)
+    check_rows(s, q, out, lse, [(r, 0, 333 - n + r) for r in sorted({0, 1, n // 2, n - 1})], scale, n_q=2)
+
+
+@pytest.mark.parametrize("amp", [1.37, 2.0 ** -110, 3 * 2.0 ** 90])
+@pytest.mark.parametrize("n", [1, 90])
+def test_attend_scales_of_any_size(torch, lsa, amp, n):
+    # page scales that are no power of two, and far from 1 (values only: scores have to stay finite)
+    say(f"[attend] scales {amp} rows {n}")
+    s = Setup(torch, lsa, [200, 130], dtype="fp8", n_kv=2, d=64, pt=16, seed=6)
+    rest = torch.from_numpy(s.g.uniform(0.6, 1.9, s.scales["k"].shape).astype(np.float32)).cuda()
+    s.parts["k_scale"] *= rest
+    s.parts["v_scale"] *= rest.flip(0) * amp
+    s.decode()
+    off = offsets([n, n])
+    q = bf16(torch, s.g, (2 * n, 4, 64))
+    out, lse = run_attend(torch, lsa, s, q, off)
+    torch.cuda.synchronize()
+    rows = [(b * n + i, b, s.totals[b] - n + i) for b in range(2) for i in sorted({0, n // 2, n - 1})]
+    check_rows(s, q, out, lse, rows, 64 ** -0.5, n_q=4)
+
+
+def test_cache_beyond_32_bit_offsets(torch, lsa):
+    """The same contents in a small cache and in the last pages of one of 4.7 GB a side give the same bits."""
+    say("[kv] long cache")
+    n_kv, d, pt, totals = 2, 128, 64, [300, 90]
+    inv = torch.from_numpy((10000.0 ** (-np.arange(d // 2) * 2.0 / d)).astype(np.float32)).cuda()
+    for news in ([1, 1], [70, 40]):
+        s = Setup(torch, lsa, totals, dtype="bf16", n_kv=n_kv, d=d, pt=pt, seed=15)
+        n = s.parts["k"].shape[0]
+        big = {x: torch.empty((145_000, n_kv, pt, d), dtype=torch.bfloat16, device="cuda") for x in ("k", "v")}
+        assert big["k"].nbytes > 1 << 32
+        shift = 145_000 - n
+        for x in big:
+            big[x][shift:] = s.parts[x]
+        table = s.table_dev.clone()
+        table[table >= 0] += shift
+        far = lsa.KvCache(k=big["k"], v=big["v"], page_table=table, kv_len=s.kv_len)
+        off = offsets(news)
+        off_dev = torch.from_numpy(off).cuda()
+        T = int(off[-1])
+        qkv = bf16(torch, s.g, (T, 8 + 2 * n_kv, d))
+        idx = torch.arange(0, 80, 2, dtype=torch.int32, device="cuda").repeat(2, 1).contiguous()
+        count = torch.tensor([40, 20], dtype=torch.int32, device="cuda")
+        got = []
+        for cache in (s.cache, far):
+            q = torch.empty((T, 8, d), dtype=torch.bfloat16, device="cuda")
+            lsa.kv_append(cache, qkv[:, 8:8 + n_kv], qkv[:, 8 + n_kv:], new_offsets=off_dev, new_offsets_host=off,
+                          q=qkv[:, :8], q_out=q, inv_freq=inv)
+            size = max(lsa.attend_workspace_size(cache, n_q=8, q_offsets_host=off, max_kv_len=300),
+                       lsa.attend_topk_workspace_size(cache, n_q=8, k=40, entry_tokens=2, window=5))
+            ws = torch.empty(max(size, 16), dtype=torch.uint8, device="cuda")
+            out, top = torch.empty_like(q), torch.empty_like(q[:2])
+            lsa.attend(cache, q, q_offsets=off_dev, q_offsets_host=off, max_kv_len=300, out=out, scale=0.1, workspace=ws)
+            lsa.attend_topk(cache, q[:2], idx=idx, count=count, out=top, scale=0.1, entry_tokens=2, window=5, workspace=ws)
+            torch.cuda.synchronize()
+            got.append((q, out, top))
+        for a, b in zip(*got):
+            assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+        for x in big:
+            assert torch.equal(big[x][shift:].view(torch.int16), s.parts[x].view(torch.int16))
+        del big, far
+        torch.cuda.empty_cache()
+
+
+def test_attend_without_lse_and_on_a_given_stream(torch, lsa):
+    say("[attend] no lse, own stream")
+    s = Setup(torch, lsa, [500, 700], dtype="fp8", n_kv=2, d=64, pt=16, seed=16)
+    off = offsets([1, 80])
+    q = bf16(torch, s.g, (81, 4, 64))
+    want, _ = run_attend(torch, lsa, s, q, off)
+    out = torch.zeros_like(q)
+    ws = torch.empty(lsa.attend_workspace_size(s.cache, n_q=4, q_offsets_host=off, max_kv_len=700), dtype=torch.uint8, device="cuda")
+    off_dev = torch.from_numpy(off).cuda()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    lsa.attend(s.cache, q, q_offsets=off_dev, q_offsets_host=off.tolist(), max_kv_len=700, out=out, scale=0.125, workspace=ws,
+               stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
 
 
 # (name, dtype, n_q, n_kv, d, page, lens, k, entry, window, sinks)
@@ -345,6 +427,7 @@ APPEND = [
     ("prompt_fp8", "fp8", 16, 2, 128, 128, [(300, 300), (129, 200)], "halves", 96),
     ("prompt_fp8_d64", "fp8", 3, 3, 64, 128, [(300, 333), (1, 128)], "halves", 16),
     ("plain_fp8", "fp8", 0, 2, 64, 16, [(30, 47), (5, 5)], None, 0),
+    ("many_sequences", "fp8", 3, 1, 64, 16, [(i % 4, 5 + (i * 37) % 200) for i in range(140)], "pairs", 32),
     ("more_new_than_cached", "fp8", 2, 1, 64, 16, [(20, 13), (3, 0), (2, 1)], "halves", 64),
 ]
 
