@@ -243,25 +243,24 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
   auto resolve = [&](int tile0, int n) {
     for (int i = tid; i < n * PLACES; i += AT_THREADS) {
       const int tile = tile0 + i / PLACES;
-      int64_t tok = -1;
+      int tok = -1;
       if constexpr (LISTED) {
         if (tile < w.near.n) {
-          tok = (int64_t)w.near.tile(tile) * 32 + i % 32;
+          tok = w.near.tile(tile) * 32 + i % 32;
           const bool seen = tok <= w.p_hi && ((a.window > 0 && tok > w.w_hi) || tok < a.sinks);
           tok = seen ? tok : -1;
         } else {
-          const int64_t at = (int64_t)(tile - w.near.n) * 32 + i % 32;
-          const int64_t e = at / a.r;
-          if (e < min(a.count[w.b], a.k)) {
+          const uint32_t at = (uint32_t)(tile - w.near.n) * 32 + i % 32, e = a.r == 1 ? at : at / (uint32_t)a.r;
+          if ((int)e < min(a.count[w.b], a.k)) {
             const int32_t* list = a.idx + (int64_t)w.b * a.k;
             const int32_t entry = list[e];
-            tok = (int64_t)entry * a.r + at % a.r;
-            const bool near = (a.window > 0 && tok > w.w_hi) || tok < a.sinks;
-            if (entry < 0 || tok > w.p_hi || near || (e > 0 && list[e - 1] == entry)) tok = -1;
+            const int64_t far = (int64_t)entry * a.r + (at - e * a.r);
+            const bool near = (a.window > 0 && far > w.w_hi) || far < a.sinks;
+            if (entry >= 0 && far <= w.p_hi && !near && !(e > 0 && list[e - 1] == entry)) tok = (int)far;
           }
         }
       } else {
-        tok = (int64_t)w.near.tile(tile) * 32 + (i % 2) * 16;
+        tok = w.near.tile(tile) * 32 + (i % 2) * 16;
         // no row sees any of the 16: the page may not be the sequence's any more
         if (tok > w.p_hi || (tok + 15 <= w.w_lo && tok >= a.sinks)) tok = -1;
       }
@@ -601,7 +600,7 @@ __global__ __launch_bounds__(AT_THREADS) void tile_join_kernel(const AttendArgs 
   const int64_t n_tok = a.off[w.b + 1] - w.t0;
   if (!of_class(a, n_tok)) return;
   const int64_t row = (t + a.first_row - w.t0) * a.G + head % a.G;
-  set_block<false>(a, seq_of<false>(a, w.b, w.t0, n_tok), (int32_t)(row / ATTEND_TILE_ROWS), ATTEND_TILE_ROWS, &w);
+  set_block(a, seq_of<false>(a, w.b, w.t0, n_tok), (int32_t)(row / ATTEND_TILE_ROWS), &w);
   const int parts = (w.tiles + a.run - 1) / a.run;
   if (parts > 1) join_row<D>(a, id, a.T * a.n_q, parts, t + a.first_row, head);
 }

@@ -82,7 +82,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   const int split = (int)((id / a.c.n_kv) % a.splits);
   // the last row blocks see the most keys: they go first
   Rows w;
-  if (!find_rows(a, a.blocks - 1 - id / ((int64_t)a.c.n_kv * a.splits), TL_M, &w)) return;
+  if (!find_rows(a, a.blocks - 1 - id / ((int64_t)a.c.n_kv * a.splits), &w)) return;
   const int parts = (w.tiles + a.run - 1) / a.run;
   if (split > 0 && split >= parts) return;
   const int first = split * a.run, count = min(a.run, w.tiles - first);

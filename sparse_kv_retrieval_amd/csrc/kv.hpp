@@ -55,7 +55,6 @@ struct AttendArgs {
   int64_t first_row, T;
   float scale_log2;       // softmax scale * log2(e)
   int32_t B, n_q, G, max_kv_len, window, sinks, k, r;
-  int32_t tile;           // keys per tile
   int64_t rows_above, rows_to;
   float* part_o;          // partial results of row blocks whose keys are split
   float* part_ml;         // and their running maximum (base 2) and sum
@@ -78,22 +77,24 @@ struct TileRange {
   __device__ __forceinline__ int32_t tile(int32_t i) const { return i < n_first ? i : first_b + (i - n_first); }
 };
 
-__host__ __device__ __forceinline__ TileRange tile_range(int32_t p_lo, int32_t p_hi, int32_t window, int32_t sinks,
-                                                         int32_t tile) {
+template <int tile>
+__device__ __forceinline__ TileRange tile_range(int32_t p_lo, int32_t p_hi, int32_t window, int32_t sinks) {
   TileRange t{0, 0, 0};
   if (p_hi < 0) return t;
-  const int32_t end = p_hi / tile + 1;
+  const int32_t end = (int32_t)((uint32_t)p_hi / tile) + 1;
   if (window > 0) {
-    const int32_t s = sinks / tile + (sinks % tile != 0);
+    const int32_t s = (int32_t)((uint32_t)sinks / tile) + (sinks % tile != 0);
     t.n_first = s < end ? s : end;
     const int32_t lo = p_lo - window + 1;  // p_lo >= -2^31 + window fits: both are at most 2^31 - 1
-    t.first_b = lo > 0 ? lo / tile : 0;
+    t.first_b = lo > 0 ? (int32_t)((uint32_t)lo / tile) : 0;
     if (t.first_b < t.n_first) t.first_b = t.n_first;
   }
   t.n = t.n_first + (end > t.first_b ? end - t.first_b : 0);
   return t;
 }
 
+constexpr int ATTEND_TILE_ROWS = 256;       // rows of a block of the tile kernel
+constexpr int ATTEND_TILE_KEYS = 64;        // keys of its tiles
 constexpr int ATTEND_RESOLVED = 64;         // tiles whose places a block of the split kernel holds at once
 constexpr int ATTEND_RESOLVED_LISTED = 16;  // the same over listed keys, each with a place of its own
 
@@ -102,8 +103,6 @@ hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_til
 hipError_t launch_attend_split_join(const AttendArgs& a, int d, int rows, bool listed, hipStream_t s);
 hipError_t launch_attend_tile_join(const AttendArgs& a, int d, hipStream_t s);
 hipError_t launch_attend_tile(const AttendArgs& a, bool fp8, int d, hipStream_t s);
-constexpr int ATTEND_TILE_ROWS = 256;  // rows of a block of attend_tile_kernel
-constexpr int ATTEND_TILE_KEYS = 64;   // keys of its tiles
 
 // Largest b in [0, B) with slot(b) <= x, for slot strictly increasing and slot(0) <= x: the lanes
 // of a wave try 64 places at a time.
@@ -172,28 +171,25 @@ __device__ __forceinline__ Seq seq_of(const AttendArgs& a, int b, int64_t row, i
           (int32_t)(row - a.first_row)};
 }
 
-template <bool LISTED>
-__device__ __forceinline__ void set_block(const AttendArgs& a, Seq s, int32_t j, int M, Rows* w) {
-  w->r0 = j * M;
-  w->n = min(M, s.n_tok * a.G - j * M);
+// Rows r0 .. r0 + n - 1 of a sequence, whose first and last belong to new tokens `lo` and `hi`, and the tiles of TILE keys
+// that they see by position.
+template <int TILE>
+__device__ __forceinline__ void set_rows(const AttendArgs& a, Seq s, int32_t r0, int32_t n, int32_t lo, int32_t hi, Rows* w) {
+  w->r0 = r0;
+  w->n = n;
   w->p0 = s.len - s.n_tok;
-  w->p_lo = w->p0 + w->r0 / a.G;
-  w->p_hi = w->p0 + (w->r0 + w->n - 1) / a.G;
+  w->p_lo = w->p0 + lo;
+  w->p_hi = w->p0 + hi;
   w->w_lo = window_start(a, w->p_lo);
   w->w_hi = window_start(a, w->p_hi);
-  if constexpr (LISTED) {
-    if (a.window > 0) {
-      w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks, a.tile);
-    } else {
-      const int32_t end = w->p_hi < 0 ? 0 : w->p_hi / 32 + 1, first = a.sinks / 32 + (a.sinks % 32 != 0);
-      w->near.n_first = w->near.n = min(first, end);
-      w->near.first_b = 0;
-    }
-    w->tiles = w->p_hi < 0 ? 0 : w->near.n + (int32_t)(((int64_t)s.listed * a.r + 31) / 32);
-  } else {
-    w->near = tile_range(w->p_lo, w->p_hi, a.window, a.sinks, a.tile);
-    w->tiles = w->near.n;
-  }
+  w->near = tile_range<TILE>(w->p_lo, w->p_hi, a.window, a.sinks);
+  w->tiles = w->near.n;
+}
+
+// Tile kernel: row block j of a sequence.
+__device__ __forceinline__ void set_block(const AttendArgs& a, Seq s, int32_t j, Rows* w) {
+  const int32_t r0 = j * ATTEND_TILE_ROWS, n = min(ATTEND_TILE_ROWS, s.n_tok * a.G - r0);
+  set_rows<ATTEND_TILE_KEYS>(a, s, r0, n, r0 / a.G, (r0 + n - 1) / a.G, w);
 }
 
 // The fields that a block agrees on, in scalar registers.
@@ -204,13 +200,14 @@ __device__ __forceinline__ void pin_rows(Rows* w) {
 }
 
 // Tile kernel: the row block of a slot (see AttendArgs::blocks), if it has rows.
-__device__ __forceinline__ bool find_rows(const AttendArgs& a, int64_t block, int M, Rows* w) {
+__device__ __forceinline__ bool find_rows(const AttendArgs& a, int64_t block, Rows* w) {
+  constexpr int M = ATTEND_TILE_ROWS;
   auto slot_of = [&](int x) -> int64_t { return (a.off[x] - a.first_row) * a.G / M + x; };
   w->b = wave_find(a.B, block, slot_of);
   w->t0 = a.off[w->b];
   const int64_t n_tok = a.off[w->b + 1] - w->t0, j = block - slot_of(w->b);
   if (j * M >= n_tok * a.G || !of_class(a, n_tok)) return false;
-  set_block<false>(a, seq_of<false>(a, w->b, w->t0, n_tok), (int32_t)j, M, w);
+  set_block(a, seq_of<false>(a, w->b, w->t0, n_tok), (int32_t)j, w);
   pin_rows(w);
   return true;
 }
@@ -219,7 +216,7 @@ __device__ __forceinline__ bool find_rows(const AttendArgs& a, int64_t block, in
 // Whether it has rows; its sequence.
 template <bool LISTED>
 __device__ __forceinline__ bool entry_seq(const AttendArgs& a, int e, Seq* s) {
-  const int b = LISTED ? e / a.per : e;
+  const int b = LISTED && a.per > 1 ? e / a.per : e;
   const int64_t row = LISTED ? b : a.off[b], n_tok = LISTED ? 1 : a.off[b + 1] - row;
   *s = seq_of<LISTED>(a, b, row, n_tok);
   if (!LISTED && !of_class(a, n_tok)) return false;
@@ -227,9 +224,21 @@ __device__ __forceinline__ bool entry_seq(const AttendArgs& a, int e, Seq* s) {
 }
 template <bool LISTED>
 __device__ __forceinline__ void set_entry(const AttendArgs& a, int e, Seq s, int M, Rows* w) {
-  w->b = LISTED ? e / a.per : e;
+  if constexpr (LISTED) {
+    w->b = a.per == 1 ? e : e / a.per;
+    const int32_t r0 = (e - w->b * a.per) * M;
+    set_rows<32>(a, s, r0, min(M, a.G - r0), 0, 0, w);
+    if (a.window == 0) {  // here no window is none, not all
+      const int32_t end = w->p_hi < 0 ? 0 : (int32_t)((uint32_t)w->p_hi / 32) + 1;
+      w->near.n_first = w->near.n = min((int32_t)((uint32_t)a.sinks / 32) + (a.sinks % 32 != 0), end);
+      w->near.first_b = 0;
+    }
+    w->tiles = w->p_hi < 0 ? 0 : w->near.n + (int32_t)(((int64_t)s.listed * a.r + 31) / 32);
+  } else {
+    w->b = e;
+    set_rows<32>(a, s, 0, s.n_tok * a.G, 0, s.n_tok - 1, w);
+  }
   w->t0 = a.first_row + s.row;
-  set_block<LISTED>(a, s, LISTED ? e - w->b * a.per : 0, M, w);
 }
 
 // The elements of a dword that are not finite, as a mask over its bits.

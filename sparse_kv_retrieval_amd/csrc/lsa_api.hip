@@ -839,7 +839,7 @@ bool plan_fits(const TilePlan& p, const AttendArgs& a) {
 hipError_t launch_plan(AttendArgs a, const SplitPlan& p, bool fp8, int32_t d, hipStream_t stream) {
   if (p.entries == 0) return hipSuccess;
   const bool listed = a.idx != nullptr;
-  a.entries = p.entries; a.per = p.per; a.workers = p.workers; a.tile = 32;
+  a.entries = p.entries; a.per = p.per; a.workers = p.workers;
   a.rows_above = 0; a.rows_to = listed ? INT64_MAX : kSplitRows;
   a.part_ml = (float*)((char*)a.part_o + p.ml);
   a.joins = (int32_t*)((char*)a.part_o + p.joins);
@@ -850,7 +850,7 @@ hipError_t launch_plan(AttendArgs a, const SplitPlan& p, bool fp8, int32_t d, hi
 
 hipError_t launch_plan(AttendArgs a, const TilePlan& p, bool fp8, int32_t d, hipStream_t stream) {
   if (!p.used) return hipSuccess;
-  a.blocks = p.blocks; a.splits = p.splits; a.run = p.run; a.tile = ATTEND_TILE_KEYS;
+  a.blocks = p.blocks; a.splits = p.splits; a.run = p.run;
   a.rows_above = kSplitRows; a.rows_to = INT64_MAX;
   a.part_ml = (float*)((char*)a.part_o + p.ml);
   hipError_t e = launch_attend_tile(a, fp8, d, stream);
