@@ -171,10 +171,15 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       char* d = dst + rr * ROWB;
       const int sw = is_v ? v_swizzle<CPR>(rr) : k_swizzle<CPR>(rr);
       if constexpr (FP8) {
+        // Eight lanes write at once and meet 32 banks: half of them begin with the upper eight codes, or they would
+        // all write even chunks, two to a bank.
+        const bool turn = lane & 4;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const u32x2 lo = widen4(in[e][2 * x], pow2), hi = widen4(in[e][2 * x + 1], pow2);
-          *(u32x4*)(d + ((2 * ch + x) ^ sw) * 16) = (u32x4){lo[0], lo[1], hi[0], hi[1]};
+          const bool upper = turn != (x == 1);
+          const uint32_t c0 = upper ? in[e][2] : in[e][0], c1 = upper ? in[e][3] : in[e][1];
+          const u32x2 lo = widen4(c0, pow2), hi = widen4(c1, pow2);
+          *(u32x4*)(d + ((2 * ch + upper) ^ sw) * 16) = (u32x4){lo[0], lo[1], hi[0], hi[1]};
         }
       } else {
         *(u32x4*)(d + (ch ^ sw) * 16) = in[e];
@@ -244,6 +249,16 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   // next, and a share of the exponentials. What is left of V's scale rides in the exponent, and leaves
   // the sum again by its reciprocal.
   bf16x8 p[2] = {as_bf16x8((u32x4){0, 0, 0, 0}), as_bf16x8((u32x4){0, 0, 0, 0})};
+  u32x4 kf[3], vf[3];
+  // a step's first operands, asked for before the scores are settled
+  auto ahead = [&](int next_buf, int next_u, int old_buf, int old_u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      kf[x] = k_operand(next_buf, next_u, x);
+      vf[x] = v_operand(old_buf, old_u, x / DT, x % DT);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
   auto step = [&](int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next, int old_buf, int old_u) __attribute__((always_inline)) {
     constexpr int E = 16 / KS;  // exponentials of a group
     static_assert(KS == 2 * DT, "as many key steps as value operands");
@@ -257,12 +272,6 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       }
     }
     uint32_t packed[8];
-    u32x4 kf[3], vf[3];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      kf[x] = k_operand(next_buf, next_u, x);
-      vf[x] = v_operand(old_buf, old_u, x / DT, x % DT);
-    }
     s_next = (f32x16)(0.f);
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
@@ -345,6 +354,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     const bool h0 = uni((int)here[0]), h1 = uni((int)here[1]), h2 = uni((int)here[2]), h3 = uni((int)here[3]);
     const bool whole = h0 && h1 && h2 && h3 && whole_tile(t0);
     // The probabilities before this step's belong to the maximum before it: the output is scaled after them.
+    ahead(buf, 1, old, 1);
     bool rose = settle(buf, t0, 0, whole, h0, h1, s0, fall);
     step(buf, 0, s0, buf, 1, s1, old, 1);
     if (rose) scale_out(fall);
@@ -360,6 +370,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    ahead(nb, 0, buf, 0);
     rose = settle(buf, t0, 1, whole, h2, h3, s1, fall);
     // after the last tile the next scores are those of an old buffer, and not used
     step(buf, 1, s1, nb, 0, s0, buf, 0);
