@@ -21,6 +21,16 @@
 // The maximum follows the scores lazily: it is raised (and the accumulators rescaled) only when
 // some score exceeds it by 2^8. Probabilities then stay below 2^8, and no bit is lost in fp32 or
 // bf16, whose exponents have room.
+//
+// Split. HBM bounds it: G query heads share each row read. The 32-key tiles of all sequences are
+// numbered through and cut on the device into equal shares for as many blocks as fit the device at once,
+// so ragged lengths balance; a second launch joins the parts of a row (see AttendArgs). A block's four
+// waves take its tiles in turn, with two or three of them in registers, and join through LDS.
+//
+// Measured on MI355X (64 query heads, 8 key heads, d_h 128): 8 x 125,000 tokens in bf16, 4.10 GB, 601 us
+// (6.8 TB/s); 32 ragged sequences of 4K to 128K in e4m3, 2.32 GB, 370 us (6.3 TB/s). Short calls are
+// bound by latency: finding the share, the page table, the rows and the queries are four dependent
+// reads, about 8 us with the launch, and the join about 4.5 us (one sequence of 4096 tokens: 7.9 + 5 us).
 #include "kv.hpp"
 
 namespace lsa {

