@@ -218,26 +218,6 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
   }
   if (again) __syncthreads();
 
-  // the block's queries: lane column = row
-  bf16x8 q[RT][KS];
-  int32_t p_row[RT], w_row[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = rt * 16 + col;
-    const bool live = r < w.n;
-    const int row = w.r0 + (live ? r : w.n - 1);
-    const int tok = row / a.G;
-    p_row[rt] = w.p0 + tok;
-    w_row[rt] = window_start(a, p_row[rt]);
-    const uint16_t* src = a.q + (w.t0 + tok) * a.q_stride + (int64_t)(h * a.G + (row - tok * a.G)) * D;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      u32x4 x = *(const u32x4*)(src + q_dim<FP8>(s, g));
-      if (!live) x = (u32x4){0, 0, 0, 0};
-      q[rt][s] = as_bf16x8(x);
-    }
-  }
-
   f32x4 acc[RT][VPL];
   float m[RT], l[RT];
 #pragma unroll
@@ -261,7 +241,7 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
           tok = seen ? tok : -1;
         } else {
           const uint32_t at = (uint32_t)(tile - w.near.n) * 32 + i % 32, e = a.r == 1 ? at : at / (uint32_t)a.r;
-          if ((int)e < min(a.count[w.b], a.k)) {
+          if ((int)e < w.listed) {
             const int32_t* list = a.idx + (int64_t)w.b * a.k;
             const int32_t entry = list[e];
             const int64_t far = (int64_t)entry * a.r + (at - e * a.r);
@@ -285,6 +265,28 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
       s_row[i] = row;
     }
   };
+
+  // the first places are asked for before the queries: loads return in order, and the keys' wait for the places
+  resolve(first, min(RUN, count));
+  // the block's queries: lane column = row
+  bf16x8 q[RT][KS];
+  int32_t p_row[RT], w_row[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = rt * 16 + col;
+    const bool live = r < w.n;
+    const int row = w.r0 + (live ? r : w.n - 1);
+    const int tok = row / a.G;
+    p_row[rt] = w.p0 + tok;
+    w_row[rt] = window_start(a, p_row[rt]);
+    const uint16_t* src = a.q + (w.t0 + tok) * a.q_stride + (int64_t)(h * a.G + (row - tok * a.G)) * D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      u32x4 x = *(const u32x4*)(src + q_dim<FP8>(s, g));
+      if (!live) x = (u32x4){0, 0, 0, 0};
+      q[rt][s] = as_bf16x8(x);
+    }
+  }
 
   // Loads of the resolved tile i. A place with nothing reads row 0 of the cache; what it brings is masked.
   auto load = [&](int i, TileT& t) {
@@ -464,9 +466,11 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
   for (int done = 0; done < count; done += RUN) {
     const int n = min(RUN, count - done);
     base = first + done;
-    if (done) __syncthreads();
-    resolve(base, n);
-    __syncthreads();
+    if (done) {
+      __syncthreads();
+      resolve(base, n);
+    }
+    lds_barrier();
     if (wave >= n) continue;
     // DEPTH tiles in registers: the loads of the next ones are in flight while one is worked on
     TileT t[DEPTH];

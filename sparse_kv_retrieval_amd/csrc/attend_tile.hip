@@ -379,10 +379,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       page = page_of(t_next);
       fetch(at);
     }
-    // as __syncthreads(), but the loads of the tile after next stay in flight: only LDS is shared
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    lds_barrier();  // the loads of the tile after next stay in flight
     ahead(nb, 0, buf, 0);
     rose = settle(buf, t0, 1, whole, h2, h3, s1, fall);
     // after the last tile the next scores are those of an old buffer, and not used

@@ -133,6 +133,13 @@ __device__ __forceinline__ int wave_scan(int x) {
 }
 __device__ __forceinline__ int wave_last(int x) { return __builtin_amdgcn_readlane(x, 63); }
 
+// As __syncthreads() for what waves share in LDS, but loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 constexpr float ATTEND_LAZY = 8.0f;
 constexpr float ATTEND_LOWEST = -3.402823466e38f;  // running maximum of a row that has seen nothing
 constexpr float LN2 = 0.6931471805599453f;
@@ -146,6 +153,7 @@ struct Rows {
   int64_t t0;          // row number of the sequence's first token in q
   TileRange near;      // tiles seen by position
   int32_t tiles;       // those and the listed ones
+  int32_t listed;      // listed entries
 };
 
 // The row at position p sees s <= p where s > window_start(a, p) or s < a.sinks.
@@ -184,6 +192,7 @@ __device__ __forceinline__ void set_rows(const AttendArgs& a, Seq s, int32_t r0,
   w->w_hi = window_start(a, w->p_hi);
   w->near = tile_range<TILE>(w->p_lo, w->p_hi, a.window, a.sinks);
   w->tiles = w->near.n;
+  w->listed = s.listed;
 }
 
 // Tile kernel: row block j of a sequence.
@@ -195,7 +204,7 @@ __device__ __forceinline__ void set_block(const AttendArgs& a, Seq s, int32_t j,
 // The fields that a block agrees on, in scalar registers.
 __device__ __forceinline__ void pin_rows(Rows* w) {
   w->b = uni(w->b); w->n = uni(w->n); w->r0 = uni(w->r0); w->p0 = uni(w->p0); w->p_lo = uni(w->p_lo); w->p_hi = uni(w->p_hi);
-  w->w_lo = uni(w->w_lo); w->w_hi = uni(w->w_hi); w->t0 = uni(w->t0); w->tiles = uni(w->tiles);
+  w->w_lo = uni(w->w_lo); w->w_hi = uni(w->w_hi); w->t0 = uni(w->t0); w->tiles = uni(w->tiles); w->listed = uni(w->listed);
   w->near.n_first = uni(w->near.n_first); w->near.first_b = uni(w->near.first_b); w->near.n = uni(w->near.n);
 }
 
