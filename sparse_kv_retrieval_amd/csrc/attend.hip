@@ -542,12 +542,20 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
 // Joins `parts` partial results of one row, at first, first + step, ...: one wave per row.
 template <int D>
 __device__ __forceinline__ void join_row(const AttendArgs& a, int64_t first, int64_t step, int parts, int64_t row, int head) {
-  constexpr int LP = D / 4, GP = 64 / LP, UN = 4;  // lanes of a part, parts at once, and of those in flight
+  constexpr int LP = D / 4, GP = 64 / LP, UN = 8;  // lanes of a part, parts at once, and of those in flight
   const int lane = threadIdx.x & 63, d0 = lane % LP * 4;
+  f32x4 o[UN];
+  auto fetch = [&](int s0, int s) {
+    const int n = min(64, parts - s0);
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+      o[u] = *(const f32x4*)(a.part_o + (first + (s0 + min(s + u * GP + lane / LP, n - 1)) * step) * D + d0);
+  };
+  fetch(0, 0);  // in flight beside the statistics
   float top = ATTEND_LOWEST;
   for (int s = lane; s < parts; s += 64) top = fmaxf(top, a.part_ml[2 * (first + s * step)]);
 #pragma unroll
-  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
   float sum = 0.f;
   f32x4 acc = (f32x4){0.f, 0.f, 0.f, 0.f};
   for (int s0 = 0; s0 < parts; s0 += 64) {
@@ -559,10 +567,7 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, int64_t first, int
       sum += ml[1] * f;
     }
     for (int s = 0; s < n; s += GP * UN) {
-      f32x4 o[UN];
-#pragma unroll
-      for (int u = 0; u < UN; ++u)
-        o[u] = *(const f32x4*)(a.part_o + (first + (s0 + min(s + u * GP + lane / LP, n - 1)) * step) * D + d0);
+      if (s0 + s > 0) fetch(s0, s);
 #pragma unroll
       for (int u = 0; u < UN; ++u) acc += o[u] * __shfl(f, s + u * GP + lane / LP);  // lanes from n on hold a factor of 0
     }
@@ -592,7 +597,7 @@ __global__ __launch_bounds__(AT_THREADS) void split_join_kernel(const AttendArgs
     r %= M;
   } else {
     if (t + a.first_row >= a.off[a.B]) return;
-    entry = upper_seq(a.off, a.B, t + a.first_row);
+    entry = wave_find(a.B, t + a.first_row, [&](int b) { return a.off[b]; });
     if (!of_class(a, a.off[entry + 1] - a.off[entry])) return;
     r += (int)(t + a.first_row - a.off[entry]) * a.G;
   }
@@ -609,7 +614,7 @@ __global__ __launch_bounds__(AT_THREADS) void tile_join_kernel(const AttendArgs 
   const int head = (int)(id - t * a.n_q);
   if (t + a.first_row >= a.off[a.B]) return;
   Rows w;
-  w.b = upper_seq(a.off, a.B, t + a.first_row);
+  w.b = wave_find(a.B, t + a.first_row, [&](int b) { return a.off[b]; });
   w.t0 = a.off[w.b];
   const int64_t n_tok = a.off[w.b + 1] - w.t0;
   if (!of_class(a, n_tok)) return;

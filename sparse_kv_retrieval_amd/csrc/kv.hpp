@@ -104,8 +104,8 @@ hipError_t launch_attend_split_join(const AttendArgs& a, int d, int rows, bool l
 hipError_t launch_attend_tile_join(const AttendArgs& a, int d, hipStream_t s);
 hipError_t launch_attend_tile(const AttendArgs& a, bool fp8, int d, hipStream_t s);
 
-// Largest b in [0, B) with slot(b) <= x, for slot strictly increasing and slot(0) <= x: the lanes
-// of a wave try 64 places at a time.
+// Largest b in [0, B) with slot(b) <= x, for slot non-decreasing and slot(0) <= x: the lanes of a wave try
+// 64 places at a time.
 template <typename F>
 __device__ __forceinline__ int wave_find(int B, int64_t x, F slot) {
   const int lane = threadIdx.x & 63;
