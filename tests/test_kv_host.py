@@ -166,12 +166,17 @@ def test_binding_checks_tensors(lsa):
         with pytest.raises(lsa.LsaError):
             lsa.KvCache(**{**good, **bad})
     q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
-    o, oh = torch.tensor([0, 1, 2]), off(1, 1)
+    o, oh = torch.tensor([0, 1, 2]), off(1, 1)  # on the host: the last check refuses it
     base = dict(q_offsets=o, q_offsets_host=oh, max_kv_len=40, out=q.clone(), scale=1.0)
     for bad in (dict(out=q[:1]), dict(out=q.float()), dict(lse=torch.zeros(2, 3)), dict(q_offsets=o[:2]), dict(q_offsets=o.int()),
                 dict(q_offsets_host=off(1, 2)), dict(q_offsets_host=off(1)), dict(lse=torch.zeros(2, 4).t().contiguous().t())):
         with pytest.raises(lsa.LsaError):
             lsa.attend(c, q, **{**base, **bad})
+    fixed = oh.copy()
+    fixed.setflags(write=False)  # read-only offsets and plain lists serve as well
+    for host in (fixed, oh.tolist(), torch.from_numpy(oh)):
+        with pytest.raises(lsa.LsaError, match="on a GPU"):
+            lsa.attend(c, q, **{**base, "q_offsets_host": host})
     for bad_q in (q.float(), q[..., ::2], q.transpose(1, 2), q[:, :, :32]):
         with pytest.raises((lsa.LsaError)):
             lsa.attend(c, bad_q, **base)
