@@ -429,6 +429,9 @@ APPEND = [
     ("plain_fp8", "fp8", 0, 2, 64, 16, [(30, 47), (5, 5)], None, 0),
     ("many_sequences", "fp8", 3, 1, 64, 16, [(i % 4, 5 + (i * 37) % 200) for i in range(140)], "pairs", 32),
     ("more_new_than_cached", "fp8", 2, 1, 64, 16, [(20, 13), (3, 0), (2, 1)], "halves", 64),
+    ("long", "bf16", 18, 6, 64, 16, [(1500, 1600), (700, 700), (3, 60)], "halves", 64),
+    ("long_fp8", "fp8", 10, 10, 128, 16, [(900, 933), (0, 20), (801, 801)], "pairs", 112),
+    ("many_of_one", "bf16", 1, 1, 64, 16, [(i % 2, 1 + i % 40) for i in range(1200)], "halves", 32),
 ]
 
 
