@@ -85,7 +85,7 @@ __device__ __forceinline__ TileRange tile_range(int32_t p_lo, int32_t p_hi, int3
   if (window > 0) {
     const int32_t s = (int32_t)((uint32_t)sinks / tile) + (sinks % tile != 0);
     t.n_first = s < end ? s : end;
-    const int32_t lo = p_lo - window + 1;  // p_lo >= -2^31 + window fits: both are at most 2^31 - 1
+    const int32_t lo = max(p_lo, 0) - window + 1;  // a row before the first cached token sees none
     t.first_b = lo > 0 ? (int32_t)((uint32_t)lo / tile) : 0;
     if (t.first_b < t.n_first) t.first_b = t.n_first;
   }

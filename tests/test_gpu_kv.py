@@ -170,6 +170,8 @@ ATTEND = [
     ("one_long_of_many", "fp8", 2, 1, 64, 64, [(1, 3)] * 66 + [(2, 9000), (1, 40)], 0, 0),
     ("window_many", "bf16", 2, 1, 64, 16, [(1, 300)] * 65, 200, 7),
     ("window_longer", "bf16", 4, 2, 64, 16, [(20, 60), (1, 9)], 500, 5),
+    ("more_queries_than_keys", "bf16", 4, 2, 64, 16, [(100, 60), (90, 0), (80, 1)], 0, 0),
+    ("more_queries_than_keys_fp8", "fp8", 8, 1, 128, 64, [(400, 190), (20, 3), (6, 1)], 30, 2),
 ]
 
 
@@ -272,6 +274,21 @@ def test_attend_length_beyond_the_bound(torch, lsa):
     torch.cuda.synchronize()
     check_rows(s, q, out, lse, [(0, 0, 69)], 64 ** -0.5, n_q=2)
     assert bool((out[1] == 0).all()) and bool(torch.isneginf(lse[1]).all())
+
+
+@pytest.mark.parametrize("n", [40, 300])
+def test_attend_largest_window(torch, lsa, n):
+    # rows far before the first cached token, and a window whose start before them passes 32 bits
+    s = Setup(torch, lsa, [30], dtype="bf16", n_kv=1, d=64, pt=128, seed=n)
+    pages = (2 ** 31 - 128) // 128
+    s.table_dev = torch.full((1, pages), -1, dtype=torch.int32, device="cuda")
+    s.table_dev[:, :s.table.shape[1]] = torch.from_numpy(s.table).cuda()
+    s.cache = lsa.KvCache(page_table=s.table_dev, kv_len=s.kv_len, **s.parts)
+    q = bf16(torch, s.g, (n, 1, 64))
+    out, lse = run_attend(torch, lsa, s, q, offsets([n]), window=2 ** 31 - 129, max_len=2 ** 31 - 128)
+    torch.cuda.synchronize()
+    check_rows(s, q, out, lse, [(i, 0, 30 - n + i) for i in range(n - 33, n)], 64 ** -0.5, n_q=1)
+    assert bool((out[:n - 30] == 0).all()) and bool(torch.isneginf(lse[:n - 30]).all())
 
 
 @pytest.mark.parametrize("n", [2, 200])
