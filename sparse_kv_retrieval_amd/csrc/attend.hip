@@ -569,7 +569,12 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, int64_t first, int
     for (int s = 0; s < n; s += GP * UN) {
       if (s0 + s > 0) fetch(s0, s);
 #pragma unroll
-      for (int u = 0; u < UN; ++u) acc += o[u] * __shfl(f, s + u * GP + lane / LP);  // lanes from n on hold a factor of 0
+      for (int u = 0; u < UN; ++u) {
+        const int at = s + u * GP + lane / LP;
+        const float w = __shfl(f, at);
+        // beyond the last part that one was read again: a factor of 0 would not clear an infinity
+        if (at < n) acc += o[u] * w;
+      }
     }
   }
 #pragma unroll

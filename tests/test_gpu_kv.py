@@ -250,6 +250,23 @@ def test_attend_values_that_are_not_finite(torch, lsa, dtype, window, news):
             assert (got[r][:, 5] == np.inf).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,total", [(1, 3000), (100, 3000), (1, 460)])
+def test_attend_infinite_values_in_split_rows(torch, lsa, n, total, d):
+    # an infinite value in the first and in the last part of rows that are worked on in parts
+    s = Setup(torch, lsa, [total], dtype="bf16", n_kv=1, d=d, pt=16, seed=d + n)
+    for pos, dim, bad in ((0, 3, float("inf")), (total - n, 9, float("-inf"))):
+        s.parts["v"][int(s.table[0, pos // 16]), 0, pos % 16, dim] = bad
+    s.decode()
+    off = offsets([n])
+    q = bf16(torch, s.g, (n, 2, d), 0.1)  # close scores: no probability is 0
+    assert lsa.attend_workspace_size(s.cache, n_q=2, q_offsets_host=off, max_kv_len=total) > 0
+    out, lse = run_attend(torch, lsa, s, q, off)
+    torch.cuda.synchronize()
+    assert bool((out[..., 3] == float("inf")).all()) and bool((out[..., 9] == float("-inf")).all())
+    check_rows(s, q, out, lse, [(r, 0, total - n + r) for r in sorted({0, n // 2, n - 1})], d ** -0.5, n_q=2)
+
+
 def test_attend_pages_that_are_not_there(torch, lsa):
     for dtype in ("bf16", "fp8"):
         say(f"[attend] bad pages {dtype}")
