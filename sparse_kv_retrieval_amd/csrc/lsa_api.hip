@@ -815,14 +815,14 @@ lsa_status attend_args(AttendArgs* a, size_t bytes, int32_t d, const void* q, in
   const int64_t row = (int64_t)a->n_q * d;
   if (q_stride < row || out_stride < row || !multiple8(q_stride) || !multiple8(out_stride))
     return fail(LSA_ERR_INVALID_ARG, "q_stride and out_stride must be multiples of 8, at least n_q * d_h = %lld", (long long)row);
-  if (!std::isfinite(softmax_scale)) return fail(LSA_ERR_INVALID_ARG, "softmax_scale must be finite");
+  a->scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+  if (!std::isfinite(a->scale_log2)) return fail(LSA_ERR_INVALID_ARG, "softmax_scale / ln 2 must be finite");
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(LSA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   if (bytes > 0 && (!workspace || workspace_bytes < bytes))
     return fail(LSA_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", bytes, workspace_bytes);
   if (bytes > 0 && !aligned16(workspace)) return fail(LSA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   a->q = (const uint16_t*)q; a->q_stride = q_stride; a->out = (uint16_t*)out; a->out_stride = out_stride; a->lse = lse;
   a->G = a->n_q / a->c.n_kv;
-  a->scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
   a->part_o = (float*)workspace;
   return LSA_OK;
 }

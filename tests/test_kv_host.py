@@ -103,6 +103,7 @@ SHARED = [
     ("INVALID_ARG", "aligned", dict(q=FAKE + 8)), ("INVALID_ARG", "aligned", dict(out=FAKE + 8)),
     ("INVALID_ARG", "overlap", dict(out=FAKE)), ("INVALID_ARG", "q_stride", dict(qs=255)), ("INVALID_ARG", "q_stride", dict(os=248)),
     ("INVALID_ARG", "softmax_scale", dict(scale=float("nan"))), ("INVALID_ARG", "softmax_scale", dict(scale=float("inf"))),
+    ("INVALID_ARG", "softmax_scale", dict(scale=3e38)),
     ("INVALID_ARG", "lse", dict(lse=FAKE + 2)), ("UNSUPPORTED", "n_q", dict(n_q=5)), ("UNSUPPORTED", "n_q", dict(n_q=4098)),
     ("INVALID_ARG", "negative", dict(window=-1)), ("INVALID_ARG", "negative", dict(sinks=-1)), ("UNSUPPORTED", "B must", dict(B=0)),
     ("WORKSPACE", "workspace needs", dict(ws=None)), ("WORKSPACE", "workspace needs", dict(nb=100)),
