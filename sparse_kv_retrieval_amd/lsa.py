@@ -379,6 +379,14 @@ def _rows(fn, name, t, dtype, shape, device):
     return step if shape[0] > 1 else shape[1] * shape[2]
 
 
+def check_rows(fn, name, t, shape, device):
+    """Refuses, in the name of `fn`, a tensor that lsa_kv_append would refuse as new rows [rows, heads, d_h]."""
+    step = _rows(fn, name, t, _torch().bfloat16, shape, device)
+    if step % 8 or step < shape[1] * shape[2] or t.data_ptr() % 16:
+        _refuse(fn, f"{name} must be 16-byte aligned, with its rows a multiple of 8 elements apart, at least "
+                    f"{shape[1] * shape[2]} (got {step})")
+
+
 def _offsets(fn, name, off, host, B, rows, device):
     """Checks device and host offsets of rows; returns (the host array, its pointer)."""
     if off.dtype is not _torch().int64 or off.shape != (B + 1,) or off.get_device() != device or not off.is_contiguous():

@@ -30,6 +30,7 @@ This module only wires buffers. All arithmetic happens in the HIP kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import sys
@@ -374,38 +375,63 @@ class Pipeline:
                                               sinks=sinks)
         self.attn_workspace = self._out((max(size, 16),), torch.uint8)
 
+    @contextlib.contextmanager
     def _grow(self, by, stream):
-        """Every sequence gets `by` tokens more, in the order of `stream`."""
+        """Within, every sequence has `by` tokens more, in the order of `stream`; an exception takes them back, so that what
+        a failed call stored lies behind the lengths and is stored again by the next one."""
         if (self.len_h + by > self.capacity).any():
             raise ValueError("the cache is full: alloc_attention(max_steps=...) bounds the steps")
-        self.len_h += by
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
-        with torch.cuda.stream(stream):  # None: the current one
-            self.kv_len.copy_(torch.from_numpy(self.len_h.astype(np.int32)))
+
+        def set_len(length):
+            with torch.cuda.stream(stream):  # None: the current one
+                self.kv_len.copy_(torch.from_numpy(length.astype(np.int32)))
+
+        set_len(self.len_h + by)
+        try:
+            yield
+        except BaseException:
+            set_len(self.len_h)
+            raise
+        self.len_h = self.len_h + by
+
+    def _check_layers(self, fn, name, given, heads, rows):
+        """Refuses new rows that are not as the appends take them, for all layers before anything is enqueued: a refused call
+        stores nothing in any layer."""
+        if len(given) < self.w.L:
+            lsa._refuse(fn, f"{name} must hold a tensor for each of the {self.w.L} layers (got {len(given)})")
+        for l in range(self.w.L):
+            lsa.check_rows(fn, f"{name}[{l}]", given[l], (rows[l], heads, self.q_rot[0].shape[2]), self.kv_len.get_device())
 
     def append_prompt(self, k, v, stream=None):
         """Once: the prompt's keys and values, [layer] -> [sum of N_b * entry_tokens, n_kv, d_h] bfloat16, before the
         rotation, sequence after sequence."""
-        self._grow(self.prompt_len, stream)
-        for l in range(self.w.L):
-            lsa.kv_append(self.caches[l], k[l], v[l], new_offsets=self.prompt_off, new_offsets_host=self.prompt_off_h,
-                          inv_freq=self.inv_freq, stream=stream)
+        rows = [max(int(self.prompt_off_h[-1]), t.shape[0]) for t in k]
+        self._check_layers("append_prompt", "k", k, self.n_kv, rows)
+        self._check_layers("append_prompt", "v", v, self.n_kv, rows)
+        with self._grow(self.prompt_len, stream):
+            for l in range(self.w.L):
+                lsa.kv_append(self.caches[l], k[l], v[l], new_offsets=self.prompt_off, new_offsets_host=self.prompt_off_h,
+                              inv_freq=self.inv_freq, stream=stream)
 
     def attend_step(self, qkv, stream=None):
         """The step's core attention, after step(): qkv [layer] -> [B, n_q + 2 n_kv, d_h] bfloat16, the step's queries, keys
         and values before the rotation. Writes attn_out and attn_lse."""
-        self._grow(1, stream)
-        n_q, n_kv = self.n_q, self.n_kv
-        for l in range(self.w.L):
-            x = qkv[l]
-            lsa.kv_append(self.caches[l], x[:, n_q:n_q + n_kv], x[:, n_q + n_kv:], new_offsets=self.one_off,
-                          new_offsets_host=self.one_off_h, q=x[:, :n_q], q_out=self.q_rot[l], inv_freq=self.inv_freq,
-                          stream=stream)
-            lsa.attend_topk(self.caches[l], self.q_rot[l], idx=self.step_idx[l], count=self.step_count[l],
-                            entry_tokens=self.entry_tokens, scale=self.q_rot[l].shape[2] ** -0.5, window=self.window,
-                            sinks=self.sinks, out=self.attn_out[l], lse=self.attn_lse[l], workspace=self.attn_workspace,
-                            stream=stream)
+        if self.keys_sub is None:
+            raise ValueError("attend_step() attends over what step() lists: alloc_steps() first")
+        n_q, n_kv, rows = self.n_q, self.n_kv, [self.w.B] * self.w.L
+        q, k, v = [x[:, :n_q] for x in qkv], [x[:, n_q:n_q + n_kv] for x in qkv], [x[:, n_q + n_kv:] for x in qkv]
+        for name, part, heads in (("queries of qkv", q, n_q), ("keys of qkv", k, n_kv), ("values of qkv", v, n_kv)):
+            self._check_layers("attend_step", name, part, heads, rows)
+        with self._grow(1, stream):
+            for l in range(self.w.L):
+                lsa.kv_append(self.caches[l], k[l], v[l], new_offsets=self.one_off, new_offsets_host=self.one_off_h, q=q[l],
+                              q_out=self.q_rot[l], inv_freq=self.inv_freq, stream=stream)
+                lsa.attend_topk(self.caches[l], self.q_rot[l], idx=self.step_idx[l], count=self.step_count[l],
+                                entry_tokens=self.entry_tokens, scale=self.q_rot[l].shape[2] ** -0.5, window=self.window,
+                                sinks=self.sinks, out=self.attn_out[l], lse=self.attn_lse[l], workspace=self.attn_workspace,
+                                stream=stream)
 
     def load(self, stream=None):
         """The load step: from the host pool when there is one, else from HBM."""
