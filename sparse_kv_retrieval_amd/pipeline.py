@@ -337,8 +337,10 @@ class Pipeline:
     def alloc_attention(self, *, n_q, n_kv, d_h=128, dtype="bf16", page_tokens=64, entry_tokens=4, window=128, sinks=4,
                         max_steps=64, rot_dim=None, theta=10000.0):
         """A paged cache per layer for every sequence's N_b * entry_tokens prompt tokens and max_steps more, and the
-        buffers of attend_step. `window` is at least the steps between triggers, so that tokens newer than the
-        last selection are seen."""
+        buffers of attend_step. The lists that step() makes hold entries of the prompt, so the steps' own tokens are seen
+        through the window alone: it must cover max_steps."""
+        if window < max_steps:
+            raise ValueError(f"a window of {window} tokens would lose steps' tokens within max_steps = {max_steps}")
         w, L, B = self.w, self.w.L, self.w.B
         bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
         self.entry_tokens, self.window, self.sinks, self.n_q, self.n_kv = entry_tokens, window, sinks, n_q, n_kv

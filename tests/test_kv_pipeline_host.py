@@ -135,3 +135,16 @@ def test_failed_launch_takes_the_lengths_back(launches, at):
     with pytest.raises(ValueError, match="full"):
         p.attend_step(step_input())
     assert state(p) == ([23, 19], [23, 19])
+
+
+def test_window_covers_the_steps(launches):
+    # a step sees its own token and the window - 1 before it; the lists hold prompt entries alone
+    for window, max_steps in ((16, 17), (0, 1), (1, 64)):
+        with pytest.raises(ValueError, match="window"):
+            pipeline(window=window, max_steps=max_steps)
+    for window, max_steps in ((16, 16), (1, 1), (0, 0), (200, 20)):
+        p = pipeline(window=window, max_steps=max_steps)
+        p.append_prompt([rows(T, N_KV)] * 2, [rows(T, N_KV)] * 2)
+        for _ in range(max_steps):
+            p.attend_step(step_input())
+        assert (p.kv_len - p.window <= torch.from_numpy(p.prompt_len)).all()  # the last step's window begins in the prompt
