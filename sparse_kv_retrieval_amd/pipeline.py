@@ -407,8 +407,10 @@ class Pipeline:
             lsa.check_rows(fn, f"{name}[{l}]", given[l], (rows[l], heads, self.q_rot[0].shape[2]), self.kv_len.get_device())
 
     def append_prompt(self, k, v, stream=None):
-        """Once: the prompt's keys and values, [layer] -> [sum of N_b * entry_tokens, n_kv, d_h] bfloat16, before the
-        rotation, sequence after sequence."""
+        """Once, before the steps: the prompt's keys and values, [layer] -> [sum of N_b * entry_tokens, n_kv, d_h] bfloat16,
+        before the rotation, sequence after sequence."""
+        if self.len_h.any():
+            raise ValueError("the prompt comes once, before the steps: its tokens are the cache's first")
         rows = [max(int(self.prompt_off_h[-1]), t.shape[0]) for t in k]
         self._check_layers("append_prompt", "k", k, self.n_kv, rows)
         self._check_layers("append_prompt", "v", v, self.n_kv, rows)

@@ -148,3 +148,21 @@ def test_window_covers_the_steps(launches):
         for _ in range(max_steps):
             p.attend_step(step_input())
         assert (p.kv_len - p.window <= torch.from_numpy(p.prompt_len)).all()  # the last step's window begins in the prompt
+
+
+def test_prompt_comes_once_and_first(launches):
+    p = pipeline(window=64, max_steps=64)  # room for the prompt twice
+    prompt = [rows(T, N_KV)] * 2
+    p.append_prompt(prompt, prompt)
+    n = len(launches.names)
+    for _ in range(2):
+        with pytest.raises(ValueError, match="prompt"):
+            p.append_prompt(prompt, prompt)
+        assert state(p)[0] == state(p)[1] and p.len_h[0] in (20, 21) and len(launches.names) == n
+        p.attend_step(step_input())
+        n = len(launches.names)
+    p = pipeline(window=64, max_steps=64)
+    p.attend_step(step_input())
+    with pytest.raises(ValueError, match="prompt"):
+        p.append_prompt(prompt, prompt)
+    assert state(p) == ([1, 1], [1, 1])
