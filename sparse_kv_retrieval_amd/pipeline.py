@@ -352,7 +352,8 @@ class Pipeline:
         for b in range(B):
             table[b, :pages[b]] = np.arange(first[b], first[b + 1])
         self.page_table = _dev(table, self.device)
-        self.len_h = np.zeros(B, np.int64)
+        self.len_h = np.zeros(B, np.int64)  # kv_len as far as the host has counted it
+        self.prompt_len_dev = _dev(self.prompt_len.astype(np.int32), self.device)
         self.kv_len = torch.zeros(B, dtype=i32, device=self.device)
         shape = (int(first[-1]), n_kv, page_tokens, d_h)
         self.caches = []
@@ -378,25 +379,24 @@ class Pipeline:
         self.attn_workspace = self._out((max(size, 16),), torch.uint8)
 
     @contextlib.contextmanager
-    def _grow(self, by, stream):
+    def _grow(self, by, by_dev, stream):
         """Within, every sequence has `by` tokens more, in the order of `stream`; an exception takes them back, so that what
-        a failed call stored lies behind the lengths and is stored again by the next one."""
+        a failed call stored lies behind the lengths and is stored again by the next one. Nothing waits for the device."""
         if (self.len_h + by > self.capacity).any():
             raise ValueError("the cache is full: alloc_attention(max_steps=...) bounds the steps")
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
-
-        def set_len(length):
-            with torch.cuda.stream(stream):  # None: the current one
-                self.kv_len.copy_(torch.from_numpy(length.astype(np.int32)))
-
-        set_len(self.len_h + by)
+        with torch.cuda.stream(stream):  # None: the current one
+            self.kv_len.add_(by_dev)
+            captured = self.device.type == "cuda" and torch.cuda.is_current_stream_capturing()
         try:
             yield
         except BaseException:
-            set_len(self.len_h)
+            with torch.cuda.stream(stream):
+                self.kv_len.sub_(by_dev)
             raise
-        self.len_h = self.len_h + by
+        if not captured:
+            self.len_h = self.len_h + by
 
     def _check_layers(self, fn, name, given, heads, rows):
         """Refuses new rows that are not as the appends take them, for all layers before anything is enqueued: a refused call
@@ -414,21 +414,24 @@ class Pipeline:
         rows = [max(int(self.prompt_off_h[-1]), t.shape[0]) for t in k]
         self._check_layers("append_prompt", "k", k, self.n_kv, rows)
         self._check_layers("append_prompt", "v", v, self.n_kv, rows)
-        with self._grow(self.prompt_len, stream):
+        with self._grow(self.prompt_len, self.prompt_len_dev, stream):
             for l in range(self.w.L):
                 lsa.kv_append(self.caches[l], k[l], v[l], new_offsets=self.prompt_off, new_offsets_host=self.prompt_off_h,
                               inv_freq=self.inv_freq, stream=stream)
 
     def attend_step(self, qkv, stream=None):
         """The step's core attention, after step(): qkv [layer] -> [B, n_q + 2 n_kv, d_h] bfloat16, the step's queries, keys
-        and values before the rotation. Writes attn_out and attn_lse."""
+        and values before the rotation. Writes attn_out and attn_lse.
+
+        May be captured, with step() before it: every replay is one more step. The host does not count replays (len_h), so
+        keeping them within max_steps is the caller's part; a token beyond the cache's pages is not stored."""
         if self.keys_sub is None:
             raise ValueError("attend_step() attends over what step() lists: alloc_steps() first")
         n_q, n_kv, rows = self.n_q, self.n_kv, [self.w.B] * self.w.L
         q, k, v = [x[:, :n_q] for x in qkv], [x[:, n_q:n_q + n_kv] for x in qkv], [x[:, n_q + n_kv:] for x in qkv]
         for name, part, heads in (("queries of qkv", q, n_q), ("keys of qkv", k, n_kv), ("values of qkv", v, n_kv)):
             self._check_layers("attend_step", name, part, heads, rows)
-        with self._grow(1, stream):
+        with self._grow(1, 1, stream):
             for l in range(self.w.L):
                 lsa.kv_append(self.caches[l], k[l], v[l], new_offsets=self.one_off, new_offsets_host=self.one_off_h, q=q[l],
                               q_out=self.q_rot[l], inv_freq=self.inv_freq, stream=stream)

@@ -74,3 +74,55 @@ def test_steps_after_refused_ones(torch, dtype):
         clean.attend_step(x)
         same(torch, p, clean, f"step {t}")
         assert p.len_h.tolist() == clean.len_h.tolist() == p.kv_len.tolist()
+
+
+def test_captured_step(torch):
+    """step() and attend_step() in one graph, replayed with eager work and waits between, against eager steps."""
+    P.say("[steps] captured")
+    w, (p, clean), hs, qkv = setup(torch, "fp8", steps=6)
+    x = qkv()
+    for q in (p, clean):  # first step eagerly: everything is loaded
+        q.set_step_hidden(hs[0])
+        q.step()
+        q.attend_step(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.step()
+        p.attend_step(x)
+    same(torch, p, clean, "after the capture")  # which ran nothing
+    assert p.len_h.tolist() == clean.len_h.tolist()
+    for t in range(1, 6):
+        for a, b in zip(x, qkv()):
+            a.copy_(b)
+        for q in (p, clean):
+            q.set_step_hidden(hs[t])
+        graph.replay()
+        torch.cuda.synchronize()
+        clean.step()
+        clean.attend_step(x)
+        same(torch, p, clean, f"replay {t}")
+    assert p.kv_len.tolist() == clean.len_h.tolist()
+
+
+def test_step_on_a_given_stream_waits_for_nothing(torch):
+    """Steps on a stream that the current one does not wait for, given as a stream and as its address; the host enqueues them while
+    the stream is still busy."""
+    P.say("[steps] own stream")
+    w, (p, clean), hs, qkv = setup(torch, "bf16")
+    stream = torch.cuda.Stream()
+    xs = [qkv() for _ in range(4)]
+    torch.cuda.synchronize()
+    busy = torch.zeros((8192, 8192), device="cuda")
+    with torch.cuda.stream(stream):
+        for _ in range(8):  # some ten milliseconds
+            busy = (busy @ busy) * 0
+        done = torch.cuda.Event()
+        done.record()
+    for t in range(4):
+        given = stream if t % 2 else stream.cuda_stream
+        p.attend_step(xs[t], stream=given)
+    assert not done.query(), "the host waited for the stream"
+    for t in range(4):
+        clean.attend_step(xs[t])
+    same(torch, p, clean, "four steps")
