@@ -582,8 +582,10 @@ typedef struct {
  * e4m3. New values are stored as e4m3(x / scale), to nearest even; infinities
  * and NaN are stored as NaN. Slots behind the last new token are left as they
  * are.
- * Supported: 1 <= B <= 4096; rot_dim a positive multiple of 16 up to d_h;
- * strides multiples of 8; k_new, v_new, q and q_out 16-byte aligned.
+ * Supported: 1 <= B <= 4096; n_q a multiple of n_kv, n_q <= 1024 * n_kv; rot_dim a
+ * positive multiple of 16 up to d_h; strides multiples of 8; k_new, v_new, q and q_out
+ * 16-byte aligned. With T new tokens in all, T * n_q and T * n_kv are at most 2^31 - 1, and
+ * (T / page_tokens + 2 B) * 2 n_kv, with q plus T * n_q / 32 + 1, is at most 2^24 - 1.
  * ---------------------------------------------------------------------- */
 enum { LSA_ROPE_NONE = 0, LSA_ROPE_HALVES = 1, LSA_ROPE_PAIRS = 2 };
 lsa_status lsa_kv_append(const lsa_kv_cache* cache /* host */, int32_t B, const void* k_new /* dev */,
@@ -621,8 +623,9 @@ lsa_status lsa_kv_append(const lsa_kv_cache* cache /* host */, int32_t B, const 
  * two captured graphs that may.
  * Supported: 1 <= B <= 4096; n_q a multiple of n_kv, n_q <= 1024 * n_kv; at most
  * 2^31 - 1 query rows times heads, and B times the tiles of 32 keys that one
- * sequence may see; strides multiples of 8; q and out 16-byte aligned; out must
- * not overlap q.
+ * sequence may see; where some sequence has more than 64 rows a key head (new
+ * tokens times n_q / n_kv), (T * (n_q / n_kv) / 256 + B) * n_kv below 2^23 for T rows
+ * of q; strides multiples of 8; q and out 16-byte aligned; out must not overlap q.
  * ---------------------------------------------------------------------- */
 size_t lsa_attend_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h,
                                  const int64_t* q_offsets_host /* host [B+1] */, int32_t max_kv_len,
@@ -649,7 +652,9 @@ lsa_status lsa_attend(const lsa_kv_cache* cache /* host */, int32_t B, const voi
  * listed twice in a row, counts once. Negative entries are skipped.
  * Everything else is as for lsa_attend, except that the host gives no bound: a kv_len
  * beyond table_stride * page_tokens counts as that.
- * Supported: as lsa_attend, with 1 <= k <= 65536 and 1 <= entry_tokens <= 128.
+ * Supported: as lsa_attend, with 1 <= k <= 65536 and 1 <= entry_tokens <= 128; where
+ * n_q > 64 * n_kv, tiles count once for each 64 of n_q / n_kv (rounded up), and B * n_kv
+ * times those is below 2^24.
  * ---------------------------------------------------------------------- */
 size_t lsa_attend_topk_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h, int32_t k,
                                       int32_t entry_tokens, int32_t window, int32_t sinks);

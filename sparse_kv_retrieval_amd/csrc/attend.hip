@@ -591,8 +591,8 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, int64_t first, int
 }
 
 template <int D, bool LISTED>
-__global__ __launch_bounds__(AT_THREADS) void split_join_kernel(const AttendArgs a, int M) {
-  const int64_t id = (int64_t)blockIdx.x * AT_WAVES + (threadIdx.x >> 6);
+__global__ __launch_bounds__(AT_THREADS) void split_join_kernel(const AttendArgs a, int M, int64_t from) {
+  const int64_t id = from + (int64_t)blockIdx.x * AT_WAVES + (threadIdx.x >> 6);
   if (id >= a.T * a.n_q) return;
   const int64_t t = id / a.n_q;
   const int head = (int)(id - t * a.n_q), h = head / a.G;
@@ -612,8 +612,8 @@ __global__ __launch_bounds__(AT_THREADS) void split_join_kernel(const AttendArgs
 }
 
 template <int D>
-__global__ __launch_bounds__(AT_THREADS) void tile_join_kernel(const AttendArgs a) {
-  const int64_t id = (int64_t)blockIdx.x * AT_WAVES + (threadIdx.x >> 6);
+__global__ __launch_bounds__(AT_THREADS) void tile_join_kernel(const AttendArgs a, int64_t from) {
+  const int64_t id = from + (int64_t)blockIdx.x * AT_WAVES + (threadIdx.x >> 6);
   if (id >= a.T * a.n_q) return;
   const int64_t t = id / a.n_q;
   const int head = (int)(id - t * a.n_q);
@@ -648,23 +648,36 @@ hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_til
   return listed ? launch_dim<true>(a, fp8, d, row_tiles, s) : launch_dim<false>(a, fp8, d, row_tiles, s);
 }
 
-static dim3 join_grid(const AttendArgs& a) { return dim3((unsigned)((a.T * a.n_q + AT_WAVES - 1) / AT_WAVES)); }
+// One wave per row and head, in launches of at most `most` blocks each: a launch has fewer than 2^32 threads.
+template <typename F>
+static hipError_t launch_joins(const AttendArgs& a, F launch) {
+  constexpr int64_t most = (int64_t)(UINT32_MAX / AT_THREADS);
+  const int64_t blocks = (a.T * a.n_q + AT_WAVES - 1) / AT_WAVES;
+  hipError_t e = hipSuccess;
+  for (int64_t at = 0; at < blocks && e == hipSuccess; at += most) {
+    launch(dim3((unsigned)(blocks - at < most ? blocks - at : most)), at * AT_WAVES);
+    e = hipGetLastError();
+  }
+  return e;
+}
 
 hipError_t launch_attend_split_join(const AttendArgs& a, int d, int M, bool listed, hipStream_t s) {
-  if (listed) {
-    if (d == 64) split_join_kernel<64, true><<<join_grid(a), AT_THREADS, 0, s>>>(a, M);
-    else split_join_kernel<128, true><<<join_grid(a), AT_THREADS, 0, s>>>(a, M);
-  } else {
-    if (d == 64) split_join_kernel<64, false><<<join_grid(a), AT_THREADS, 0, s>>>(a, M);
-    else split_join_kernel<128, false><<<join_grid(a), AT_THREADS, 0, s>>>(a, M);
-  }
-  return hipGetLastError();
+  return launch_joins(a, [&](dim3 grid, int64_t from) {
+    if (listed) {
+      if (d == 64) split_join_kernel<64, true><<<grid, AT_THREADS, 0, s>>>(a, M, from);
+      else split_join_kernel<128, true><<<grid, AT_THREADS, 0, s>>>(a, M, from);
+    } else {
+      if (d == 64) split_join_kernel<64, false><<<grid, AT_THREADS, 0, s>>>(a, M, from);
+      else split_join_kernel<128, false><<<grid, AT_THREADS, 0, s>>>(a, M, from);
+    }
+  });
 }
 
 hipError_t launch_attend_tile_join(const AttendArgs& a, int d, hipStream_t s) {
-  if (d == 64) tile_join_kernel<64><<<join_grid(a), AT_THREADS, 0, s>>>(a);
-  else tile_join_kernel<128><<<join_grid(a), AT_THREADS, 0, s>>>(a);
-  return hipGetLastError();
+  return launch_joins(a, [&](dim3 grid, int64_t from) {
+    if (d == 64) tile_join_kernel<64><<<grid, AT_THREADS, 0, s>>>(a, from);
+    else tile_join_kernel<128><<<grid, AT_THREADS, 0, s>>>(a, from);
+  });
 }
 
 }  // namespace lsa

@@ -829,11 +829,11 @@ lsa_status attend_args(AttendArgs* a, size_t bytes, int32_t d, const void* q, in
 
 bool plan_fits(const SplitPlan& p, const AttendArgs& a) {
   // the split kernel counts tiles (with at least one a row block) in int32
-  return p.entries * std::max<int64_t>(p.tiles, 1) <= INT32_MAX && (int64_t)std::max(p.workers, p.entries) * a.c.n_kv <= kMaxBlocks && a.T * a.n_q <= kMaxBlocks * 4;
+  return p.entries * std::max<int64_t>(p.tiles, 1) <= INT32_MAX && (int64_t)std::max(p.workers, p.entries) * a.c.n_kv <= kMaxBlocks;
 }
 bool plan_fits(const TilePlan& p, const AttendArgs& a) {
   // its blocks have 512 threads
-  return !p.used || (p.blocks * p.splits * a.c.n_kv <= kMaxBlocks / 2 && a.T * a.n_q <= kMaxBlocks * 4);
+  return !p.used || p.blocks * p.splits * a.c.n_kv <= kMaxBlocks / 2;
 }
 
 hipError_t launch_plan(AttendArgs a, const SplitPlan& p, bool fp8, int32_t d, hipStream_t stream) {
@@ -961,6 +961,7 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, 
   if ((s = check_cache(cache, &fp8, &a.c)) != LSA_OK) return s;
   if (!plan_sizes_ok(B, n_q, a.c.n_kv, cache->d_h, 0, 0))
     return fail(LSA_ERR_UNSUPPORTED, "B must be in [1, %d] and n_q a multiple of n_kv, at most %d times it", kKvMaxB, kKvMaxGroup);
+  if (n_q > INT32_MAX / B) return fail(LSA_ERR_UNSUPPORTED, "at most 2^31-1 rows times heads");
   if (!idx || !count) return fail(LSA_ERR_INVALID_ARG, "idx and count must be set");
   if (k < 1 || k > 65536) return fail(LSA_ERR_UNSUPPORTED, "k must be in [1, 65536] (got %d)", k);
   if (entry_tokens < 1 || entry_tokens > 128) return fail(LSA_ERR_UNSUPPORTED, "entry_tokens must be in [1, 128] (got %d)", entry_tokens);

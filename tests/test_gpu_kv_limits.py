@@ -1,0 +1,59 @@
+"""Large calls of the paged cache's attention (marked gpu), against the float64 oracle of test_gpu_kv.py, whose tolerances are
+used as they are."""
+import numpy as np
+import pytest
+
+from tests.parity import say
+from tests.test_gpu_kv import bf16, check_rows, lsa, offsets, torch  # noqa: F401 (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+
+class Shared:
+    """A bf16 cache of one sequence's pages that several sequences read, as check_rows takes it."""
+
+    def __init__(self, torch, lsa, totals, *, n_kv, d, pt, width, seed):
+        g = self.g = np.random.default_rng(seed)
+        self.n_kv, self.d, self.totals = n_kv, d, list(totals)
+        pages = 40
+        x = {n: torch.from_numpy(g.normal(size=(pages, n_kv, pt, d))).to(torch.bfloat16) for n in ("k", "v")}
+        self.decoded = {n: y.double().numpy() for n, y in x.items()}
+        self.table = np.tile(np.arange(width, dtype=np.int32) % pages, (len(totals), 1))
+        self.kv_len = torch.tensor(totals, dtype=torch.int32, device="cuda")
+        self.cache = lsa.KvCache(k=x["k"].cuda(), v=x["v"].cuda(), page_table=torch.from_numpy(self.table).cuda(),
+                                 kv_len=self.kv_len)
+
+
+def test_attend_more_rows_than_one_joining_launch(torch, lsa):
+    """A prompt of 8,389,208 tokens and 40 decode rows behind it, 8 heads: 67,113,984 rows times heads. The decode
+    rows are worked on in parts, and the launch that joins them takes 4 * (2^24 - 1) at a time: they are beyond."""
+    say("[attend] many rows")
+    n_kv, d, pt, window, tail = 8, 64, 128, 2048, 40
+    prompt = (1 << 23) + 600
+    decode = [3000 + 17 * i for i in range(tail)]
+    s = Shared(torch, lsa, [prompt] + decode, n_kv=n_kv, d=d, pt=pt, width=-(-prompt // pt), seed=2)
+    off = offsets([prompt] + [1] * tail)
+    rows = int(off[-1])
+    assert (prompt * n_kv) > 4 * (2 ** 24 - 1)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    q = torch.empty((rows, n_kv, d), dtype=torch.bfloat16, device="cuda")
+    for x in q.split(1 << 20):
+        x.normal_(generator=g)
+    out = torch.full_like(q, -7.0)
+    lse = torch.full((rows, n_kv), -7.0, device="cuda")
+    size = lsa.attend_workspace_size(s.cache, n_q=n_kv, q_offsets_host=off, max_kv_len=prompt, window=window)
+    assert size > 0
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    lsa.attend(s.cache, q, q_offsets=torch.from_numpy(off).cuda(), q_offsets_host=off, max_kv_len=prompt, out=out, lse=lse,
+               scale=d ** -0.5, window=window, workspace=ws)
+    torch.cuda.synchronize()
+    assert bool((lse != -7).all())
+    # the decode rows, as a call of their own would number them
+    at = prompt
+    s.totals = decode
+    s.table = s.table[1:, :-(-max(decode) // pt)]
+    check_rows(s, q[at:], out[at:], lse[at:], [(i, i, decode[i] - 1) for i in (0, 1, 19, 38, 39)], d ** -0.5, window, n_q=n_kv)
+    # and the prompt's first ones
+    s.totals, s.table = [3000], s.table[:1]
+    check_rows(s, q[:3000], out[:3000], lse[:3000], [(i, 0, i) for i in (0, 1, 2047, 2048, 2999)], d ** -0.5, window, n_q=n_kv)
