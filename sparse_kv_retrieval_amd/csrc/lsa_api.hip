@@ -693,6 +693,7 @@ lsa_status check_rows(int32_t B, const int64_t* off, const int64_t* off_host, in
   return LSA_OK;
 }
 
+// Most tiles that a row sees by its window and as first tokens.
 int64_t near_tiles(int64_t window, int64_t sinks, int64_t tile) {
   return (sinks + tile - 1) / tile + (window > 0 ? (window + tile - 2) / tile + 1 : 0);
 }
@@ -788,6 +789,8 @@ RaggedPlan plan_ragged(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, const in
   return r;
 }
 
+int64_t listed_tiles(int64_t k, int64_t entry_tokens) { return (k * entry_tokens + 31) / 32; }
+
 SplitPlan plan_listed(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t k, int32_t entry_tokens, int32_t window,
                       int32_t sinks, bool fp8 = false) {
   SplitPlan p;
@@ -795,7 +798,7 @@ SplitPlan plan_listed(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t k
   p.rows = G <= 16 ? 16 : G <= 32 ? 32 : 64;
   p.per = (G + p.rows - 1) / p.rows;
   p.entries = B * p.per;
-  share_tiles(&p, n_kv, d, fp8, near_tiles(window, sinks, 32) + ((int64_t)k * entry_tokens + 31) / 32);
+  share_tiles(&p, n_kv, d, fp8, near_tiles(window, sinks, 32) + listed_tiles(k, entry_tokens));
   return p;
 }
 
@@ -969,8 +972,11 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, 
   a.max_kv_len = (int32_t)std::min<int64_t>(cache->table_stride * cache->page_tokens, INT32_MAX - 64);
   a.idx = idx; a.count = count; a.k = k; a.r = entry_tokens;
   a.first_row = 0; a.T = B; a.B = B; a.n_q = n_q;
-  const SplitPlan p = plan_listed(B, n_q, a.c.n_kv, cache->d_h, k, entry_tokens, window, sinks, fp8);
+  // The workspace is laid out by the window as given, for its size is asked without a table; the tiles there are end
+  // with the table.
+  SplitPlan p = plan_listed(B, n_q, a.c.n_kv, cache->d_h, k, entry_tokens, window, sinks, fp8);
   a.window = std::min(window, a.max_kv_len); a.sinks = std::min(sinks, a.max_kv_len);
+  p.tiles = std::min(near_tiles(a.window, a.sinks, 32), ((int64_t)a.max_kv_len + 31) / 32) + listed_tiles(k, entry_tokens);
   if ((s = attend_args(&a, p.bytes, cache->d_h, q, q_stride, softmax_scale, out, out_stride, lse, workspace,
                        workspace_bytes)) != LSA_OK)
     return s;

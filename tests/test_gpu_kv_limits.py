@@ -57,3 +57,22 @@ def test_attend_more_rows_than_one_joining_launch(torch, lsa):
     # and the prompt's first ones
     s.totals, s.table = [3000], s.table[:1]
     check_rows(s, q[:3000], out[:3000], lse[:3000], [(i, 0, i) for i in (0, 1, 2047, 2048, 2999)], d ** -0.5, window, n_q=n_kv)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (9, 2 ** 31 - 1)])
+def test_topk_of_any_window(torch, lsa, window, sinks):
+    # more sequences than windows of 2^31 - 1 could have tiles, and a table that ends after 300 tokens or so
+    say(f"[attend_topk] window {window} sinks {sinks}")
+    B, n_q, n_kv, d, pt, k = 70, 4, 2, 64, 16, 12
+    lens = [(7 * b) % 300 for b in range(B)]
+    s = Shared(torch, lsa, lens, n_kv=n_kv, d=d, pt=pt, width=19, seed=4)
+    idx = np.sort(s.g.integers(0, 150, (B, k)).astype(np.int32), 1)
+    listed = [sorted(set(x.tolist())) for x in idx]
+    q = bf16(torch, s.g, (B, n_q, d))
+    out, lse = torch.full_like(q, -7.0), torch.full((B, n_q), -7.0, device="cuda")
+    size = lsa.attend_topk_workspace_size(s.cache, n_q=n_q, k=k, entry_tokens=2, window=window, sinks=sinks)
+    ws = torch.full((max(size, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    lsa.attend_topk(s.cache, q, idx=torch.from_numpy(idx).cuda(), count=torch.full((B,), k, dtype=torch.int32, device="cuda"), out=out,
+                    lse=lse, scale=d ** -0.5, entry_tokens=2, window=window, sinks=sinks, workspace=ws)
+    torch.cuda.synchronize()
+    check_rows(s, q, out, lse, [(b, b, lens[b] - 1) for b in range(B)], d ** -0.5, window, sinks, listed, 2, n_q)

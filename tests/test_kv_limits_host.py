@@ -74,3 +74,21 @@ def test_append_limit(lsa):
             taken(lsa, st)
         else:
             refused(lsa, lsa.ERR_UNSUPPORTED, "too many", st)
+
+
+@pytest.mark.parametrize("window,sinks", [(1 << 30, 0), ((1 << 31) - 1, 0), (5, (1 << 31) - 1), ((1 << 31) - 1, (1 << 31) - 1)])
+@pytest.mark.parametrize("B", [32, 128, 4096])
+def test_topk_takes_any_window(lsa, B, window, sinks):
+    # 8 pages of 16 tokens: four tiles by position at most, whatever the window
+    taken(lsa, topk(lsa, cache(lsa), B=B, window=window, sinks=sinks, nb=1 << 40))
+
+
+def test_topk_counts_the_tiles_of_the_table(lsa):
+    # 2^19 tiles by position and 2 of the list: 4095 sequences of them pass, 4096 do not
+    c = cache(lsa, page_tokens=128, table_stride=1 << 17)
+    for B, ok in ((4095, True), (4096, False)):
+        st = topk(lsa, c, B=B, window=(1 << 31) - 1, nb=1 << 40)
+        if ok:
+            taken(lsa, st)
+        else:
+            refused(lsa, lsa.ERR_UNSUPPORTED, "too many", st)
