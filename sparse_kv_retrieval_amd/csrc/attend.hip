@@ -172,7 +172,7 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
 
   for (bool again = false;; again = true) {
   Rows w;
-  int first = 0, count, parts = 1, entry = worker;
+  int first = 0, count, parts = 1, entry = worker, owner = worker;  // owner: the worker that begins this row block
   if (a.workers > 0) {
     if (at >= end) return;
     while (at >= before + wave_last(upto)) {
@@ -188,7 +188,6 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
     set_entry<LISTED>(a, entry, s, M, &w);
     pin_rows(&w);
     const int last = before + __builtin_amdgcn_readlane(upto, which), n = max(w.tiles, 1);
-    int owner;  // the worker that begins this row block
     if (whole) {
       parts = (n + share - 1) / share;
       owner = last - parts;
@@ -529,7 +528,7 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
         if (a.lse && tid % 16 == 0)
           a.lse[(w.t0 + tok) * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (top + __log2f(sum)) * LN2;
       } else {
-        const int64_t to = (((int64_t)worker + entry) * a.c.n_kv + h) * M + r;
+        const int64_t to = (part_slot(a, worker, entry, owner) * a.c.n_kv + h) * M + r;
 #pragma unroll
         for (int e = 0; e < VPL; e += 4) *(f32x4*)(a.part_o + to * D + d0 + e) = (f32x4){o[e], o[e + 1], o[e + 2], o[e + 3]};
         if (tid % 16 == 0) *(f32x2*)(a.part_ml + 2 * to) = (f32x2){top, sum};
@@ -608,7 +607,7 @@ __global__ __launch_bounds__(AT_THREADS) void split_join_kernel(const AttendArgs
   }
   const int worker = a.joins[2 * ((int64_t)entry * a.c.n_kv + h)], parts = a.joins[2 * ((int64_t)entry * a.c.n_kv + h) + 1];
   if (parts == 0) return;
-  join_row<D>(a, (((int64_t)worker + entry) * a.c.n_kv + h) * M + r, (int64_t)a.c.n_kv * M, parts, t + a.first_row, head);
+  join_row<D>(a, (part_slot(a, worker, entry, worker) * a.c.n_kv + h) * M + r, (int64_t)a.c.n_kv * M, parts, t + a.first_row, head);
 }
 
 template <int D>

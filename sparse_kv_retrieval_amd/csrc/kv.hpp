@@ -63,12 +63,18 @@ struct AttendArgs {
   int32_t splits, run;
   // Split kernel: the tiles of all row blocks of a key head, one after the other, are shared evenly by
   // `workers` blocks (0: each row block has a worker of its own). A worker's part of a row block goes to
-  // partials [worker + row block][n_kv][M][D], a number that no two parts have, and
-  // joins[row block][n_kv] says which workers took part.
+  // partials [part_slot()][n_kv][M][D], and joins[row block][n_kv] says which workers took part.
   int32_t entries, per;   // row blocks, and how many of them a sequence has (LISTED)
   int32_t workers;
   int32_t* joins;         // pairs: first worker, number of parts (0: written whole)
 };
+
+// Where the part goes that `worker` has of row block `entry`, which worker `owner` begins. From a part to the next one the
+// worker grows (the same row block), or the row block does, and with it the owner: only the last row block that a
+// worker begins can have several parts. So neither sum is met twice; the one that needs less room is taken.
+__device__ __forceinline__ int64_t part_slot(const AttendArgs& a, int32_t worker, int32_t entry, int32_t owner) {
+  return (int64_t)worker + (a.entries < a.workers ? entry : owner);
+}
 
 // Tiles of `tile` tokens that the rows at positions p_lo..p_hi see. Tile i < n_first is tile i of the
 // sequence, tile i >= n_first is tile first_b + i - n_first.

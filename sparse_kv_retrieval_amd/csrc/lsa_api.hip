@@ -713,7 +713,8 @@ struct SplitPlan {
 // registers are many (four row tiles, or two of bf16, at d_h 128), two otherwise. More were slower on every
 // size tried (32 ragged sequences in e4m3: 401 us with 512, 407 with 1024, 416 with 2048; their windows of 1024:
 // 28.4, 32.9 and 37.1 us): they add partial results and a second round. Row blocks of at most four tiles, one
-// a wave, are not worth sharing. The workspace's size does not depend on the cache's dtype.
+// a wave, are not worth sharing. The workspace's size does not depend on the cache's dtype, and its partial results
+// are no more than two per worker.
 void share_tiles(SplitPlan* p, int32_t n_kv, int32_t d, bool fp8, int64_t tiles) {
   p->tiles = tiles;
   if (p->entries == 0 || tiles <= 4) return;
@@ -722,7 +723,7 @@ void share_tiles(SplitPlan* p, int32_t n_kv, int32_t d, bool fp8, int64_t tiles)
     return (int32_t)std::min<int64_t>(std::max<int64_t>(blocks / n_kv, 1), (p->entries * tiles + 3) / 4);
   };
   p->workers = workers(p->rows * d * (fp8 ? 1 : 2) >= 64 * 128 ? 256 : 512);
-  const size_t rows = (size_t)(workers(512) + p->entries) * n_kv * p->rows;
+  const size_t rows = (size_t)(workers(512) + std::min(p->entries, workers(512))) * n_kv * p->rows;
   p->ml = rows * d * 4;
   p->joins = p->ml + rows * 8;
   p->bytes = p->joins + (size_t)p->entries * n_kv * 8;

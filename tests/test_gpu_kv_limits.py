@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from tests.parity import say
-from tests.test_gpu_kv import bf16, check_rows, lsa, offsets, torch  # noqa: F401 (fixtures)
+from tests.test_gpu_kv import Setup, bf16, check_rows, lsa, offsets, run_attend, torch  # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,44 @@ def test_topk_of_any_window(torch, lsa, window, sinks):
                     lse=lse, scale=d ** -0.5, entry_tokens=2, window=window, sinks=sinks, workspace=ws)
     torch.cuda.synchronize()
     check_rows(s, q, out, lse, [(b, b, lens[b] - 1) for b in range(B)], d ** -0.5, window, sinks, listed, 2, n_q)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("B", [64, 65, 200])
+def test_parts_of_more_sequences_than_workers(torch, lsa, dtype, B):
+    """8 key heads leave 64 workers a head (32 where rows fill a CU), so their shares end within sequences. The workspace has
+    the size asked for, between bytes that have to stay."""
+    say(f"[attend] {B} sequences {dtype}")
+    n_q, n_kv, d, pt, k = 16, 8, 64, 16, 40
+    totals = [1 + (i * 211) % 700 for i in range(B)]
+    s = Setup(torch, lsa, totals, dtype=dtype, n_kv=n_kv, d=d, pt=pt, seed=B)
+    guard = 4096
+
+    def workspace(size):
+        assert size > 0
+        raw = torch.full((size + 2 * guard,), 0xFF, dtype=torch.uint8, device="cuda")
+        return raw, raw[guard:guard + size]
+
+    def untouched(raw):
+        return bool((raw[:guard] == 0xFF).all()) and bool((raw[-guard:] == 0xFF).all())
+
+    news = [1 + i % 2 * (i % 9) for i in range(B)]  # up to nine tokens of two heads each
+    for new in ([1] * B, news):
+        off = offsets(new)
+        q = bf16(torch, s.g, (int(off[-1]), n_q, d))
+        raw, ws = workspace(lsa.attend_workspace_size(s.cache, n_q=n_q, q_offsets_host=off, max_kv_len=max(totals)))
+        out, lse = run_attend(torch, lsa, s, q, off, ws=ws)
+        torch.cuda.synchronize()
+        assert untouched(raw)
+        check_rows(s, q, out, lse, [(int(off[b]) + i, b, totals[b] - new[b] + i) for b in range(B) for i in range(new[b])],
+                   d ** -0.5, n_q=n_q, tag=f"{new[:3]}")
+    idx = np.sort(s.g.integers(0, 100, (B, k)).astype(np.int32), 1)
+    q = bf16(torch, s.g, (B, n_q, d))
+    out, lse = torch.full_like(q, -7.0), torch.full((B, n_q), -7.0, device="cuda")
+    raw, ws = workspace(lsa.attend_topk_workspace_size(s.cache, n_q=n_q, k=k, entry_tokens=4, window=100, sinks=3))
+    lsa.attend_topk(s.cache, q, idx=torch.from_numpy(idx).cuda(), count=torch.full((B,), k, dtype=torch.int32, device="cuda"), out=out,
+                    lse=lse, scale=d ** -0.5, entry_tokens=4, window=100, sinks=3, workspace=ws)
+    torch.cuda.synchronize()
+    assert untouched(raw)
+    check_rows(s, q, out, lse, [(b, b, totals[b] - 1) for b in range(B)], d ** -0.5, 100, 3, [sorted(set(x.tolist())) for x in idx], 4,
+               n_q)

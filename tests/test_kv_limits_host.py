@@ -92,3 +92,23 @@ def test_topk_counts_the_tiles_of_the_table(lsa):
             taken(lsa, st)
         else:
             refused(lsa, lsa.ERR_UNSUPPORTED, "too many", st)
+
+
+@pytest.mark.parametrize("n_q,n_kv", [(128, 128), (64, 8), (64, 1), (1024, 1024), (256, 2), (8, 8)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_workspaces_do_not_grow_with_the_batch(lsa, n_q, n_kv, d):
+    # parts are as many as two per block that shares the keys, and a pair of integers per row block says where they are
+    for news in ([1], [2], [8] + [1]):
+        def size(B):
+            host = off(*((news + [1] * B)[:B]))
+            return lsa._attend_ws(B, n_q, n_kv, d, host.ctypes.data, 1 << 17, 0, 0)
+
+        most = news[0] * (n_q // n_kv)
+        rows = 16 if most <= 16 else 32 if most <= 32 else 64
+        if most > 64:
+            continue
+        for B in (64, 256, 4096):
+            assert 0 < size(B) <= 2 * max(512, n_kv) * rows * (d + 2) * 4 + B * n_kv * 8 <= 1 << 28, (B, news)
+    per = -(-(n_q // n_kv) // 64)
+    for B in (64, 256, 4096):
+        assert 0 < lsa._attend_topk_ws(B, n_q, n_kv, d, 2048, 4, 128, 4) <= 2 * max(512, n_kv) * 64 * (d + 2) * 4 + B * per * n_kv * 8
