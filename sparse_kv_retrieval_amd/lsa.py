@@ -506,8 +506,16 @@ def kv_append(cache, k_new, v_new, *, new_offsets, new_offsets_host, q=None, q_o
                                   new_offsets.data_ptr(), host_at, style, inv_at, rot, pos_at), stream)
 
 
+def _int32(fn, *values):
+    """Refuses numbers that would arrive in the library as others: ctypes takes the lower 32 bits."""
+    for x in values:
+        if not -0x80000000 <= x <= 0x7FFFFFFF:
+            _refuse(fn, f"{x} does not fit 32 bits")
+
+
 def attend_workspace_size(cache, *, n_q, q_offsets_host, max_kv_len, window=0, sinks=0) -> int:
     """lsa_attend_workspace_size for this cache."""
+    _int32("lsa_attend_workspace_size", n_q, max_kv_len, window, sinks)
     off, offp = _host64(q_offsets_host)
     return int(_attend_ws(off.size - 1, n_q, cache.n_kv, cache.d_h, offp, max_kv_len, window, sinks))
 
@@ -537,6 +545,7 @@ def attend(cache, q, *, q_offsets, q_offsets_host, max_kv_len, out, scale, windo
     or None; q_offsets [B + 1] int64 on the device and on the host; workspace a tensor of at least
     attend_workspace_size(...) bytes for the same arguments."""
     fn = "lsa_attend"
+    _int32(fn, max_kv_len, window, sinks)
     rows, n_q, qs, os_, lse_at, ws_at, nbytes = _attend_tensors(fn, cache, q, out, lse, workspace)
     host, host_at = _offsets(fn, "q_offsets", q_offsets, q_offsets_host, cache.B, rows, cache.device)
     _launch(cache.device, fn, _attend, (cache.ref, cache.B, q.data_ptr(), qs, n_q, q_offsets.data_ptr(), host_at, max_kv_len,
@@ -545,6 +554,7 @@ def attend(cache, q, *, q_offsets, q_offsets_host, max_kv_len, out, scale, windo
 
 def attend_topk_workspace_size(cache, *, n_q, k, entry_tokens=1, window=0, sinks=0) -> int:
     """lsa_attend_topk_workspace_size for this cache."""
+    _int32("lsa_attend_topk_workspace_size", n_q, k, entry_tokens, window, sinks)
     return int(_attend_topk_ws(cache.B, n_q, cache.n_kv, cache.d_h, k, entry_tokens, window, sinks))
 
 
@@ -553,6 +563,7 @@ def attend_topk(cache, q, *, idx, count, out, scale, entry_tokens=1, window=0, s
     """lsa_attend_topk: q and out [B, n_q, d_h] bfloat16, idx [B, k] and count [B] int32 as topk and topk_step
     write them, lse [B, n_q] float32 or None; workspace of at least attend_topk_workspace_size(...) bytes."""
     fn, torch, B = "lsa_attend_topk", _torch(), cache.B
+    _int32(fn, entry_tokens, window, sinks)
     rows, n_q, qs, os_, lse_at, ws_at, nbytes = _attend_tensors(fn, cache, q, out, lse, workspace)
     if rows != B or idx.dim() != 2:
         _refuse(fn, f"q must have one row per sequence and idx must be [B, k] (got {rows} rows for {B}, {list(idx.shape)})")
