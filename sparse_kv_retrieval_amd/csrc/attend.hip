@@ -172,7 +172,7 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
 
   for (bool again = false;; again = true) {
   Rows w;
-  int first = 0, count, parts = 1, entry = worker, owner = worker;  // owner: the worker that begins this row block
+  int first = 0, count, slot = -1, entry = worker;  // slot: where the worker's part goes; negative: it is the whole
   if (a.workers > 0) {
     if (at >= end) return;
     while (at >= before + wave_last(upto)) {
@@ -188,6 +188,7 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
     set_entry<LISTED>(a, entry, s, M, &w);
     pin_rows(&w);
     const int last = before + __builtin_amdgcn_readlane(upto, which), n = max(w.tiles, 1);
+    int owner, parts;  // owner: the worker that begins this row block
     if (whole) {
       parts = (n + share - 1) / share;
       owner = last - parts;
@@ -207,6 +208,7 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
       a.joins[2 * (entry * a.c.n_kv + h)] = worker;
       a.joins[2 * (entry * a.c.n_kv + h) + 1] = parts > 1 ? parts : 0;
     }
+    slot = uni(parts > 1 ? part_slot(a, worker, entry, owner) : -1);
     count = min(count, w.tiles - first);  // 0 where nothing is seen
   } else {
     Seq s;
@@ -519,7 +521,7 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
         for (int e = 0; e < VPL; ++e) o[e] += s_o[v][r][d0 + e] * f;
       }
       const int row = w.r0 + r, tok = row / a.G, head = h * a.G + (row - tok * a.G);
-      if (parts <= 1) {
+      if (slot < 0) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         uint16_t* dst = a.out + (w.t0 + tok) * a.out_stride + (int64_t)head * D + d0;
 #pragma unroll
@@ -528,7 +530,7 @@ __global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1
         if (a.lse && tid % 16 == 0)
           a.lse[(w.t0 + tok) * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (top + __log2f(sum)) * LN2;
       } else {
-        const int64_t to = (part_slot(a, worker, entry, owner) * a.c.n_kv + h) * M + r;
+        const int64_t to = ((int64_t)slot * a.c.n_kv + h) * M + r;
 #pragma unroll
         for (int e = 0; e < VPL; e += 4) *(f32x4*)(a.part_o + to * D + d0 + e) = (f32x4){o[e], o[e + 1], o[e + 2], o[e + 3]};
         if (tid % 16 == 0) *(f32x2*)(a.part_ml + 2 * to) = (f32x2){top, sum};
@@ -607,7 +609,7 @@ __global__ __launch_bounds__(AT_THREADS) void split_join_kernel(const AttendArgs
   }
   const int worker = a.joins[2 * ((int64_t)entry * a.c.n_kv + h)], parts = a.joins[2 * ((int64_t)entry * a.c.n_kv + h) + 1];
   if (parts == 0) return;
-  join_row<D>(a, (part_slot(a, worker, entry, worker) * a.c.n_kv + h) * M + r, (int64_t)a.c.n_kv * M, parts, t + a.first_row, head);
+  join_row<D>(a, ((int64_t)part_slot(a, worker, entry, worker) * a.c.n_kv + h) * M + r, (int64_t)a.c.n_kv * M, parts, t + a.first_row, head);
 }
 
 template <int D>

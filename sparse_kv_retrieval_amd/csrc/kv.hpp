@@ -72,8 +72,8 @@ struct AttendArgs {
 // Where the part goes that `worker` has of row block `entry`, which worker `owner` begins. From a part to the next one the
 // worker grows (the same row block), or the row block does, and with it the owner: only the last row block that a
 // worker begins can have several parts. So neither sum is met twice; the one that needs less room is taken.
-__device__ __forceinline__ int64_t part_slot(const AttendArgs& a, int32_t worker, int32_t entry, int32_t owner) {
-  return (int64_t)worker + (a.entries < a.workers ? entry : owner);
+__device__ __forceinline__ int32_t part_slot(const AttendArgs& a, int32_t worker, int32_t entry, int32_t owner) {
+  return worker + (a.entries < a.workers ? entry : owner);
 }
 
 // Tiles of `tile` tokens that the rows at positions p_lo..p_hi see. Tile i < n_first is tile i of the
