@@ -116,7 +116,7 @@ __device__ __forceinline__ bf16x8 v_operand(const Tile<FP8, D>& t, int i) {
 }
 
 template <bool FP8, int D, int RT, bool LISTED>
-__global__ __launch_bounds__(AT_THREADS, RT == 1 || (D == 64 && RT == 2) ? 2 : 1) void attend_split_kernel(const AttendArgs a) {
+__global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void attend_split_kernel(const AttendArgs a) {
   using TileT = Tile<FP8, D>;
   constexpr int KS = D / 32, VPL = TileT::VPL, ROW = TileT::ROW, M = 16 * RT;
   constexpr int RUN = LISTED ? ATTEND_RESOLVED_LISTED : ATTEND_RESOLVED;

@@ -104,6 +104,10 @@ constexpr int ATTEND_TILE_KEYS = 64;        // keys of its tiles
 constexpr int ATTEND_RESOLVED = 64;         // tiles whose places a block of the split kernel holds at once
 constexpr int ATTEND_RESOLVED_LISTED = 16;  // the same over listed keys, each with a place of its own
 
+// Blocks of the split kernel that a compute unit holds: what a lane keeps of its rows grows with their number and with
+// the dimensions, and from 32 rows of 128 dimensions (or 64 of 64) on a wave needs a SIMD's registers.
+constexpr int attend_split_blocks(int rows, int d) { return rows * d >= 32 * 128 ? 1 : 2; }
+
 hipError_t launch_kv_append(const AppendArgs& a, bool fp8, int d, int style, hipStream_t s);
 hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_tiles, bool listed, hipStream_t s);
 hipError_t launch_attend_split_join(const AttendArgs& a, int d, int rows, bool listed, hipStream_t s);

@@ -709,20 +709,20 @@ struct SplitPlan {
   size_t bytes = 0;
 };
 
-// The blocks that share the tiles are as many as the device holds at once: one a CU where the rows' and a tile's
-// registers are many (four row tiles, or two of bf16, at d_h 128), two otherwise. More were slower on every
-// size tried (32 ragged sequences in e4m3: 401 us with 512, 407 with 1024, 416 with 2048; their windows of 1024:
+// The blocks that share the tiles are as many as the device holds at once, one or two for each of its 256 compute units.
+// Twice as many are slower (32 rows at d_h 128 in e4m3: one sequence of 131,072 tokens 67 us with 256 blocks and 76 with 512,
+// 32 of 2048 38 and 55), and so were more on every size tried (32 ragged sequences in e4m3: 401 us with 512, 407 with 1024, 416 with 2048; their windows of 1024:
 // 28.4, 32.9 and 37.1 us): they add partial results and a second round. Row blocks of at most four tiles, one
 // a wave, are not worth sharing. The workspace's size does not depend on the cache's dtype, and its partial results
 // are no more than two per worker.
-void share_tiles(SplitPlan* p, int32_t n_kv, int32_t d, bool fp8, int64_t tiles) {
+void share_tiles(SplitPlan* p, int32_t n_kv, int32_t d, int64_t tiles) {
   p->tiles = tiles;
   if (p->entries == 0 || tiles <= 4) return;
   // no worker has fewer than four tiles
   auto workers = [&](int64_t blocks) {
     return (int32_t)std::min<int64_t>(std::max<int64_t>(blocks / n_kv, 1), (p->entries * tiles + 3) / 4);
   };
-  p->workers = workers(p->rows * d * (fp8 ? 1 : 2) >= 64 * 128 ? 256 : 512);
+  p->workers = workers(256 * attend_split_blocks(p->rows, d));
   const size_t rows = (size_t)(workers(512) + std::min(p->entries, workers(512))) * n_kv * p->rows;
   p->ml = rows * d * 4;
   p->joins = p->ml + rows * 8;
@@ -767,7 +767,7 @@ struct RaggedPlan {
 };
 
 RaggedPlan plan_ragged(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, const int64_t* off, int32_t max_kv_len,
-                       int32_t window, int32_t sinks, bool fp8 = false) {
+                       int32_t window, int32_t sinks) {
   RaggedPlan r;
   const int64_t T = off[B] - off[0], G = n_q / n_kv;
   int64_t most = 0, many = 0;
@@ -784,7 +784,7 @@ RaggedPlan plan_ragged(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, const in
     const int64_t all = ((int64_t)max_kv_len + tile - 1) / tile;
     return window > 0 ? std::min(all, near_tiles((int64_t)window + rows - 1, sinks, tile)) : all;
   };
-  share_tiles(&r.few, n_kv, d, fp8, tiles(r.few.rows, 32));
+  share_tiles(&r.few, n_kv, d, tiles(r.few.rows, 32));
   split_keys(&r.many, many * n_kv, T, n_q, d, tiles(ATTEND_TILE_ROWS, ATTEND_TILE_KEYS));
   r.bytes = std::max(r.few.bytes, r.many.bytes);
   return r;
@@ -793,13 +793,13 @@ RaggedPlan plan_ragged(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, const in
 int64_t listed_tiles(int64_t k, int64_t entry_tokens) { return (k * entry_tokens + 31) / 32; }
 
 SplitPlan plan_listed(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t k, int32_t entry_tokens, int32_t window,
-                      int32_t sinks, bool fp8 = false) {
+                      int32_t sinks) {
   SplitPlan p;
   const int32_t G = n_q / n_kv;
   p.rows = G <= 16 ? 16 : G <= 32 ? 32 : 64;
   p.per = (G + p.rows - 1) / p.rows;
   p.entries = B * p.per;
-  share_tiles(&p, n_kv, d, fp8, near_tiles(window, sinks, 32) + listed_tiles(k, entry_tokens));
+  share_tiles(&p, n_kv, d, near_tiles(window, sinks, 32) + listed_tiles(k, entry_tokens));
   return p;
 }
 
@@ -939,7 +939,7 @@ lsa_status lsa_attend(const lsa_kv_cache* cache, int32_t B, const void* q, int64
   a.B = B; a.n_q = n_q; a.max_kv_len = max_kv_len; a.window = window; a.sinks = sinks; a.r = 1;
   if (a.T == 0) return LSA_OK;  // no rows: q and out may be NULL
   const int32_t d = cache->d_h;
-  const RaggedPlan p = plan_ragged(B, n_q, a.c.n_kv, d, q_offsets_host, max_kv_len, window, sinks, fp8);
+  const RaggedPlan p = plan_ragged(B, n_q, a.c.n_kv, d, q_offsets_host, max_kv_len, window, sinks);
   if ((s = attend_args(&a, p.bytes, d, q, q_stride, softmax_scale, out, out_stride, lse, workspace, workspace_bytes)) != LSA_OK)
     return s;
   if (!plan_fits(p.few, a) || !plan_fits(p.many, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows or keys for one call");
@@ -975,7 +975,7 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, 
   a.first_row = 0; a.T = B; a.B = B; a.n_q = n_q;
   // The workspace is laid out by the window as given, for its size is asked without a table; the tiles there are end
   // with the table.
-  SplitPlan p = plan_listed(B, n_q, a.c.n_kv, cache->d_h, k, entry_tokens, window, sinks, fp8);
+  SplitPlan p = plan_listed(B, n_q, a.c.n_kv, cache->d_h, k, entry_tokens, window, sinks);
   a.window = std::min(window, a.max_kv_len); a.sinks = std::min(sinks, a.max_kv_len);
   p.tiles = std::min(near_tiles(a.window, a.sinks, 32), ((int64_t)a.max_kv_len + 31) / 32) + listed_tiles(k, entry_tokens);
   if ((s = attend_args(&a, p.bytes, cache->d_h, q, q_stride, softmax_scale, out, out_stride, lse, workspace,

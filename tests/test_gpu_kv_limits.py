@@ -117,3 +117,23 @@ def test_parts_of_more_sequences_than_workers(torch, lsa, dtype, B):
     assert untouched(raw)
     check_rows(s, q, out, lse, [(b, b, totals[b] - 1) for b in range(B)], d ** -0.5, 100, 3, [sorted(set(x.tolist())) for x in idx], 4,
                n_q)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("new", [2, 4, 8], ids=lambda n: f"{8 * n}rows")
+def test_blocks_that_share_the_keys(torch, lsa, dtype, d, new):
+    """As many as the device holds at once, one or two a compute unit: with 8 key heads one long sequence has 32 or 64 parts a
+    head. The workspace ends with the pairs (first block, number of parts) that say so."""
+    n_q, n_kv = 64, 8
+    s = Setup(torch, lsa, [9000], dtype=dtype, n_kv=n_kv, d=d, pt=128, seed=new)
+    off = offsets([new])
+    q = bf16(torch, s.g, (new, n_q, d))
+    size = lsa.attend_workspace_size(s.cache, n_q=n_q, q_offsets_host=off, max_kv_len=9000)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    out, lse = run_attend(torch, lsa, s, q, off, ws=ws)
+    torch.cuda.synchronize()
+    pairs = ws[size - 8 * n_kv:].view(torch.int32).view(n_kv, 2).tolist()
+    most = 32 if 8 * new * d >= 32 * 128 else 64
+    assert all(first == 0 and most * 0.8 < parts <= most for first, parts in pairs), pairs
+    check_rows(s, q, out, lse, [(new - 1, 0, 8999)], d ** -0.5, n_q=n_q)
