@@ -617,6 +617,8 @@ lsa_status lsa_kv_append(const lsa_kv_cache* cache /* host */, int32_t B, const 
  * counts as max_kv_len. It must not exceed table_stride * page_tokens.
  * Precision: products of bf16 (e4m3 codes are exact in bf16) accumulate in fp32;
  * the softmax is fp32; probabilities are rounded to bf16 for the second product.
+ * The sum over V is divided at its end, so it may overflow where 256 * (seen keys) *
+ * (largest |V|) does.
  * The workspace holds lsa_attend_workspace_size(...) bytes of device memory for the
  * same sizes, 16-byte aligned (it may be NULL if that is 0); its contents on entry do
  * not matter. Calls that may overlap in time need workspaces of their own; so do

@@ -12,11 +12,15 @@
 // one that the registers hold is used. V^T's operand then wants, for each dimension, those eight
 // keys of a lane group: every lane loads the same D/16 dimensions of its group's eight rows and
 // transposes the small block in registers. Keys and values go from HBM to registers with no
-// exchange through LDS; nothing is read twice.
+// exchange through LDS, and no row block reads one twice (of listed entries with more than 64 query heads a key
+// head, each row block of 64 heads reads the rows again).
 //
 // Precision. q and bf16 keys enter the matrix cores as they are, e4m3 codes widen to bf16 exactly;
 // page scales multiply the fp32 score (keys) and the probability (values). The probability is
-// rounded once, to bf16, for the second product; sums and accumulators are fp32.
+// rounded once, to bf16, for the second product; sums and accumulators are fp32. bf16 because the values' operand is
+// bf16, and an fp32 probability would take a second product with what the rounding left. It costs as much as the output's own
+// rounding at most: outputs are off by 1.9 to 2.3e-3 of their norm against 64 bits, where the output's rounding alone
+// is 1.6 to 1.7e-3.
 //
 // The maximum follows the scores lazily: it is raised (and the accumulators rescaled) only when
 // some score exceeds it by 2^8. Probabilities then stay below 2^8, and no bit is lost in fp32 or
@@ -27,10 +31,12 @@
 // so ragged lengths balance; a second launch joins the parts of a row (see AttendArgs). A block's four
 // waves take its tiles in turn, with two or three of them in registers, and join through LDS.
 //
-// Measured on MI355X (64 query heads, 8 key heads, d_h 128): 8 x 125,000 tokens in bf16, 4.10 GB, 601 us
-// (6.8 TB/s); 32 ragged sequences of 4K to 128K in e4m3, 2.32 GB, 370 us (6.3 TB/s). Short calls are
+// Measured on MI355X (64 query heads, 8 key heads, d_h 128; the kernel's time in a trace): 8 x 125,000 tokens in bf16,
+// 4.10 GB, 602 us (6.8 TB/s); 32 ragged sequences of 4K to 128K in e4m3, 2.32 GB, 375 us (6.2 TB/s). Short calls are
 // bound by latency: finding the share, the page table, the rows and the queries are four dependent
-// reads, about 8 us with the launch, and the join about 4.5 us (one sequence of 4096 tokens: 7.9 + 5 us).
+// reads, about 8 us with the launch, and the join 4 to 5 us (one sequence of 4096 tokens: 8.2 + 5.1 us).
+// 33 to 64 rows (17 to 64 at d_h 128) take all registers, one wave a SIMD, and the bf16 instance of 64 at d_h 128 spills ten
+// (44 bytes of scratch a lane): 64 rows over 131,072 tokens in bf16 take 108 us (5.0 TB/s) where 16 rows take 93 (5.8).
 #include "kv.hpp"
 
 namespace lsa {

@@ -21,8 +21,9 @@
 // argument and costs nothing.
 //
 // Measured on MI355X (64 query heads, 8 key heads, d_h 128; torch's bf16 matrix product of 8192^3 reaches
-// 1269 TFLOP/s there): 2048 tokens on top of 30,720 in e4m3 2.1 ms (1.01 PFLOP/s); prompts of 4981 and 4888 tokens in
-// bf16 850 us (0.94 PFLOP/s); of 7203 and 6711 tokens with a window of 1024 600 us (0.73 PFLOP/s of visible pairs). The matrix
+// 1269 TFLOP/s there; the kernel's time in a trace): 2048 tokens on top of 30,720 in e4m3 2.1 ms (1.01 PFLOP/s); prompts of
+// 4981 and 4888 tokens in bf16 850 us (0.94 PFLOP/s); of 7203 and 6711 tokens with a window of 1024 593 us (0.73 PFLOP/s of
+// visible pairs). The matrix
 // pipes are busy 42 % of the time in the first, the vector ALUs about as long; without exponentials, LDS
 // reads, staging and maxima the second still takes 617 us. A block's first tile, its queries and its output
 // cost some 6 us that nothing overlaps, as one block fills a CU's registers and LDS: they are what

@@ -17,8 +17,9 @@
 // launch, each thread turning some heads with one set of angles.
 //
 // Measured on MI355X (64 query heads, 8 key heads, d_h 128): 13,612 new tokens of four prompts into e4m3 pages,
-// 530 MB read and written, 108 us, the rate of a plain copy (4.9 TB/s against 5.1); one token of 32 sequences
-// 6.0 us, which is launch and dependent reads (offsets, length, page, scale).
+// 530 MB read and written, 108 us, the rate of a plain copy (4.9 TB/s against 5.1), into bf16 pages 111 us (5.0 TB/s);
+// at d_h 64 54 us (4.9 TB/s) and 62 (4.5); one token of 32 sequences
+// 6.1 us, which is launch and dependent reads (offsets, length, page, scale).
 #include "kv.hpp"
 
 namespace lsa {

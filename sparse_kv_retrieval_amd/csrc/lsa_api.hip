@@ -652,7 +652,7 @@ namespace {
 // Limits of the paged-cache calls.
 constexpr int32_t kKvMaxB = 4096, kKvMaxHeads = 1024, kKvMaxGroup = 1024;
 constexpr int64_t kMaxBlocks = (1 << 24) - 1;          // of 256 threads: a launch has fewer than 2^32
-constexpr size_t kPartialBytes = (size_t)256 << 20;    // partial attention results of one call, about
+constexpr size_t kPartialBytes = (size_t)256 << 20;    // partial results of the tile kernel, where more than two splits fit
 
 bool multiple8(int64_t x) { return x % 8 == 0; }
 
@@ -710,11 +710,11 @@ struct SplitPlan {
 };
 
 // The blocks that share the tiles are as many as the device holds at once, one or two for each of its 256 compute units.
-// Twice as many are slower (32 rows at d_h 128 in e4m3: one sequence of 131,072 tokens 67 us with 256 blocks and 76 with 512,
-// 32 of 2048 38 and 55), and so were more on every size tried (32 ragged sequences in e4m3: 401 us with 512, 407 with 1024, 416 with 2048; their windows of 1024:
-// 28.4, 32.9 and 37.1 us): they add partial results and a second round. Row blocks of at most four tiles, one
-// a wave, are not worth sharing. The workspace's size does not depend on the cache's dtype, and its partial results
-// are no more than two per worker.
+// Twice as many add partial results and a second round: 32 rows at d_h 128 in e4m3 take 67 us with 256 blocks and 76 with
+// 512 over one sequence of 131,072 tokens, 38 and 55 over 32 of 2048. (8 rows, before loads were non-temporal: 32 ragged
+// sequences 401 us with 512, 407 with 1024, 416 with 2048; their windows of 1024 28.4, 32.9 and 37.1.) Row blocks of at
+// most four tiles, one a wave, are not worth sharing. The workspace's size does not depend on the cache's dtype, and its
+// partial results are no more than two per worker.
 void share_tiles(SplitPlan* p, int32_t n_kv, int32_t d, int64_t tiles) {
   p->tiles = tiles;
   if (p->entries == 0 || tiles <= 4) return;
@@ -757,7 +757,13 @@ void split_keys(TilePlan* p, int64_t filled, int64_t T, int32_t n_q, int32_t d, 
 }
 
 // Sequences with at most this many rows (new tokens times query heads of a group) go to the split
-// kernel, whose waves share no keys, the others to the tile kernel.
+// kernel, whose waves share no keys, the others to the tile kernel, which pads them to 256. 64 is all that the split
+// kernel's registers hold. Measured on both sides with 8 key heads of 8 query heads, d_h 128 (split and tile kernel, us):
+//   one sequence of 131,072 tokens, bf16   24 rows 96 and 168, 64 rows 108 and 165   (72 rows: 172, tile)
+//                                   e4m3   24 rows 66 and 165, 64 rows 87 and 158    (72 rows: 165, tile)
+//   32 sequences of 2048 tokens,    bf16   24 rows 54 and 132, 64 rows 66 and 85     (72 rows: 89, tile)
+//                                   e4m3   24 rows 38 and 137, 64 rows 52 and 83     (72 rows: 85, tile)
+// With one key head of 64 and 32 short sequences the two are even (bf16 26 and 24, e4m3 23 and 23).
 constexpr int64_t kSplitRows = 64;
 
 struct RaggedPlan {
