@@ -106,8 +106,8 @@ def test_captured_step(torch):
 
 
 def test_step_on_a_given_stream_waits_for_nothing(torch):
-    """Steps on a stream that the current one does not wait for, given as a stream and as its address; the host enqueues them while
-    the stream is still busy."""
+    """Steps on a stream of their own, given as a stream and as its address; the host enqueues them while it is still
+    busy."""
     P.say("[steps] own stream")
     w, (p, clean), hs, qkv = setup(torch, "bf16")
     stream = torch.cuda.Stream()
@@ -115,7 +115,7 @@ def test_step_on_a_given_stream_waits_for_nothing(torch):
     torch.cuda.synchronize()
     busy = torch.zeros((8192, 8192), device="cuda")
     with torch.cuda.stream(stream):
-        for _ in range(8):  # some ten milliseconds
+        for _ in range(24):  # some tenths of a second; four steps take the host about a millisecond
             busy = (busy @ busy) * 0
         done = torch.cuda.Event()
         done.record()
