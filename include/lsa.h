@@ -35,6 +35,12 @@
  *   lsa_attend_topk    attention of one token per sequence over the entries the
  *                      native top-k listed, the window and the first tokens
  *                                       [BLOG] §2.2, [HYPER] 方法 (C^CoreComp)
+ *   lsa_attend_ex, lsa_attend_topk_ex   the same with capped or distance-biased
+ *                      scores, and (the first) documents and prefixes as masks
+ *   lsa_kv_kept, lsa_kv_compact   the listed tokens of a cache, dense in other
+ *                      pages: C^MemComp as a cache   [HYPER] 方法 (load C^MemComp)
+ *   lsa_kv_extend, lsa_kv_fork, lsa_kv_free   pages taken from a pool, shared
+ *                      between sequences and given back
  *
  * Conventions shared by every call:
  *  - Ownership: the caller allocates every buffer. Pointers marked "dev" are
@@ -666,6 +672,151 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache /* host */, int32_t B, cons
                            float softmax_scale, int32_t window, int32_t sinks, void* out /* dev */,
                            int64_t out_stride, float* lse /* dev or NULL */, void* workspace /* dev */,
                            size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * lsa_attend_ex, lsa_attend_topk_ex: lsa_attend and lsa_attend_topk with other
+ * scores and masks. form == NULL, or one whose fields are all 0, is the plain
+ * call.
+ *
+ * Scores: y = softmax_scale * q . K_s; where softcap > 0 it becomes
+ * softcap * tanh(y / softcap); where slopes is set, query head i then loses
+ * slopes[i] * |p - s| for the query at position p. out and lse are of these
+ * scores. Positions are places in the cache (as for the window), and slopes must
+ * be finite; negative ones are allowed.
+ * Masks (lsa_attend_ex only), by rows of q: a row sees position s only if
+ * s >= doc_start[row], and s <= p or s < prefix_end[row], where doc_start and
+ * prefix_end are set. The window and the first tokens restrict it as before: the
+ * sinks are the sequence's first tokens, not the document's. Only cached
+ * positions s < kv_len are seen, wherever prefix_end lies; a negative doc_start
+ * is 0.
+ * So documents packed into one sequence have their first position as doc_start
+ * of each row (and their last + 1 as prefix_end where they see themselves in both
+ * directions), and a prompt's prefix of n tokens has prefix_end n in every row.
+ *
+ * Everything else is as for the plain calls, whose workspaces of the same sizes
+ * they take. Precision: the capped score is formed in fp32, off by about
+ * 2^-22 softcap; the bias is added in fp32, off by 2^-23 of its size.
+ * Supported: as the plain calls; softcap 0 or in [2^-10, 1024]; prefix_end only
+ * without a window; lsa_attend_topk_ex takes neither doc_start nor prefix_end.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  float softcap;              /* 0: none */
+  const float* slopes;        /* dev [n_q] fp32, or NULL */
+  const int32_t* doc_start;   /* dev [rows] by rows of q, or NULL */
+  const int32_t* prefix_end;  /* dev [rows] by rows of q, or NULL */
+} lsa_attend_form;
+
+lsa_status lsa_attend_ex(const lsa_kv_cache* cache /* host */, int32_t B, const void* q /* dev */, int64_t q_stride,
+                         int32_t n_q, const int64_t* q_offsets /* dev [B+1] */,
+                         const int64_t* q_offsets_host /* host [B+1] */, int32_t max_kv_len, float softmax_scale,
+                         int32_t window, int32_t sinks, const lsa_attend_form* form /* host, or NULL */,
+                         void* out /* dev */, int64_t out_stride, float* lse /* dev or NULL */,
+                         void* workspace /* dev */, size_t workspace_bytes, hipStream_t stream);
+lsa_status lsa_attend_topk_ex(const lsa_kv_cache* cache /* host */, int32_t B, const void* q /* dev */,
+                              int64_t q_stride, int32_t n_q, const int32_t* idx /* dev [B, k] */,
+                              const int32_t* count /* dev [B] */, int32_t k, int32_t entry_tokens,
+                              float softmax_scale, int32_t window, int32_t sinks,
+                              const lsa_attend_form* form /* host, or NULL */, void* out /* dev */,
+                              int64_t out_stride, float* lse /* dev or NULL */, void* workspace /* dev */,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * lsa_kv_kept, lsa_kv_compact: the tokens worth keeping, dense in other pages.
+ *
+ * Sequence b keeps position s < kv_len[b] if s's entry is listed, or
+ * s >= kv_len[b] - window, or s < sinks (window == 0 is no window): what
+ * lsa_attend_topk would see. Its list is the first count[b] values of idx from
+ * idx_offsets[b] on, strictly ascending and not negative, as lsa_union_compact
+ * writes them; entry e covers positions e * entry_tokens .. + entry_tokens - 1.
+ *
+ * lsa_kv_kept writes the number of kept positions of each sequence to kept_out,
+ * which may serve as the kv_len of the destination.
+ *
+ * lsa_kv_compact copies them: in each layer l, the i-th kept position of
+ * sequence b goes to position i of row b of the destination to[l]. All layers
+ * share the list and from[0]'s (to[0]'s) page_table and kv_len; those and all
+ * sizes must be equal in from (in to). kv_len of the destination is not read.
+ * max_kept bounds the kept positions of a sequence on the host (for the launch's
+ * shape); those beyond it are not copied. It must not exceed the destination's
+ * table_stride * page_tokens. Pages of the destination must not be pages of the
+ * source that the call reads. What the cache holds of positions whose source or
+ * destination page is not there, and slots behind the last kept one, stay as
+ * they are.
+ * bf16 is copied bit for bit. e4m3: per page and key head of the destination the
+ * scale becomes the least power of two (at least 2^-118) with |x| <= 448 scale
+ * for every finite x = code * old scale that goes there, and codes are stored as
+ * e4m3(x / scale), to nearest even (x formed in fp32; NaN, and x beyond fp32, as
+ * NaN). A code whose page's scale was the same stays the same.
+ * Supported: 1 <= B <= 4096; 1 <= L <= 1024; dtype, d_h and n_kv equal in from
+ * and to; page_tokens may differ; 1 <= entry_tokens <= 128; the pages that
+ * max_kept takes, times B and 2 n_kv, at most 2^24 - 1.
+ * ---------------------------------------------------------------------- */
+lsa_status lsa_kv_kept(const lsa_kv_cache* from /* host */, int32_t B, const int32_t* idx /* dev */,
+                       const int64_t* idx_offsets /* dev [B] */, const int32_t* count /* dev [B] */,
+                       int32_t entry_tokens, int32_t window, int32_t sinks, int32_t* kept_out /* dev [B] */,
+                       hipStream_t stream);
+lsa_status lsa_kv_compact(const lsa_kv_cache* from /* host [L] */, const lsa_kv_cache* to /* host [L] */, int32_t L,
+                          int32_t B, const int32_t* idx /* dev */, const int64_t* idx_offsets /* dev [B] */,
+                          const int32_t* count /* dev [B] */, int32_t entry_tokens, int32_t window, int32_t sinks,
+                          int32_t max_kept, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * lsa_kv_extend, lsa_kv_fork, lsa_kv_free: sequences share a pool of pages.
+ *
+ * refs[page] counts the table entries that hold the page; a page with 0 (or
+ * less) is free. Row b of page_table holds the pages of its first
+ * ceil(kv_len[b] / page_tokens) entries (at most table_stride); of those, an
+ * entry outside [0, n_pages) holds none. Entries behind them are not read. The
+ * caller sets up refs, page_table and kv_len once (all 0, -1 and 0: an empty
+ * pool) and from then on these calls keep them; lsa_kv_append and the attention
+ * read the same page_table and kv_len. Pages are taken in ascending order of
+ * their numbers, so results do not depend on timing. Calls on one pool must be
+ * ordered on a stream.
+ *
+ * lsa_kv_extend: sequence b grows by n_new[b] tokens (a negative number is 0):
+ * it takes pages for the entries that its new length needs, and kv_len[b] becomes
+ * kv_len[b] + n_new[b] (a negative kv_len counts as 0). Pages are given out in the
+ * order of the sequences: from the first one on for which the free pages do not
+ * suffice, every one that needs a page stays as it was. missing_out[b] (if not
+ * NULL) receives 0, or the number of pages that such a sequence asked for, or -1
+ * where the table's row is too short (it stays as it was and asks for none).
+ *
+ * lsa_kv_fork: for each i < n, sequence dst[i] gives its pages back and becomes a
+ * copy of sequence src[i]: it shares the full pages, and where src's last page is not
+ * full, takes a page and copies the used slots of every layer's k and v to it (with the
+ * scales of an e4m3 cache). status_out[i] receives 0; or 1 where no page
+ * was free, and then dst[i] has the full pages' tokens only; or -1 where the pair
+ * was refused and nothing was done for it: a number outside [0, B), a dst that is
+ * among the srcs, or a dst that came before. Free pages go to the pairs in their order.
+ * The workspace holds lsa_kv_fork_workspace_size(n) bytes, 16-byte aligned; its
+ * contents on entry do not matter.
+ *
+ * lsa_kv_free: each of the n sequences seqs[i] gives its pages back: their refs
+ * fall by one, its entries become -1 and its kv_len 0. Numbers outside [0, B) and
+ * those that came before are skipped.
+ *
+ * Supported: 1 <= B <= 4096, 1 <= n <= 4096 (n == 0 does nothing), 1 <= L <= 1024
+ * layers, whose caches have the pool's page_tokens and n_pages and equal n_kv,
+ * d_h and dtype (their own page_table and kv_len are not read); n * 2 n_kv * min(L, 16) at
+ * most 2^24 - 1; refs 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t* refs;        /* dev [n_pages] */
+  int32_t* page_table;  /* dev [B, table_stride] */
+  int32_t* kv_len;      /* dev [B] */
+  int64_t table_stride;
+  int32_t B, n_pages, page_tokens;
+} lsa_kv_pool;
+
+lsa_status lsa_kv_extend(const lsa_kv_pool* pool /* host */, const int32_t* n_new /* dev [B] */,
+                         int32_t* missing_out /* dev [B] or NULL */, hipStream_t stream);
+size_t lsa_kv_fork_workspace_size(int32_t n);
+lsa_status lsa_kv_fork(const lsa_kv_pool* pool /* host */, const lsa_kv_cache* layers /* host [L] */, int32_t L,
+                       int32_t n, const int32_t* src /* dev [n] */, const int32_t* dst /* dev [n] */,
+                       int32_t* status_out /* dev [n] */, void* workspace /* dev */, size_t workspace_bytes,
+                       hipStream_t stream);
+lsa_status lsa_kv_free(const lsa_kv_pool* pool /* host */, int32_t n, const int32_t* seqs /* dev [n] */,
+                       hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * lsa_debug_range_errors: in a debug build (compiled with LSA_DEBUG_CHECKS=1),

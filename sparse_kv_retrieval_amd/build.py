@@ -8,11 +8,12 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ["score.hip", "score_stream.hip", "union.hip", "topk.hip", "gather.hip", "project.hip", "golden.hip",
-           "train.hip", "kv_append.hip", "attend.hip", "attend_tile.hip", "lsa_api.hip"]
+           "train.hip", "kv_append.hip", "kv_compact.hip", "kv_pages.hip", "attend.hip", "attend_tile.hip", "lsa_api.hip"]
 OUT = os.path.join(HERE, "liblsa.so")
 # the streaming-read reference of the rooflines: a separate library, not part of lsa.h
 PROBE_SOURCE = "probe.hip"
@@ -26,32 +27,41 @@ HIPCC_FLAGS = [
     # MFMA results in ordinary VGPRs: the epilogues read them without v_accvgpr_read copies
     "-mllvm", "-amdgpu-mfma-vgpr-form=1",
 ]
-SOURCE_FLAGS: dict = {}  # per-source additions to HIPCC_FLAGS
+# Objects that are not their source alone: the attention's further forms (enum Form in kv.hpp)
+FORM_OBJECTS = {f"{s}_form{f}": (s + ".hip", [f"-DATTEND_FORM={f}"]) for s in ("attend", "attend_tile") for f in (1, 2, 4, 6)}
 _NOISE = "is not a recognized feature for this target"
 
 
 def _run(cmds, verbose):
-    procs = []
-    for cmd in cmds:
+    def one(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
-        procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True))
-    for cmd, p in zip(cmds, procs):
-        _, err = p.communicate()
-        err = "\n".join(ln for ln in (err or "").splitlines() if _NOISE not in ln)
+        p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+        err = "\n".join(ln for ln in (p.stderr or "").splitlines() if _NOISE not in ln)
         if p.returncode != 0:
             raise RuntimeError(f"hipcc failed ({p.returncode}): {' '.join(cmd)}\n{err}")
         if err.strip() and verbose:
             print(err, file=sys.stderr)
+
+    with ThreadPoolExecutor(min(len(cmds), os.cpu_count() or 1, 16)) as pool:
+        list(pool.map(one, cmds))
+
+
+def _objects(without=()) -> dict:
+    """Object file -> (source, flags of its own) of everything in liblsa.so, except of the sources `without`."""
+    of = {s.replace(".hip", ""): (s, []) for s in SOURCES}
+    of.update(FORM_OBJECTS)
+    return {os.path.join(BUILD_DIR, name + ".o"): x for name, x in of.items() if x[0] not in without}
 
 
 def build(verbose: bool = False) -> str:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     os.makedirs(BUILD_DIR, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include")]
-    objs = [os.path.join(BUILD_DIR, s.replace(".hip", ".o")) for s in SOURCES]
-    _run([[hipcc, *HIPCC_FLAGS, *SOURCE_FLAGS.get(s, []), *inc, "-c", os.path.join(HERE, "csrc", s), "-o", o]
-          for s, o in zip(SOURCES, objs)], verbose)
+    objs = _objects()
+    # the longest ones first: they are as many as the machine's cores or more
+    _run([[hipcc, *HIPCC_FLAGS, *flags, *inc, "-c", os.path.join(HERE, "csrc", s), "-o", o]
+          for o, (s, flags) in sorted(objs.items(), key=lambda x: -len(x[1][1]))], verbose)
     tmp = OUT + ".tmp"
     ptmp = PROBE_OUT + ".tmp"
     _run([[hipcc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp],
@@ -73,7 +83,7 @@ SAN_FLAGS = ["-O1", "-g", "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-
 def build_sanitized_host(verbose: bool = False) -> str:
     """Build <SAN_DIR>/sparse_kv_retrieval_amd (liblsa.so with a sanitized host layer, and the binding)."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    objs = [os.path.join(BUILD_DIR, s.replace(".hip", ".o")) for s in SOURCES if s != "lsa_api.hip"]
+    objs = list(_objects(without=["lsa_api.hip"]))
     if not all(os.path.exists(o) for o in objs):
         build(verbose)
     pkg = os.path.join(SAN_DIR, "sparse_kv_retrieval_amd")
@@ -100,7 +110,7 @@ DEBUG_SOURCES = ["score.hip", "gather.hip", "lsa_api.hip"]
 def build_debug(verbose: bool = False) -> str:
     """Build <DEBUG_DIR>/sparse_kv_retrieval_amd (liblsa.so with the device range checks, and the binding)."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    objs = [os.path.join(BUILD_DIR, s.replace(".hip", ".o")) for s in SOURCES if s not in DEBUG_SOURCES]
+    objs = list(_objects(without=DEBUG_SOURCES))
     if not all(os.path.exists(o) for o in objs):
         build(verbose)
     pkg = os.path.join(DEBUG_DIR, "sparse_kv_retrieval_amd")

@@ -121,14 +121,16 @@ __device__ __forceinline__ bf16x8 v_operand(const Tile<FP8, D>& t, int i) {
   }
 }
 
-template <bool FP8, int D, int RT, bool LISTED>
+template <bool FP8, int D, int RT, bool LISTED, int FORM>
 __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void attend_split_kernel(const AttendArgs a) {
   using TileT = Tile<FP8, D>;
   constexpr int KS = D / 32, VPL = TileT::VPL, ROW = TileT::ROW, M = 16 * RT;
   constexpr int RUN = LISTED ? ATTEND_RESOLVED_LISTED : ATTEND_RESOLVED;
   constexpr int DEPTH = (FP8 || D == 64) && RT <= 2 && !LISTED ? 3 : 2;
   constexpr int PLACES = LISTED ? 32 : 2;  // places resolved per tile: single keys, or 16 in a row
+  constexpr bool SEEN = (FORM & FORM_SEEN) != 0, CAP = (FORM & FORM_CAP) != 0, BIAS = (FORM & FORM_BIAS) != 0;
   __shared__ int64_t s_row[RUN * PLACES];  // cached row of the place, or -1: nothing there
+  __shared__ int32_t s_tok[LISTED && BIAS ? RUN * PLACES : 1];  // position of the place
   __shared__ float s_o[AT_WAVES][M][D + 4];
   __shared__ float s_m[AT_WAVES][M], s_l[AT_WAVES][M];
 
@@ -143,13 +145,13 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
   // least one tile, so that someone writes the rows that see nothing.
   int chunk = 0, upto = 0, before = 0, at = 0, end = 0, share = 1, mine_tiles = 0;
   bool whole = false;
-  Seq mine{0, 0, 0, 0};  // row block chunk + lane
+  Seq mine{};  // row block chunk + lane
   auto look = [&]() {
     const int e = chunk + lane;
     mine_tiles = 0;
-    if (e < a.entries && entry_seq<LISTED>(a, e, &mine)) {
+    if (e < a.entries && entry_seq<LISTED, FORM>(a, e, &mine)) {
       Rows w;
-      set_entry<LISTED>(a, e, mine, M, &w);
+      set_entry<LISTED, FORM>(a, e, mine, M, &w);
       mine_tiles = max(w.tiles, 1);
     }
   };
@@ -189,10 +191,13 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
     }
     const int which = __ffsll((unsigned long long)__ballot(before + upto > at)) - 1;
     entry = uni(chunk + which);
-    const Seq s = {__builtin_amdgcn_readlane(mine.n_tok, which), __builtin_amdgcn_readlane(mine.len, which),
-                   __builtin_amdgcn_readlane(mine.listed, which), __builtin_amdgcn_readlane(mine.row, which)};
-    set_entry<LISTED>(a, entry, s, M, &w);
-    pin_rows(&w);
+    auto of = [&](int x) { return __builtin_amdgcn_readlane(x, which); };
+    Seq s{of(mine.n_tok), of(mine.len), of(mine.listed), of(mine.row), 0, 0, 0, 0};
+    if constexpr (SEEN) {
+      s.f_lo = of(mine.f_lo); s.f_hi = of(mine.f_hi); s.e_lo = of(mine.e_lo); s.e_hi = of(mine.e_hi);
+    }
+    set_entry<LISTED, FORM>(a, entry, s, M, &w);
+    pin_rows<FORM>(&w);
     const int last = before + __builtin_amdgcn_readlane(upto, which), n = max(w.tiles, 1);
     int owner, parts;  // owner: the worker that begins this row block
     if (whole) {
@@ -218,9 +223,9 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
     count = min(count, w.tiles - first);  // 0 where nothing is seen
   } else {
     Seq s;
-    if (again || !entry_seq<LISTED>(a, entry, &s)) return;
-    set_entry<LISTED>(a, entry, s, M, &w);
-    pin_rows(&w);
+    if (again || !entry_seq<LISTED, FORM>(a, entry, &s)) return;
+    set_entry<LISTED, FORM>(a, entry, s, M, &w);
+    pin_rows<FORM>(&w);
     count = w.tiles;
   }
   if (again) __syncthreads();
@@ -259,7 +264,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
       } else {
         tok = w.near.tile(tile) * 32 + (i % 2) * 16;
         // no row sees any of the 16: the page may not be the sequence's any more
-        if (tok > w.p_hi || (tok + 15 <= w.w_lo && tok >= a.sinks)) tok = -1;
+        if (tok > end_hi<FORM>(w) || !some_begin<FORM>(a, w, tok, tok + 15)) tok = -1;
       }
       int64_t row = -1;
       if (tok >= 0) {
@@ -270,6 +275,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
         }
       }
       s_row[i] = row;
+      if constexpr (LISTED && BIAS) s_tok[i] = tok;
     }
   };
 
@@ -277,7 +283,8 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
   resolve(first, min(RUN, count));
   // the block's queries: lane column = row
   bf16x8 q[RT][KS];
-  int32_t p_row[RT], w_row[RT];
+  int32_t p_row[RT], w_row[RT], f_row[SEEN ? RT : 1], e_row[SEEN ? RT : 1];
+  float slope[BIAS ? RT : 1];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int r = rt * 16 + col;
@@ -286,6 +293,11 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
     const int tok = row / a.G;
     p_row[rt] = w.p0 + tok;
     w_row[rt] = window_start(a, p_row[rt]);
+    if constexpr (SEEN) {
+      f_row[rt] = first_seen(a, w.t0 + tok);
+      e_row[rt] = last_seen(a, w.t0 + tok, p_row[rt], w.len);
+    }
+    if constexpr (BIAS) slope[rt] = a.slopes[h * a.G + (row - tok * a.G)] * LOG2E;
     const uint16_t* src = a.q + (w.t0 + tok) * a.q_stride + (int64_t)(h * a.G + (row - tok * a.G)) * D;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -359,9 +371,23 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
         for (int j = 0; j < 4; ++j) {
           float f = a.scale_log2;
           if constexpr (FP8) f *= LISTED ? ks[4 * sub + j] : t.scale[sub];
-          x[rt][4 * sub + j] = s[rt][j] * f;
+          float y = s[rt][j] * f;
+          if constexpr (CAP) y = cap_score(a, y);
+          x[rt][4 * sub + j] = y;
         }
     }
+    if constexpr (BIAS) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = 16 * (j / 4) + 4 * g + j % 4, tok = LISTED ? s_tok[32 * i + at] : w.near.tile(base + i) * 32 + at;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) x[rt][j] = __builtin_fmaf(-slope[rt], fabsf((float)(p_row[rt] - tok)), x[rt][j]);
+      }
+    }
+    auto sees = [&](int rt, int tok) {
+      if constexpr (SEEN) return tok <= e_row[rt] && tok >= f_row[rt] && (tok > w_row[rt] || tok < a.sinks);
+      else return tok <= p_row[rt] && (tok > w_row[rt] || tok < a.sinks);
+    };
     // masks
     bool rescue = false;
     if constexpr (LISTED) {
@@ -376,21 +402,17 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
     } else {
       const int t0 = w.near.tile(base + i) * 32;
       const bool here0 = uni(s_row[2 * i]) >= 0, here1 = uni(s_row[2 * i + 1]) >= 0;
-      const bool whole = here0 && here1 && t0 + 31 <= w.p_lo &&
-                         (t0 > w.w_hi || t0 + 31 < a.sinks);
+      const bool whole = here0 && here1 && t0 + 31 <= end_lo<FORM>(w) && all_begin<FORM>(a, w, t0, t0 + 31);
       if (!whole) {
         uint32_t odd = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int tok = t0 + 16 * (j / 4) + 4 * g + j % 4;
           const bool here = j < 4 ? here0 : here1;
-          const bool some = here && tok <= w.p_hi &&
-                            (tok > w.w_lo || tok < a.sinks);
+          const bool some = here && tok <= end_hi<FORM>(w) && some_begin<FORM>(a, w, tok, tok);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            const bool seen = here && tok <= p_row[rt] &&
-                              (tok > w_row[rt] || tok < a.sinks);
-            x[rt][j] = seen ? x[rt][j] : -__builtin_inff();
+            x[rt][j] = here && sees(rt, tok) ? x[rt][j] : -__builtin_inff();
           }
 #pragma unroll
           for (int e = 0; e < TileT::VB / 4; ++e) {
@@ -461,7 +483,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
               const float y = cached_value<FP8>(src, VPL * (4 * g + c) + e);
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt)
-                if (tok <= p_row[rt] && (tok > w_row[rt] || tok < a.sinks) && !(fabsf(y) < __builtin_inff())) acc[rt][e][c] += y;
+                if (sees(rt, tok) && !(fabsf(y) < __builtin_inff())) acc[rt][e][c] += y;
             }
             __builtin_amdgcn_sched_barrier(0);  // rare: keep its registers few
           }
@@ -618,7 +640,7 @@ __global__ __launch_bounds__(AT_THREADS) void split_join_kernel(const AttendArgs
   join_row<D>(a, ((int64_t)part_slot(a, worker, entry, worker) * a.c.n_kv + h) * M + r, (int64_t)a.c.n_kv * M, parts, t + a.first_row, head);
 }
 
-template <int D>
+template <int D, int FORM>
 __global__ __launch_bounds__(AT_THREADS) void tile_join_kernel(const AttendArgs a, int64_t from) {
   const int64_t id = from + (int64_t)blockIdx.x * AT_WAVES + (threadIdx.x >> 6);
   if (id >= a.T * a.n_q) return;
@@ -631,30 +653,41 @@ __global__ __launch_bounds__(AT_THREADS) void tile_join_kernel(const AttendArgs 
   const int64_t n_tok = a.off[w.b + 1] - w.t0;
   if (!of_class(a, n_tok)) return;
   const int64_t row = (t + a.first_row - w.t0) * a.G + head % a.G;
-  set_block(a, seq_of<false>(a, w.b, w.t0, n_tok), (int32_t)(row / ATTEND_TILE_ROWS), &w);
+  set_block<FORM>(a, seq_of<false>(a, w.b, w.t0, n_tok), (int32_t)(row / ATTEND_TILE_ROWS), &w);
   const int parts = (w.tiles + a.run - 1) / a.run;
   if (parts > 1) join_row<D>(a, id, a.T * a.n_q, parts, t + a.first_row, head);
 }
 
-template <bool FP8, int D, bool LISTED>
+template <bool FP8, int D, bool LISTED, int FORM>
 static hipError_t launch_rows(const AttendArgs& a, int row_tiles, hipStream_t s) {
   const dim3 grid((unsigned)((a.workers > 0 ? a.workers : a.entries) * (int64_t)a.c.n_kv));
-  if (row_tiles == 1) attend_split_kernel<FP8, D, 1, LISTED><<<grid, AT_THREADS, 0, s>>>(a);
-  else if (row_tiles == 2) attend_split_kernel<FP8, D, 2, LISTED><<<grid, AT_THREADS, 0, s>>>(a);
-  else attend_split_kernel<FP8, D, 4, LISTED><<<grid, AT_THREADS, 0, s>>>(a);
+  if (row_tiles == 1) attend_split_kernel<FP8, D, 1, LISTED, FORM><<<grid, AT_THREADS, 0, s>>>(a);
+  else if (row_tiles == 2) attend_split_kernel<FP8, D, 2, LISTED, FORM><<<grid, AT_THREADS, 0, s>>>(a);
+  else attend_split_kernel<FP8, D, 4, LISTED, FORM><<<grid, AT_THREADS, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <bool LISTED>
+template <bool LISTED, int FORM>
 static hipError_t launch_dim(const AttendArgs& a, bool fp8, int d, int row_tiles, hipStream_t s) {
-  if (d == 64) return fp8 ? launch_rows<true, 64, LISTED>(a, row_tiles, s) : launch_rows<false, 64, LISTED>(a, row_tiles, s);
-  return fp8 ? launch_rows<true, 128, LISTED>(a, row_tiles, s) : launch_rows<false, 128, LISTED>(a, row_tiles, s);
+  if (d == 64) return fp8 ? launch_rows<true, 64, LISTED, FORM>(a, row_tiles, s) : launch_rows<false, 64, LISTED, FORM>(a, row_tiles, s);
+  return fp8 ? launch_rows<true, 128, LISTED, FORM>(a, row_tiles, s) : launch_rows<false, 128, LISTED, FORM>(a, row_tiles, s);
 }
 
+// Listed positions are seen for what they are: there, forms with SEEN alone do not exist, and the others go without it.
+template <int FORM>
 hipError_t launch_attend_split(const AttendArgs& a, bool fp8, int d, int row_tiles, bool listed, hipStream_t s) {
-  return listed ? launch_dim<true>(a, fp8, d, row_tiles, s) : launch_dim<false>(a, fp8, d, row_tiles, s);
+  if (!listed) return launch_dim<false, FORM ? FORM | FORM_SEEN : FORM_PLAIN>(a, fp8, d, row_tiles, s);
+  if constexpr (FORM == FORM_SEEN) return hipErrorInvalidValue;
+  else return launch_dim<true, FORM>(a, fp8, d, row_tiles, s);
 }
 
+// One object of this file for each form, so that they are compiled side by side; the first has the joins.
+#ifndef ATTEND_FORM
+#define ATTEND_FORM 0
+#endif
+template hipError_t launch_attend_split<ATTEND_FORM>(const AttendArgs&, bool, int, int, bool, hipStream_t);
+
+#if ATTEND_FORM == 0
 // One wave per row and head, in launches of at most `most` blocks each: a launch has fewer than 2^32 threads.
 template <typename F>
 static hipError_t launch_joins(const AttendArgs& a, F launch) {
@@ -680,11 +713,17 @@ hipError_t launch_attend_split_join(const AttendArgs& a, int d, int M, bool list
   });
 }
 
-hipError_t launch_attend_tile_join(const AttendArgs& a, int d, hipStream_t s) {
+hipError_t launch_attend_tile_join(const AttendArgs& a, int d, bool seen, hipStream_t s) {
   return launch_joins(a, [&](dim3 grid, int64_t from) {
-    if (d == 64) tile_join_kernel<64><<<grid, AT_THREADS, 0, s>>>(a, from);
-    else tile_join_kernel<128><<<grid, AT_THREADS, 0, s>>>(a, from);
+    if (seen) {
+      if (d == 64) tile_join_kernel<64, FORM_SEEN><<<grid, AT_THREADS, 0, s>>>(a, from);
+      else tile_join_kernel<128, FORM_SEEN><<<grid, AT_THREADS, 0, s>>>(a, from);
+    } else {
+      if (d == 64) tile_join_kernel<64, FORM_PLAIN><<<grid, AT_THREADS, 0, s>>>(a, from);
+      else tile_join_kernel<128, FORM_PLAIN><<<grid, AT_THREADS, 0, s>>>(a, from);
+    }
   });
 }
+#endif
 
 }  // namespace lsa

@@ -75,13 +75,14 @@ __device__ __forceinline__ void split_scale(float s, float* pow2, float* rest) {
   *rest = s * __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
-template <bool FP8, int D>
+template <bool FP8, int D, int FORM>
 __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const AttendArgs a) {
   constexpr int CPR = D / 8;                  // 16-byte chunks of a row in LDS
   constexpr int SRC = FP8 ? D / 16 : D / 8;   // and of a cached row
   constexpr int LOADS = SRC / 4;              // 16-byte loads per lane of 16 rows
   constexpr int ROWB = 2 * D;                 // bytes of a row in LDS
   constexpr int KS = D / 16, DT = D / 32;
+  constexpr bool SEEN = (FORM & FORM_SEEN) != 0, CAP = (FORM & FORM_CAP) != 0, BIAS = (FORM & FORM_BIAS) != 0;
   __shared__ __attribute__((aligned(16))) char s_k[TL_BUFS][TL_N * ROWB], s_v[TL_BUFS][TL_N * ROWB];
   // what is left of the scales of 16 keys: of K times c, of V as log2 and reciprocal
   __shared__ __attribute__((aligned(16))) float s_kc[TL_BUFS][TL_SUBS], s_vlog[TL_BUFS][TL_SUBS], s_vinv[TL_BUFS][TL_SUBS];
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   const int split = (int)((id / a.c.n_kv) % a.splits);
   // the last row blocks see the most keys: they go first
   Rows w;
-  if (!find_rows(a, a.blocks - 1 - id / ((int64_t)a.c.n_kv * a.splits), &w)) return;
+  if (!find_rows<FORM>(a, a.blocks - 1 - id / ((int64_t)a.c.n_kv * a.splits), &w)) return;
   const int parts = (w.tiles + a.run - 1) / a.run;
   if (split > 0 && split >= parts) return;
   const int first = split * a.run, count = min(a.run, w.tiles - first);
@@ -107,6 +108,9 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   const int r = wave * 32 + col;
   const int row = w.r0 + min(r, w.n - 1), tok = row / a.G, head = kv * a.G + (row - tok * a.G);
   const int p_row = w.p0 + tok, w_row = window_start(a, p_row);
+  const int f_row = SEEN ? first_seen(a, w.t0 + tok) : 0;
+  const int e_row = SEEN ? last_seen(a, w.t0 + tok, p_row, w.len) : p_row;
+  const float slope = BIAS ? a.slopes[head] * LOG2E : 0.f;
   bf16x8 q[KS];
   {
     const uint16_t* from = a.q + (w.t0 + tok) * a.q_stride + (int64_t)head * D + 8 * h;
@@ -120,7 +124,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   auto tokens = [&](int i) __attribute__((always_inline)) -> int {
     if (i >= count) return -1;
     const int t = w.near.tile(first + i) * TL_N + sub * 16;
-    return t > w.p_hi || (t + 15 <= w.w_lo && t >= a.sinks) ? -1 : t;
+    return t > end_hi<FORM>(w) || !some_begin<FORM>(a, w, t, t + 15) ? -1 : t;
   };
   const int32_t* table = a.c.table + w.b * a.c.table_stride;
   auto page_of = [&](int t) __attribute__((always_inline)) -> int32_t { return table[max(t, 0) >> a.c.pt_log2]; };
@@ -140,7 +144,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     for (int i = 0; i < LOADS; ++i) in[i] = *(const u32x4*)(src + row0 * (SRC * 16) + (uint32_t)((i * 64 + lane) * 16));
     if constexpr (FP8) in_scale = src_scale[row0 >> a.c.pt_log2];
   };
-  auto whole_tile = [&](int t0) __attribute__((always_inline)) { return t0 + TL_N - 1 <= w.p_lo && (t0 > w.w_hi || t0 + TL_N - 1 < a.sinks); };
+  auto whole_tile = [&](int t0) __attribute__((always_inline)) { return t0 + TL_N - 1 <= end_lo<FORM>(w) && all_begin<FORM>(a, w, t0, t0 + TL_N - 1); };
   // Values that no row of the block sees become 0: a probability of 0 would not clear an infinity. (Keys
   // may stay, their scores are masked.) Where some rows see a value and others do not, one that is not
   // finite becomes 0 as well, and the tile is marked: rescue() brings it to the rows that see it.
@@ -152,7 +156,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
 #pragma unroll
         for (int e = 0; e < LOADS; ++e) {
           const int t = t0 + (e * 64 + lane) / SRC;
-          const bool some = at >= 0 && t <= w.p_hi && (t > w.w_lo || t < a.sinks);
+          const bool some = at >= 0 && t <= end_hi<FORM>(w) && some_begin<FORM>(a, w, t, t);
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const uint32_t x = some ? in[e][z] : 0u, bad = not_finite<FP8>(x);
@@ -225,16 +229,25 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     }
     return v;
   };
-  auto seen = [&](int t) __attribute__((always_inline)) { return t <= p_row && (t > w_row || t < a.sinks); };
+  auto seen = [&](int t) __attribute__((always_inline)) { return t <= e_row && (t > w_row || t < a.sinks) && (!SEEN || t >= f_row); };
 
   // Scores of 32 keys before their softmax: register i of a lane is key 8 (i / 4) + 4 h + i % 4. Applies the mask and
   // raises the maximum; returns whether it rose for some row of the wave, and then what to scale by in `fall`.
   auto settle = [&](int buf, int t0, int u, bool whole, bool here0, bool here1, f32x16& s, float& fall) __attribute__((always_inline)) -> bool {
+    if constexpr (CAP || BIAS) {  // scores in base 2 from here on, capped and with their bias
+      const int near = p_row - (t0 + 32 * u + 4 * h);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] *= FP8 ? s_kc[buf][2 * u + i / 8] : c;
+        if constexpr (CAP) s[i] = cap_score(a, s[i]);
+        if constexpr (BIAS) s[i] = __builtin_fmaf(-slope, fabsf((float)(near - (8 * (i / 4) + i % 4))), s[i]);
+      }
+    }
     if (!whole) {
       // a bit for each of the 32 keys from the lane's first on: x <= hi, and x > lo or x < few
       const int base = t0 + 32 * u + 4 * h;
-      const uint32_t in = low_bits(p_row - base + 1) & (~low_bits(w_row - base + 1) | low_bits(a.sinks - base)) &
-                          ((here0 ? 0x0000FFFFu : 0u) | (here1 ? 0xFFFF0000u : 0u));
+      const uint32_t in = low_bits(e_row - base + 1) & (~low_bits(w_row - base + 1) | low_bits(a.sinks - base)) &
+                          (SEEN ? ~low_bits(f_row - base) : ~0u) & ((here0 ? 0x0000FFFFu : 0u) | (here1 ? 0xFFFF0000u : 0u));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const uint32_t see = __builtin_amdgcn_sbfe((int)in, 8 * (i / 4) + i % 4, 1);  // all ones or none
@@ -247,7 +260,8 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       top = fmaxf(top, s[i]);
       top1 = fmaxf(top1, s[8 + i]);
     }
-    top = FP8 ? fmaxf(top * s_kc[buf][2 * u], top1 * s_kc[buf][2 * u + 1]) : fmaxf(top, top1) * c;
+    if constexpr (CAP || BIAS) top = fmaxf(top, top1);
+    else top = FP8 ? fmaxf(top * s_kc[buf][2 * u], top1 * s_kc[buf][2 * u + 1]) : fmaxf(top, top1) * c;
     if (!__any(top > m + ATTEND_LAZY)) return false;
     const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
     const float high = fmaxf(m, fmaxf(__uint_as_float(o[0]), __uint_as_float(o[1])));
@@ -276,11 +290,12 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   auto step = [&](int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next, int old_buf, int old_u) __attribute__((always_inline)) {
     constexpr int E = 16 / KS;  // exponentials of a group
     static_assert(KS == 2 * DT, "as many key steps as value operands");
-    float c2[2] = {c, c}, add[2] = {-m, -m}, inv[2] = {1.f, 1.f};
+    float c2[2], add[2] = {-m, -m}, inv[2] = {1.f, 1.f};
+    c2[0] = c2[1] = CAP || BIAS ? 1.f : c;
     if constexpr (FP8) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        c2[x] = s_kc[buf][2 * u + x];
+        if constexpr (!CAP && !BIAS) c2[x] = s_kc[buf][2 * u + x];
         add[x] = s_vlog[buf][2 * u + x] - m;
         inv[x] = s_vinv[buf][2 * u + x];
       }
@@ -323,7 +338,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
 #pragma unroll 1
     for (int j = 0; j < TL_N; ++j) {
       const int t = t0 + j;
-      if (t > w.p_hi || !(t > w.w_lo || t < a.sinks)) continue;
+      if (t > end_hi<FORM>(w) || !some_begin<FORM>(a, w, t, t)) continue;
       const int64_t row = place(t, page_of(t));
       if (row < 0) continue;
       const char* from = a.c.v + row * (SRC * 16);
@@ -435,16 +450,24 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   }
 }
 
+template <int FORM>
 hipError_t launch_attend_tile(const AttendArgs& a, bool fp8, int d, hipStream_t s) {
+  constexpr int F = FORM ? FORM | FORM_SEEN : FORM_PLAIN;
   const dim3 grid((unsigned)(a.blocks * a.splits * a.c.n_kv));
   if (d == 64) {
-    if (fp8) attend_tile_kernel<true, 64><<<grid, TL_THREADS, 0, s>>>(a);
-    else attend_tile_kernel<false, 64><<<grid, TL_THREADS, 0, s>>>(a);
+    if (fp8) attend_tile_kernel<true, 64, F><<<grid, TL_THREADS, 0, s>>>(a);
+    else attend_tile_kernel<false, 64, F><<<grid, TL_THREADS, 0, s>>>(a);
   } else {
-    if (fp8) attend_tile_kernel<true, 128><<<grid, TL_THREADS, 0, s>>>(a);
-    else attend_tile_kernel<false, 128><<<grid, TL_THREADS, 0, s>>>(a);
+    if (fp8) attend_tile_kernel<true, 128, F><<<grid, TL_THREADS, 0, s>>>(a);
+    else attend_tile_kernel<false, 128, F><<<grid, TL_THREADS, 0, s>>>(a);
   }
   return hipGetLastError();
 }
+
+// One object of this file for each form.
+#ifndef ATTEND_FORM
+#define ATTEND_FORM 0
+#endif
+template hipError_t launch_attend_tile<ATTEND_FORM>(const AttendArgs&, bool, int, hipStream_t);
 
 }  // namespace lsa

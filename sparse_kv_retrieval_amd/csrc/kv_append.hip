@@ -95,17 +95,6 @@ __device__ __forceinline__ void store_bf16(uint16_t* row, Unit w, const float (&
   *(u32x4*)(row + w.b) = b;
 }
 
-// Four values to e4m3 codes, to nearest even. Values that are not finite become NaN.
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-  const float inf = __builtin_inff(), nan = __builtin_nanf("");
-  a = fabsf(a) < inf ? a : nan;
-  b = fabsf(b) < inf ? b : nan;
-  c = fabsf(c) < inf ? c : nan;
-  d = fabsf(d) < inf ? d : nan;
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-}
-
 // x / s: s is a power of two wherever this library wrote it, and then the product with its
 // reciprocal is exact and equal to the quotient.
 struct Divide {
@@ -116,15 +105,6 @@ struct Divide {
   }
   __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : x / s; }
 };
-
-// The least power of two s >= 2^-118 with a <= 448 s. 448 = 1.75 * 2^8, so with a = 1.m * 2^e it is
-// 2^(e - 8), or twice that when 1.m > 1.75.
-__device__ __forceinline__ float least_scale(float a) {
-  const uint32_t u = __float_as_uint(a);
-  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x007FFFFFu) > 0x00600000u ? 1 : 0);
-  e = e < -118 ? -118 : e;
-  return __uint_as_float((uint32_t)(e + 127) << 23);
-}
 
 template <int D, bool SHORT>
 __device__ __forceinline__ void append_queries(const AppendArgs& a, int style, int64_t block) {

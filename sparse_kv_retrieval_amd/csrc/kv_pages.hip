@@ -1,0 +1,292 @@
+// lsa_kv_extend, lsa_kv_fork and lsa_kv_free: pages of a pool taken, shared and given back.
+//
+// A page is free when no entry of the table holds it (refs <= 0), and the free pages with the lowest numbers are taken first.
+// So refs, table and lengths are the whole state: there is no list of free pages to keep in order, counts are sums
+// and do not depend on the order of their atomics, and the pages that a call takes depend on the state alone. The price is a
+// search of refs, 4 bytes a page, by one block of 1024 threads: 16,384 pages a round trip to memory, and none where no
+// sequence crosses the end of a page.
+//
+// Everything here is bound by latency: launches and a few dependent reads (length, table, refs). Giving back and sharing have one
+// block per sequence, so that no two threads look at one entry; taking has one block, which needs no order between blocks.
+#include "kv_pages.hpp"
+
+namespace lsa {
+
+static constexpr int PG_THREADS = 256;    // of a block that goes through one sequence's entries
+static constexpr int TAKE_THREADS = 1024; // of the block that takes pages
+static constexpr int TAKE_WAVES = TAKE_THREADS / 64;
+static constexpr int TAKE_CHUNK = 16 * TAKE_THREADS;  // pages looked at together
+static constexpr int TAKE_HELD = 4096;    // pages found before they are given out
+static constexpr int PER_THREAD = POOL_MAX / TAKE_THREADS;
+
+__device__ __forceinline__ bool is_page(const PoolArgs& p, int32_t page) { return page >= 0 && page < p.n_pages; }
+
+__device__ __forceinline__ int32_t held_len(const PoolArgs& p, int b) { return max(p.kv_len[b], 0); }
+__device__ __forceinline__ int64_t pages_of(const PoolArgs& p, int64_t len) { return (len + (1 << p.pt_log2) - 1) >> p.pt_log2; }
+// Entries of a row that hold its pages.
+__device__ __forceinline__ int32_t held_entries(const PoolArgs& p, int b) {
+  return (int32_t)min(pages_of(p, held_len(p, b)), p.table_stride);
+}
+
+// Whether x is among list[0 .. n - 1], for a whole block.
+__device__ __forceinline__ bool block_has(const int32_t* list, int n, int32_t x) {
+  bool hit = false;
+  for (int i = threadIdx.x; i < n; i += PG_THREADS) hit |= list[i] == x;
+  return __syncthreads_or(hit) != 0;
+}
+
+__global__ __launch_bounds__(PG_THREADS) void free_kernel(const PoolArgs p, const int32_t* seqs) {
+  const int i = blockIdx.x, b = seqs[i];
+  if (b < 0 || b >= p.B || block_has(seqs, i, b)) return;
+  const int held = held_entries(p, b);
+  int32_t* row = p.table + b * p.table_stride;
+  for (int j = threadIdx.x; j < held; j += PG_THREADS) {
+    const int32_t page = row[j];
+    if (is_page(p, page)) atomicSub(p.refs + page, 1);
+    row[j] = -1;
+  }
+  __syncthreads();  // every thread has read the length
+  if (threadIdx.x == 0) p.kv_len[b] = 0;
+}
+
+// One pair: dst's pages back, src's full pages shared. The last page is left to take_tails_kernel.
+__global__ __launch_bounds__(PG_THREADS) void share_kernel(const PoolArgs p, int n, const int32_t* src, const int32_t* dst, ForkPair* pairs) {
+  const int i = blockIdx.x, s = src[i], t = dst[i];
+  const bool bad = s < 0 || s >= p.B || t < 0 || t >= p.B;
+  if (bad || block_has(src, n, t) || block_has(dst, i, t)) {
+    if (threadIdx.x == 0) pairs[i] = {-1, -1, -1, 0};
+    return;
+  }
+  const int held = held_entries(p, t);
+  const int32_t len = (int32_t)min((int64_t)held_len(p, s), p.table_stride << p.pt_log2);
+  const int full = len >> p.pt_log2, tail = len & ((1 << p.pt_log2) - 1);
+  const int32_t* from = p.table + s * p.table_stride;
+  int32_t* to = p.table + t * p.table_stride;
+  const int end = max(held, full + (tail > 0));
+  for (int j = threadIdx.x; j < end; j += PG_THREADS) {
+    if (j < held) {
+      const int32_t old = to[j];
+      if (is_page(p, old)) atomicSub(p.refs + old, 1);
+    }
+    int32_t page = -1;
+    if (j < full) {
+      page = from[j];
+      if (is_page(p, page)) atomicAdd(p.refs + page, 1);
+      else page = -1;
+    }
+    to[j] = page;
+  }
+  __syncthreads();  // every thread has read dst's length
+  if (threadIdx.x == 0) {
+    // where src's last entry holds no page there is nothing to copy
+    const int32_t last = tail > 0 ? from[full] : -1;
+    const bool copies = is_page(p, last);
+    pairs[i] = {copies ? tail : 0, last, -1, 0};
+    p.kv_len[t] = copies ? full << p.pt_log2 : len;
+  }
+}
+
+// Inclusive sum over the threads of a block of TAKE_THREADS, and the whole sum. `s_sums` is read until the next barrier of
+// the caller's.
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T* s_sums, T* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const T y = __shfl_up(x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 63) s_sums[wave] = x;
+  __syncthreads();
+  T before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < TAKE_WAVES; ++w) {
+    const T y = s_sums[w];
+    if (w < wave) before += y;
+    all += y;
+  }
+  *total = all;
+  return before + x;
+}
+
+// Which of the pages base .. base + 15 are free, as bits.
+__device__ __forceinline__ uint32_t free_bits(const PoolArgs& p, int64_t base) {
+  uint32_t bits = 0;
+  if (base + 16 <= p.n_pages) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4 r = *(const u32x4*)(p.refs + base + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bits |= ((int32_t)r[e] <= 0 ? 1u : 0u) << (4 * i + e);
+    }
+  } else {
+    for (int i = 0; i < 16 && base + i < p.n_pages; ++i) bits |= (p.refs[base + i] <= 0 ? 1u : 0u) << i;
+  }
+  return bits;
+}
+
+// Looks for free pages from page *at on until `want` are found or all were looked at; the first TAKE_HELD of them go to s_ids, in
+// ascending order. Returns how many there are (at most `want`); *at becomes the first page of the last chunk, where a search
+// that goes on after those pages were taken begins.
+__device__ __forceinline__ int32_t find_free(const PoolArgs& p, int64_t* at, int32_t want, int32_t* s_ids, int32_t (*s_sums)[TAKE_WAVES]) {
+  int64_t found = 0, chunk = *at;
+  int turn = 0;
+  uint32_t next = free_bits(p, chunk + 16 * (int64_t)threadIdx.x);
+  for (; found < want && chunk < p.n_pages; chunk += TAKE_CHUNK, turn ^= 1) {
+    *at = chunk;
+    const uint32_t bits = next;
+    // the next chunk is on its way while this one is counted
+    next = free_bits(p, chunk + TAKE_CHUNK + 16 * (int64_t)threadIdx.x);
+    int32_t total;
+    const int32_t n = __popc(bits), upto = block_scan(n, s_sums[turn], &total);
+    int64_t rank = found + upto - n;
+    for (uint32_t left = bits; left && rank < min(want, TAKE_HELD); left &= left - 1, ++rank)
+      s_ids[rank] = (int32_t)(chunk + 16 * threadIdx.x + __ffs(left) - 1);
+    found += total;
+  }
+  __syncthreads();  // s_ids is whole
+  return (int32_t)min(found, (int64_t)want);
+}
+
+__global__ __launch_bounds__(TAKE_THREADS) void extend_kernel(const PoolArgs p, const int32_t* n_new, int32_t* missing) {
+  __shared__ int32_t s_ids[TAKE_HELD], s_upto[POOL_MAX], s_have[POOL_MAX];
+  __shared__ int32_t s_sums[2][TAKE_WAVES];
+  __shared__ int64_t s_sums64[TAKE_WAVES];
+  __shared__ int32_t s_limit;
+  const int b0 = PER_THREAD * threadIdx.x;
+  int64_t need[PER_THREAD], mine = 0, total;
+  int32_t after[PER_THREAD];  // the length with the new tokens
+  bool fits[PER_THREAD];
+#pragma unroll
+  for (int i = 0; i < PER_THREAD; ++i) {
+    need[i] = 0;
+    fits[i] = true;
+    if (b0 + i >= p.B) continue;
+    const int64_t len = held_len(p, b0 + i), more = max(n_new[b0 + i], 0);
+    const int64_t have = pages_of(p, len), want = pages_of(p, len + more);
+    fits[i] = more == 0 || (want <= p.table_stride && len + more <= INT32_MAX);
+    after[i] = (int32_t)(fits[i] ? len + more : len);
+    need[i] = fits[i] ? want - have : 0;
+    s_have[b0 + i] = (int32_t)have;
+    mine += need[i];
+  }
+  int64_t upto = block_scan(mine, s_sums64, &total) - mine;
+  if (threadIdx.x == 0) s_limit = 0;
+  __syncthreads();
+  int64_t at = 0;
+  int32_t found = 0;
+  if (total > 0) {
+    // all that are asked for, or all that there are: the number decides who gets any
+    found = find_free(p, &at, (int32_t)min(total, (int64_t)p.n_pages), s_ids, s_sums);
+  }
+#pragma unroll
+  for (int i = 0; i < PER_THREAD; ++i) {
+    if (b0 + i >= p.B) continue;
+    upto += need[i];
+    const bool granted = need[i] == 0 || upto <= found;
+    s_upto[b0 + i] = (int32_t)min(upto, (int64_t)INT32_MAX);
+    if (granted && need[i] > 0) atomicMax(&s_limit, (int32_t)upto);
+    if (missing) missing[b0 + i] = !fits[i] ? -1 : granted ? 0 : (int32_t)min(need[i], (int64_t)INT32_MAX);
+    if (granted && fits[i]) p.kv_len[b0 + i] = after[i];
+  }
+  __syncthreads();
+  const int32_t limit = s_limit;
+  // s_ids holds the first of them; where there are more, the search goes on behind those that are taken by now
+  if (found > TAKE_HELD) at = 0;
+  for (int32_t done = 0; done < limit;) {
+    const int32_t n = min(limit - done, TAKE_HELD);
+    if (done > 0) find_free(p, &at, n, s_ids, s_sums);
+    for (int32_t x = threadIdx.x; x < n; x += TAKE_THREADS) {
+      const int32_t rank = done + x;
+      int lo = 0, hi = p.B - 1;  // the first sequence with s_upto > rank
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s_upto[mid] > rank) hi = mid;
+        else lo = mid + 1;
+      }
+      const int32_t page = s_ids[x], before = lo > 0 ? s_upto[lo - 1] : 0;
+      p.refs[page] = 1;
+      p.table[lo * p.table_stride + s_have[lo] + (rank - before)] = page;
+    }
+    done += n;
+    __syncthreads();  // the counts are written before they are looked at again, and s_ids is read
+  }
+}
+
+// The last pages of a fork: one page for each pair that copies, lowest first.
+__global__ __launch_bounds__(TAKE_THREADS) void take_tails_kernel(const PoolArgs p, int n, const int32_t* dst, int32_t* status, ForkPair* pairs) {
+  __shared__ int32_t s_ids[TAKE_HELD];
+  __shared__ int32_t s_sums[2][TAKE_WAVES], s_first[TAKE_WAVES];
+  static_assert(TAKE_HELD >= POOL_MAX, "every pair's page is held at once");
+  const int i0 = PER_THREAD * threadIdx.x;
+  int32_t tail[PER_THREAD], mine = 0, total;
+#pragma unroll
+  for (int i = 0; i < PER_THREAD; ++i) {
+    tail[i] = i0 + i < n ? pairs[i0 + i].tail : 0;
+    mine += tail[i] > 0;
+  }
+  int32_t rank = block_scan(mine, s_first, &total) - mine, found = 0;
+  int64_t at = 0;
+  if (total > 0) found = find_free(p, &at, total, s_ids, s_sums);
+#pragma unroll
+  for (int i = 0; i < PER_THREAD; ++i) {
+    if (i0 + i >= n) continue;
+    int32_t st = tail[i] < 0 ? -1 : 0;
+    if (tail[i] > 0) {
+      if (rank < found) {
+        const int32_t page = s_ids[rank], t = dst[i0 + i], len = p.kv_len[t];
+        p.refs[page] = 1;
+        p.table[t * p.table_stride + (len >> p.pt_log2)] = page;
+        p.kv_len[t] = len + tail[i];
+        pairs[i0 + i].dst_page = page;
+      } else {
+        st = 1;
+      }
+      ++rank;
+    }
+    status[i0 + i] = st;
+  }
+}
+
+// One pair, layer, K or V and head: the used slots of the last page are one run of bytes.
+__global__ __launch_bounds__(PG_THREADS) void copy_tails_kernel(const ForkCopyArgs a) {
+  const ForkPair pair = a.pairs[blockIdx.x];
+  if (pair.dst_page < 0) return;
+  const int h = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  const ForkLayer& l = a.layer[blockIdx.z];
+  char* base = is_v ? l.v : l.k;
+  float* scale = is_v ? l.v_scale : l.k_scale;
+  const int64_t from = (int64_t)pair.src_page * a.n_kv + h, to = (int64_t)pair.dst_page * a.n_kv + h;
+  const u32x4* in = (const u32x4*)(base + (from << a.pt_log2) * a.row_bytes);
+  u32x4* out = (u32x4*)(base + (to << a.pt_log2) * a.row_bytes);
+  const int units = pair.tail * (a.row_bytes / 16);
+  for (int i = threadIdx.x; i < units; i += PG_THREADS) out[i] = in[i];
+  if (scale && threadIdx.x == 0) scale[to] = scale[from];
+}
+
+hipError_t launch_kv_extend(const PoolArgs& p, const int32_t* n_new, int32_t* missing, hipStream_t s) {
+  extend_kernel<<<1, TAKE_THREADS, 0, s>>>(p, n_new, missing);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_fork(const PoolArgs& p, int n, const int32_t* src, const int32_t* dst, int32_t* status, ForkPair* pairs,
+                          hipStream_t s) {
+  share_kernel<<<n, PG_THREADS, 0, s>>>(p, n, src, dst, pairs);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  take_tails_kernel<<<1, TAKE_THREADS, 0, s>>>(p, n, dst, status, pairs);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_fork_copy(const ForkCopyArgs& a, int n, int layers, hipStream_t s) {
+  copy_tails_kernel<<<dim3(n, 2 * a.n_kv, layers), PG_THREADS, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_free(const PoolArgs& p, int n, const int32_t* seqs, hipStream_t s) {
+  free_kernel<<<n, PG_THREADS, 0, s>>>(p, seqs);
+  return hipGetLastError();
+}
+
+}  // namespace lsa

@@ -11,6 +11,7 @@
 
 #include "kernels.hpp"
 #include "kv.hpp"
+#include "kv_pages.hpp"
 
 using namespace lsa;
 
@@ -652,6 +653,7 @@ namespace {
 // Limits of the paged-cache calls.
 constexpr int32_t kKvMaxB = 4096, kKvMaxHeads = 1024, kKvMaxGroup = 1024;
 constexpr int64_t kMaxBlocks = (1 << 24) - 1;          // of 256 threads: a launch has fewer than 2^32
+constexpr int64_t kCompactBlocks = 2048;               // of a compaction: eight for each of 256 compute units
 constexpr size_t kPartialBytes = (size_t)256 << 20;    // partial results of the tile kernel, where more than two splits fit
 
 bool multiple8(int64_t x) { return x % 8 == 0; }
@@ -846,6 +848,48 @@ bool plan_fits(const TilePlan& p, const AttendArgs& a) {
   return !p.used || p.blocks * p.splits * a.c.n_kv <= kMaxBlocks / 2;
 }
 
+// The kernels of the call's form: capped and biased ones have document and prefix masks too.
+hipError_t launch_split_form(const AttendArgs& a, bool fp8, int32_t d, int row_tiles, bool listed, hipStream_t stream) {
+  switch ((a.cap_log2 > 0.f ? FORM_CAP : 0) | (a.slopes ? FORM_BIAS : 0)) {
+    case FORM_CAP: return launch_attend_split<FORM_CAP>(a, fp8, d, row_tiles, listed, stream);
+    case FORM_BIAS: return launch_attend_split<FORM_BIAS>(a, fp8, d, row_tiles, listed, stream);
+    case FORM_CAP | FORM_BIAS: return launch_attend_split<FORM_CAP | FORM_BIAS>(a, fp8, d, row_tiles, listed, stream);
+    default: break;
+  }
+  if (a.doc_start || a.prefix_end) return launch_attend_split<FORM_SEEN>(a, fp8, d, row_tiles, listed, stream);
+  return launch_attend_split<FORM_PLAIN>(a, fp8, d, row_tiles, listed, stream);
+}
+hipError_t launch_tile_form(const AttendArgs& a, bool fp8, int32_t d, hipStream_t stream) {
+  switch ((a.cap_log2 > 0.f ? FORM_CAP : 0) | (a.slopes ? FORM_BIAS : 0)) {
+    case FORM_CAP: return launch_attend_tile<FORM_CAP>(a, fp8, d, stream);
+    case FORM_BIAS: return launch_attend_tile<FORM_BIAS>(a, fp8, d, stream);
+    case FORM_CAP | FORM_BIAS: return launch_attend_tile<FORM_CAP | FORM_BIAS>(a, fp8, d, stream);
+    default: break;
+  }
+  if (a.doc_start || a.prefix_end) return launch_attend_tile<FORM_SEEN>(a, fp8, d, stream);
+  return launch_attend_tile<FORM_PLAIN>(a, fp8, d, stream);
+}
+
+// The checks of a form, and what of the arguments follows from it.
+lsa_status form_args(AttendArgs* a, const lsa_attend_form* form, int32_t window, bool listed) {
+  if (!form) return LSA_OK;
+  const float cap = form->softcap;
+  if (cap != 0.f && !(cap >= 0x1p-10f && cap <= 1024.f))
+    return fail(LSA_ERR_UNSUPPORTED, "softcap must be 0 or in [2^-10, 1024] (got %g)", (double)cap);
+  if (reinterpret_cast<uintptr_t>(form->slopes) & 3u || reinterpret_cast<uintptr_t>(form->doc_start) & 3u ||
+      reinterpret_cast<uintptr_t>(form->prefix_end) & 3u)
+    return fail(LSA_ERR_INVALID_ARG, "slopes, doc_start and prefix_end must be 4-byte aligned");
+  if (listed && (form->doc_start || form->prefix_end))
+    return fail(LSA_ERR_UNSUPPORTED, "doc_start and prefix_end are not for listed entries");
+  if (window > 0 && form->prefix_end) return fail(LSA_ERR_UNSUPPORTED, "prefix_end is not supported with a window");
+  a->slopes = form->slopes; a->doc_start = form->doc_start; a->prefix_end = form->prefix_end;
+  if (cap > 0.f) {
+    a->cap_log2 = (float)((double)cap * 1.4426950408889634);
+    a->two_over_cap = (float)(2.0 / (double)cap);
+  }
+  return LSA_OK;
+}
+
 hipError_t launch_plan(AttendArgs a, const SplitPlan& p, bool fp8, int32_t d, hipStream_t stream) {
   if (p.entries == 0) return hipSuccess;
   const bool listed = a.idx != nullptr;
@@ -853,7 +897,7 @@ hipError_t launch_plan(AttendArgs a, const SplitPlan& p, bool fp8, int32_t d, hi
   a.rows_above = 0; a.rows_to = listed ? INT64_MAX : kSplitRows;
   a.part_ml = (float*)((char*)a.part_o + p.ml);
   a.joins = (int32_t*)((char*)a.part_o + p.joins);
-  hipError_t e = launch_attend_split(a, fp8, d, p.rows / 16, listed, stream);
+  hipError_t e = launch_split_form(a, fp8, d, p.rows / 16, listed, stream);
   if (e == hipSuccess && p.workers > 0) e = launch_attend_split_join(a, d, p.rows, listed, stream);
   return e;
 }
@@ -863,8 +907,8 @@ hipError_t launch_plan(AttendArgs a, const TilePlan& p, bool fp8, int32_t d, hip
   a.blocks = p.blocks; a.splits = p.splits; a.run = p.run;
   a.rows_above = kSplitRows; a.rows_to = INT64_MAX;
   a.part_ml = (float*)((char*)a.part_o + p.ml);
-  hipError_t e = launch_attend_tile(a, fp8, d, stream);
-  if (e == hipSuccess && p.splits > 1) e = launch_attend_tile_join(a, d, stream);
+  hipError_t e = launch_tile_form(a, fp8, d, stream);
+  if (e == hipSuccess && p.splits > 1) e = launch_attend_tile_join(a, d, a.doc_start || a.prefix_end, stream);
   return e;
 }
 
@@ -927,10 +971,10 @@ size_t lsa_attend_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d
   return plan_ragged(B, n_q, n_kv, d_h, q_offsets_host, max_kv_len, window, sinks).bytes;
 }
 
-lsa_status lsa_attend(const lsa_kv_cache* cache, int32_t B, const void* q, int64_t q_stride, int32_t n_q,
-                      const int64_t* q_offsets, const int64_t* q_offsets_host, int32_t max_kv_len, float softmax_scale,
-                      int32_t window, int32_t sinks, void* out, int64_t out_stride, float* lse, void* workspace,
-                      size_t workspace_bytes, hipStream_t stream) {
+lsa_status lsa_attend_ex(const lsa_kv_cache* cache, int32_t B, const void* q, int64_t q_stride, int32_t n_q,
+                         const int64_t* q_offsets, const int64_t* q_offsets_host, int32_t max_kv_len, float softmax_scale,
+                         int32_t window, int32_t sinks, const lsa_attend_form* form, void* out, int64_t out_stride, float* lse,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
   AttendArgs a{};
   bool fp8 = false;
   lsa_status s;
@@ -940,6 +984,7 @@ lsa_status lsa_attend(const lsa_kv_cache* cache, int32_t B, const void* q, int64
   if (max_kv_len < 0 || max_kv_len > cache->table_stride * cache->page_tokens)
     return fail(LSA_ERR_INVALID_ARG, "max_kv_len must be in [0, table_stride * page_tokens] (got %d)", max_kv_len);
   if (max_kv_len > INT32_MAX - 64) return fail(LSA_ERR_UNSUPPORTED, "max_kv_len must be below 2^31 - 64");
+  if ((s = form_args(&a, form, window, false)) != LSA_OK) return s;
   clip_window(max_kv_len, &window, &sinks);
   a.off = q_offsets; a.first_row = q_offsets_host[0]; a.T = q_offsets_host[B] - q_offsets_host[0];
   a.B = B; a.n_q = n_q; a.max_kv_len = max_kv_len; a.window = window; a.sinks = sinks; a.r = 1;
@@ -955,16 +1000,24 @@ lsa_status lsa_attend(const lsa_kv_cache* cache, int32_t B, const void* q, int64
   return e == hipSuccess ? LSA_OK : hip_fail("lsa_attend launch", e);
 }
 
+lsa_status lsa_attend(const lsa_kv_cache* cache, int32_t B, const void* q, int64_t q_stride, int32_t n_q,
+                      const int64_t* q_offsets, const int64_t* q_offsets_host, int32_t max_kv_len, float softmax_scale,
+                      int32_t window, int32_t sinks, void* out, int64_t out_stride, float* lse, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+  return lsa_attend_ex(cache, B, q, q_stride, n_q, q_offsets, q_offsets_host, max_kv_len, softmax_scale, window, sinks, nullptr,
+                       out, out_stride, lse, workspace, workspace_bytes, stream);
+}
+
 size_t lsa_attend_topk_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d_h, int32_t k,
                                       int32_t entry_tokens, int32_t window, int32_t sinks) {
   if (!plan_sizes_ok(B, n_q, n_kv, d_h, window, sinks) || k < 1 || entry_tokens < 1) return 0;
   return plan_listed(B, n_q, n_kv, d_h, k, entry_tokens, window, sinks).bytes;
 }
 
-lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, int64_t q_stride, int32_t n_q,
-                           const int32_t* idx, const int32_t* count, int32_t k, int32_t entry_tokens,
-                           float softmax_scale, int32_t window, int32_t sinks, void* out, int64_t out_stride, float* lse,
-                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
+lsa_status lsa_attend_topk_ex(const lsa_kv_cache* cache, int32_t B, const void* q, int64_t q_stride, int32_t n_q,
+                              const int32_t* idx, const int32_t* count, int32_t k, int32_t entry_tokens,
+                              float softmax_scale, int32_t window, int32_t sinks, const lsa_attend_form* form, void* out,
+                              int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   AttendArgs a{};
   bool fp8 = false;
   lsa_status s;
@@ -976,6 +1029,7 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, 
   if (k < 1 || k > 65536) return fail(LSA_ERR_UNSUPPORTED, "k must be in [1, 65536] (got %d)", k);
   if (entry_tokens < 1 || entry_tokens > 128) return fail(LSA_ERR_UNSUPPORTED, "entry_tokens must be in [1, 128] (got %d)", entry_tokens);
   if (window < 0 || sinks < 0) return fail(LSA_ERR_INVALID_ARG, "window and sinks must not be negative");
+  if ((s = form_args(&a, form, window, true)) != LSA_OK) return s;
   a.max_kv_len = (int32_t)std::min<int64_t>(cache->table_stride * cache->page_tokens, INT32_MAX - 64);
   a.idx = idx; a.count = count; a.k = k; a.r = entry_tokens;
   a.first_row = 0; a.T = B; a.B = B; a.n_q = n_q;
@@ -990,6 +1044,181 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, 
   if (!plan_fits(p, a)) return fail(LSA_ERR_UNSUPPORTED, "too many rows or keys for one call");
   const hipError_t e = launch_plan(a, p, fp8, cache->d_h, stream);
   return e == hipSuccess ? LSA_OK : hip_fail("lsa_attend_topk launch", e);
+}
+
+lsa_status lsa_attend_topk(const lsa_kv_cache* cache, int32_t B, const void* q, int64_t q_stride, int32_t n_q,
+                           const int32_t* idx, const int32_t* count, int32_t k, int32_t entry_tokens,
+                           float softmax_scale, int32_t window, int32_t sinks, void* out, int64_t out_stride, float* lse,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return lsa_attend_topk_ex(cache, B, q, q_stride, n_q, idx, count, k, entry_tokens, softmax_scale, window, sinks, nullptr, out,
+                            out_stride, lse, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- pages and kept tokens
+namespace {
+
+constexpr int32_t kMaxCacheLayers = 1024;
+
+// Checks L caches that must agree in what the kernels take once for all of them: sizes and dtype, and with `one_table` the
+// table and lengths as well.
+lsa_status check_layers(const lsa_kv_cache* c, int32_t L, const char* name, bool one_table, bool* fp8, KvView* v) {
+  if (!c) return fail(LSA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (L < 1 || L > kMaxCacheLayers) return fail(LSA_ERR_UNSUPPORTED, "L must be in [1, %d] (got %d)", kMaxCacheLayers, L);
+  for (int32_t l = L - 1; l >= 0; --l) {  // the first one's view is what stays
+    const lsa_status s = check_cache(c + l, fp8, v);
+    if (s != LSA_OK) return s;
+    if (dtype_value(c[l].dtype) != dtype_value(c[0].dtype) || c[l].n_kv != c[0].n_kv || c[l].d_h != c[0].d_h ||
+        c[l].page_tokens != c[0].page_tokens || c[l].n_pages != c[0].n_pages)
+      return fail(LSA_ERR_INVALID_ARG, "%s[%d] must have the dtype and sizes of %s[0]", name, l, name);
+    if (one_table && (c[l].page_table != c[0].page_table || c[l].kv_len != c[0].kv_len || c[l].table_stride != c[0].table_stride))
+      return fail(LSA_ERR_INVALID_ARG, "%s[%d] must have the page_table and kv_len of %s[0]", name, l, name);
+  }
+  return LSA_OK;
+}
+
+PageMap page_map(const KvView& v) { return {v.table, v.table_stride, v.n_pages, v.pt_log2}; }
+
+// The arguments that lsa_kv_kept and lsa_kv_compact share.
+lsa_status compact_args(CompactArgs* a, const KvView& from, int32_t B, const int32_t* idx, const int64_t* idx_offsets,
+                        const int32_t* count, int32_t entry_tokens, int32_t window, int32_t sinks) {
+  if (B < 1 || B > kKvMaxB) return fail(LSA_ERR_UNSUPPORTED, "B must be in [1, %d] (got %d)", kKvMaxB, B);
+  if (!idx || !idx_offsets || !count) return fail(LSA_ERR_INVALID_ARG, "idx, idx_offsets and count must be set");
+  if (entry_tokens < 1 || entry_tokens > 128) return fail(LSA_ERR_UNSUPPORTED, "entry_tokens must be in [1, 128] (got %d)", entry_tokens);
+  if (window < 0 || sinks < 0) return fail(LSA_ERR_INVALID_ARG, "window and sinks must not be negative");
+  a->from = page_map(from); a->kv_len = from.kv_len; a->n_kv = from.n_kv;
+  a->idx = idx; a->idx_offsets = idx_offsets; a->count = count;
+  a->B = B; a->r = entry_tokens; a->window = window; a->sinks = sinks;
+  return LSA_OK;
+}
+
+lsa_status check_pool(const lsa_kv_pool* p, PoolArgs* a) {
+  if (!p) return fail(LSA_ERR_INVALID_ARG, "pool is NULL");
+  if (!p->refs || !p->page_table || !p->kv_len) return fail(LSA_ERR_INVALID_ARG, "the pool's refs, page_table and kv_len must be set");
+  if (!aligned16(p->refs)) return fail(LSA_ERR_INVALID_ARG, "the pool's refs must be 16-byte aligned");
+  if (p->B < 1 || p->B > POOL_MAX) return fail(LSA_ERR_UNSUPPORTED, "B must be in [1, %d] (got %d)", POOL_MAX, p->B);
+  if (p->n_pages < 1) return fail(LSA_ERR_INVALID_ARG, "n_pages must be >= 1 (got %d)", p->n_pages);
+  if (p->page_tokens != 16 && p->page_tokens != 32 && p->page_tokens != 64 && p->page_tokens != 128)
+    return fail(LSA_ERR_UNSUPPORTED, "page_tokens must be 16, 32, 64 or 128 (got %d)", p->page_tokens);
+  if (p->table_stride < 1 || p->table_stride > INT32_MAX / 16)
+    return fail(LSA_ERR_INVALID_ARG, "table_stride must be in [1, 2^27) (got %lld)", (long long)p->table_stride);
+  *a = {p->refs, p->page_table, p->kv_len, p->table_stride, p->B, p->n_pages,
+        p->page_tokens == 16 ? 4 : p->page_tokens == 32 ? 5 : p->page_tokens == 64 ? 6 : 7};
+  return LSA_OK;
+}
+
+lsa_status check_count(int32_t n) {
+  if (n < 0 || n > POOL_MAX) return fail(LSA_ERR_UNSUPPORTED, "n must be in [0, %d] (got %d)", POOL_MAX, n);
+  return LSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lsa_status lsa_kv_kept(const lsa_kv_cache* from, int32_t B, const int32_t* idx, const int64_t* idx_offsets, const int32_t* count,
+                       int32_t entry_tokens, int32_t window, int32_t sinks, int32_t* kept_out, hipStream_t stream) {
+  CompactArgs a{};
+  KvView v;
+  bool fp8 = false;
+  lsa_status s;
+  if ((s = check_cache(from, &fp8, &v)) != LSA_OK) return s;
+  if ((s = compact_args(&a, v, B, idx, idx_offsets, count, entry_tokens, window, sinks)) != LSA_OK) return s;
+  if (!kept_out) return fail(LSA_ERR_INVALID_ARG, "kept_out must be set");
+  const hipError_t e = launch_kv_kept(a, kept_out, stream);
+  return e == hipSuccess ? LSA_OK : hip_fail("lsa_kv_kept launch", e);
+}
+
+lsa_status lsa_kv_compact(const lsa_kv_cache* from, const lsa_kv_cache* to, int32_t L, int32_t B, const int32_t* idx,
+                          const int64_t* idx_offsets, const int32_t* count, int32_t entry_tokens, int32_t window,
+                          int32_t sinks, int32_t max_kept, hipStream_t stream) {
+  CompactArgs a{};
+  KvView v, w;
+  bool fp8 = false, to_fp8 = false;
+  lsa_status s;
+  if ((s = check_layers(from, L, "from", true, &fp8, &v)) != LSA_OK) return s;
+  if ((s = check_layers(to, L, "to", true, &to_fp8, &w)) != LSA_OK) return s;
+  if (fp8 != to_fp8 || v.n_kv != w.n_kv || from->d_h != to->d_h)
+    return fail(LSA_ERR_INVALID_ARG, "from and to must have equal dtype, n_kv and d_h");
+  if ((s = compact_args(&a, v, B, idx, idx_offsets, count, entry_tokens, window, sinks)) != LSA_OK) return s;
+  const int32_t pt = to->page_tokens;
+  if (max_kept < 0 || max_kept > to->table_stride * pt)
+    return fail(LSA_ERR_INVALID_ARG, "max_kept must be in [0, table_stride * page_tokens] of the destination (got %d)", max_kept);
+  if (max_kept == 0) return LSA_OK;
+  a.to = page_map(w);
+  a.max_kept = max_kept;
+  a.pages = (max_kept - 1) / pt + 1;
+  const int64_t all = (int64_t)B * a.pages;
+  if (all * 2 * a.n_kv > kMaxBlocks) return fail(LSA_ERR_UNSUPPORTED, "too many pages for one call");
+  hipError_t e = hipSuccess;
+  for (int32_t l0 = 0; l0 < L && e == hipSuccess; l0 += KV_LAYERS) {
+    const int32_t n = std::min(L - l0, KV_LAYERS);
+    for (int32_t l = 0; l < n; ++l) {
+      const lsa_kv_cache &x = from[l0 + l], &y = to[l0 + l];
+      a.layer[l] = {(const char*)x.k, (const char*)x.v, x.k_scale, x.v_scale, (char*)y.k, (char*)y.v, y.k_scale, y.v_scale};
+    }
+    // A page's tokens are found once a block: as few blocks a page as fill the device, each with a tile a wave at least.
+    a.tiles = n * 2 * a.n_kv;
+    const int64_t groups = std::min<int64_t>((a.tiles + 3) / 4, (kCompactBlocks + all - 1) / all);
+    a.per_group = (int32_t)((a.tiles + groups - 1) / groups);
+    a.groups = (a.tiles + a.per_group - 1) / a.per_group;
+    e = launch_kv_compact(a, fp8, from->d_h, stream);
+  }
+  return e == hipSuccess ? LSA_OK : hip_fail("lsa_kv_compact launch", e);
+}
+
+lsa_status lsa_kv_extend(const lsa_kv_pool* pool, const int32_t* n_new, int32_t* missing_out, hipStream_t stream) {
+  PoolArgs p;
+  lsa_status s;
+  if ((s = check_pool(pool, &p)) != LSA_OK) return s;
+  if (!n_new) return fail(LSA_ERR_INVALID_ARG, "n_new must be set");
+  const hipError_t e = launch_kv_extend(p, n_new, missing_out, stream);
+  return e == hipSuccess ? LSA_OK : hip_fail("lsa_kv_extend launch", e);
+}
+
+size_t lsa_kv_fork_workspace_size(int32_t n) { return n < 0 || n > POOL_MAX ? 0 : (size_t)n * sizeof(ForkPair); }
+
+lsa_status lsa_kv_fork(const lsa_kv_pool* pool, const lsa_kv_cache* layers, int32_t L, int32_t n, const int32_t* src,
+                       const int32_t* dst, int32_t* status_out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  PoolArgs p;
+  KvView v;
+  bool fp8 = false;
+  lsa_status s;
+  if ((s = check_pool(pool, &p)) != LSA_OK) return s;
+  if ((s = check_layers(layers, L, "layers", false, &fp8, &v)) != LSA_OK) return s;
+  if (v.n_pages != p.n_pages || v.pt_log2 != p.pt_log2)
+    return fail(LSA_ERR_INVALID_ARG, "the layers must have the pool's n_pages and page_tokens");
+  if ((s = check_count(n)) != LSA_OK) return s;
+  if (n == 0) return LSA_OK;
+  if (!src || !dst || !status_out) return fail(LSA_ERR_INVALID_ARG, "src, dst and status_out must be set");
+  const size_t bytes = lsa_kv_fork_workspace_size(n);
+  if (!workspace || workspace_bytes < bytes) return fail(LSA_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", bytes, workspace_bytes);
+  if (!aligned16(workspace)) return fail(LSA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  if ((int64_t)n * 2 * v.n_kv * std::min(L, KV_LAYERS) > kMaxBlocks) return fail(LSA_ERR_UNSUPPORTED, "too many pairs for one call");
+  hipError_t e = launch_kv_fork(p, n, src, dst, status_out, (ForkPair*)workspace, stream);
+  for (int32_t l0 = 0; l0 < L && e == hipSuccess; l0 += KV_LAYERS) {
+    ForkCopyArgs a{};
+    const int32_t m = std::min(L - l0, KV_LAYERS);
+    a.pairs = (const ForkPair*)workspace; a.n_kv = v.n_kv; a.pt_log2 = v.pt_log2; a.row_bytes = layers->d_h * (fp8 ? 1 : 2);
+    for (int32_t l = 0; l < m; ++l) {
+      const lsa_kv_cache& x = layers[l0 + l];
+      a.layer[l] = {(char*)x.k, (char*)x.v, x.k_scale, x.v_scale};
+    }
+    e = launch_kv_fork_copy(a, n, m, stream);
+  }
+  return e == hipSuccess ? LSA_OK : hip_fail("lsa_kv_fork launch", e);
+}
+
+lsa_status lsa_kv_free(const lsa_kv_pool* pool, int32_t n, const int32_t* seqs, hipStream_t stream) {
+  PoolArgs p;
+  lsa_status s;
+  if ((s = check_pool(pool, &p)) != LSA_OK) return s;
+  if ((s = check_count(n)) != LSA_OK) return s;
+  if (n == 0) return LSA_OK;
+  if (!seqs) return fail(LSA_ERR_INVALID_ARG, "seqs must be set");
+  const hipError_t e = launch_kv_free(p, n, seqs, stream);
+  return e == hipSuccess ? LSA_OK : hip_fail("lsa_kv_free launch", e);
 }
 
 }  // extern "C"

@@ -64,6 +64,15 @@ class _KvCache(ctypes.Structure):
                 ("dtype", _i32)]
 
 
+class _AttendForm(ctypes.Structure):
+    _fields_ = [("softcap", _f32), ("slopes", _vp), ("doc_start", _vp), ("prefix_end", _vp)]
+
+
+class _KvPool(ctypes.Structure):
+    _fields_ = [("refs", _vp), ("page_table", _vp), ("kv_len", _vp), ("table_stride", _i64), ("B", _i32), ("n_pages", _i32),
+                ("page_tokens", _i32)]
+
+
 ROPE = {None: 0, "none": 0, "halves": 1, "pairs": 2}
 
 
@@ -112,6 +121,19 @@ _attend = _sig("lsa_attend", _i32, [ctypes.POINTER(_KvCache), _i32, _vp, _i64, _
 _attend_topk_ws = _sig("lsa_attend_topk_workspace_size", _sz, [_i32] * 8)
 _attend_topk = _sig("lsa_attend_topk", _i32, [ctypes.POINTER(_KvCache), _i32, _vp, _i64, _i32, _vp, _vp, _i32, _i32,
                                               _f32, _i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp])
+_attend_ex = _sig("lsa_attend_ex", _i32, [ctypes.POINTER(_KvCache), _i32, _vp, _i64, _i32, _vp, _vp, _i32, _f32, _i32, _i32,
+                                          ctypes.POINTER(_AttendForm), _vp, _i64, _vp, _vp, _sz, _vp])
+_attend_topk_ex = _sig("lsa_attend_topk_ex", _i32, [ctypes.POINTER(_KvCache), _i32, _vp, _i64, _i32, _vp, _vp, _i32, _i32,
+                                                    _f32, _i32, _i32, ctypes.POINTER(_AttendForm), _vp, _i64, _vp, _vp, _sz,
+                                                    _vp])
+_kv_kept = _sig("lsa_kv_kept", _i32, [ctypes.POINTER(_KvCache), _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp])
+_kv_compact = _sig("lsa_kv_compact", _i32, [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvCache), _i32, _i32, _vp, _vp, _vp,
+                                            _i32, _i32, _i32, _i32, _vp])
+_kv_extend = _sig("lsa_kv_extend", _i32, [ctypes.POINTER(_KvPool), _vp, _vp, _vp])
+_kv_fork_ws = _sig("lsa_kv_fork_workspace_size", _sz, [_i32])
+_kv_fork = _sig("lsa_kv_fork", _i32, [ctypes.POINTER(_KvPool), ctypes.POINTER(_KvCache), _i32, _i32, _vp, _vp, _vp, _vp, _sz,
+                                      _vp])
+_kv_free = _sig("lsa_kv_free", _i32, [ctypes.POINTER(_KvPool), _i32, _vp, _vp])
 _debug_range_errors = _sig("lsa_debug_range_errors", _i32, [_vp, ctypes.POINTER(_i64)])
 _last_error = _sig("lsa_last_error", ctypes.c_char_p, [])
 _version = _sig("lsa_version", _i32, [])
@@ -121,8 +143,9 @@ EXPORTED = ("lsa_project", "lsa_pack_weights_size", "lsa_pack_weights", "lsa_pro
             "lsa_topk_score", "lsa_topk_select", "lsa_union_compact", "lsa_topk_workspace_size", "lsa_topk",
             "lsa_gather", "lsa_fetch_host", "lsa_golden_workspace_size", "lsa_golden_labels", "lsa_train_workspace_size",
             "lsa_train_step", "lsa_kv_append", "lsa_attend_workspace_size", "lsa_attend",
-            "lsa_attend_topk_workspace_size", "lsa_attend_topk", "lsa_debug_range_errors", "lsa_last_error",
-            "lsa_version")
+            "lsa_attend_topk_workspace_size", "lsa_attend_topk", "lsa_attend_ex", "lsa_attend_topk_ex", "lsa_kv_kept",
+            "lsa_kv_compact", "lsa_kv_extend", "lsa_kv_fork_workspace_size", "lsa_kv_fork", "lsa_kv_free",
+            "lsa_debug_range_errors", "lsa_last_error", "lsa_version")
 
 
 def last_error() -> str:
@@ -539,17 +562,39 @@ def _attend_tensors(fn, cache, q, out, lse, workspace):
     return rows, n_q, qs, os_, lse_at, ws_at, nbytes
 
 
+def _attend_form(fn, cache, rows, n_q, softcap, slopes, doc_start, prefix_end):
+    torch, dev = _torch(), cache.device
+    form = _AttendForm(softcap)
+    if slopes is not None:
+        _want(fn, "slopes", slopes, torch.float32, (n_q,), dev)
+        form.slopes = slopes.data_ptr()
+    if doc_start is not None:
+        _want(fn, "doc_start", doc_start, torch.int32, (rows,), dev)
+        form.doc_start = doc_start.data_ptr()
+    if prefix_end is not None:
+        _want(fn, "prefix_end", prefix_end, torch.int32, (rows,), dev)
+        form.prefix_end = prefix_end.data_ptr()
+    return form
+
+
 def attend(cache, q, *, q_offsets, q_offsets_host, max_kv_len, out, scale, window=0, sinks=0, lse=None, workspace=None,
-           stream=None):
+           stream=None, softcap=0.0, slopes=None, doc_start=None, prefix_end=None):
     """lsa_attend: q and out [rows, n_q, d_h] bfloat16 with contiguous rows at any distance, lse [rows, n_q] float32
     or None; q_offsets [B + 1] int64 on the device and on the host; workspace a tensor of at least
-    attend_workspace_size(...) bytes for the same arguments."""
+    attend_workspace_size(...) bytes for the same arguments.
+
+    With softcap, slopes [n_q] float32, doc_start or prefix_end [rows] int32, lsa_attend_ex with these."""
     fn = "lsa_attend"
     _int32(fn, max_kv_len, window, sinks)
     rows, n_q, qs, os_, lse_at, ws_at, nbytes = _attend_tensors(fn, cache, q, out, lse, workspace)
     host, host_at = _offsets(fn, "q_offsets", q_offsets, q_offsets_host, cache.B, rows, cache.device)
-    _launch(cache.device, fn, _attend, (cache.ref, cache.B, q.data_ptr(), qs, n_q, q_offsets.data_ptr(), host_at, max_kv_len,
-                                        scale, window, sinks, out.data_ptr(), os_, lse_at, ws_at, nbytes), stream)
+    args = (cache.ref, cache.B, q.data_ptr(), qs, n_q, q_offsets.data_ptr(), host_at, max_kv_len, scale, window, sinks)
+    outs = (out.data_ptr(), os_, lse_at, ws_at, nbytes)
+    if softcap == 0.0 and slopes is None and doc_start is None and prefix_end is None:
+        _launch(cache.device, fn, _attend, args + outs, stream)
+    else:
+        form = _attend_form("lsa_attend_ex", cache, rows, n_q, softcap, slopes, doc_start, prefix_end)
+        _launch(cache.device, "lsa_attend_ex", _attend_ex, (*args, form, *outs), stream)
 
 
 def attend_topk_workspace_size(cache, *, n_q, k, entry_tokens=1, window=0, sinks=0) -> int:
@@ -559,9 +604,11 @@ def attend_topk_workspace_size(cache, *, n_q, k, entry_tokens=1, window=0, sinks
 
 
 def attend_topk(cache, q, *, idx, count, out, scale, entry_tokens=1, window=0, sinks=0, lse=None, workspace=None,
-                stream=None):
+                stream=None, softcap=0.0, slopes=None):
     """lsa_attend_topk: q and out [B, n_q, d_h] bfloat16, idx [B, k] and count [B] int32 as topk and topk_step
-    write them, lse [B, n_q] float32 or None; workspace of at least attend_topk_workspace_size(...) bytes."""
+    write them, lse [B, n_q] float32 or None; workspace of at least attend_topk_workspace_size(...) bytes.
+
+    With softcap or slopes [n_q] float32, lsa_attend_topk_ex with these."""
     fn, torch, B = "lsa_attend_topk", _torch(), cache.B
     _int32(fn, entry_tokens, window, sinks)
     rows, n_q, qs, os_, lse_at, ws_at, nbytes = _attend_tensors(fn, cache, q, out, lse, workspace)
@@ -570,6 +617,108 @@ def attend_topk(cache, q, *, idx, count, out, scale, entry_tokens=1, window=0, s
     k = idx.shape[1]
     _want(fn, "idx", idx, torch.int32, (B, k), cache.device)
     _want(fn, "count", count, torch.int32, (B,), cache.device)
-    _launch(cache.device, fn, _attend_topk, (cache.ref, B, q.data_ptr(), qs, n_q, idx.data_ptr(), count.data_ptr(), k,
-                                             entry_tokens, scale, window, sinks, out.data_ptr(), os_, lse_at, ws_at, nbytes),
-            stream)
+    args = (cache.ref, B, q.data_ptr(), qs, n_q, idx.data_ptr(), count.data_ptr(), k, entry_tokens, scale, window, sinks)
+    outs = (out.data_ptr(), os_, lse_at, ws_at, nbytes)
+    if softcap == 0.0 and slopes is None:
+        _launch(cache.device, fn, _attend_topk, args + outs, stream)
+    else:
+        form = _attend_form("lsa_attend_topk_ex", cache, rows, n_q, softcap, slopes, None, None)
+        _launch(cache.device, "lsa_attend_topk_ex", _attend_topk_ex, (*args, form, *outs), stream)
+
+
+# ------------------------------------------------------------------ kept tokens and pages
+def _lists(fn, cache, idx, idx_offsets, count):
+    torch, B, dev = _torch(), cache.B, cache.device
+    _want(fn, "idx", idx, torch.int32, (idx.numel(),), dev)
+    if idx_offsets.shape not in ((B,), (B + 1,)):
+        _refuse(fn, f"idx_offsets must have {B} elements, or one more (got {list(idx_offsets.shape)})")
+    _want(fn, "idx_offsets", idx_offsets, torch.int64, idx_offsets.shape, dev)
+    _want(fn, "count", count, torch.int32, (B,), dev)
+    return idx.data_ptr(), idx_offsets.data_ptr(), count.data_ptr()
+
+
+def _layers(fn, name, caches, device):
+    """The lsa_kv_cache array of these layers."""
+    if not caches or any(c.device != device for c in caches):
+        _refuse(fn, f"{name} must be caches on device {device}, one at least")
+    return (_KvCache * len(caches))(*[c._c for c in caches])
+
+
+def kv_kept(cache, *, idx, idx_offsets, count, out, entry_tokens=1, window=0, sinks=0, stream=None):
+    """lsa_kv_kept: idx [rows] int32, idx_offsets [B] (or [B + 1]) int64 and count [B] int32 as union_compact takes and writes
+    them; out [B] int32."""
+    fn = "lsa_kv_kept"
+    _int32(fn, entry_tokens, window, sinks)
+    lists = _lists(fn, cache, idx, idx_offsets, count)
+    _want(fn, "out", out, _torch().int32, (cache.B,), cache.device)
+    _launch(cache.device, fn, _kv_kept, (cache.ref, cache.B, *lists, entry_tokens, window, sinks, out.data_ptr()), stream)
+
+
+def kv_compact(caches, to, *, idx, idx_offsets, count, max_kept, entry_tokens=1, window=0, sinks=0, stream=None):
+    """lsa_kv_compact: `caches` and `to` lists of KvCache, one a layer; the lists as for kv_kept."""
+    fn = "lsa_kv_compact"
+    _int32(fn, entry_tokens, window, sinks, max_kept)
+    if len(caches) != len(to) or not caches:
+        _refuse(fn, f"as many caches from as to, and one at least (got {len(caches)} and {len(to)})")
+    dev, B = caches[0].device, caches[0].B
+    if any(c.B != B for c in (*caches, *to)):
+        _refuse(fn, f"all caches must have {B} sequences")
+    lists = _lists(fn, caches[0], idx, idx_offsets, count)
+    _launch(dev, fn, _kv_compact, (_layers(fn, "caches", caches, dev), _layers(fn, "to", to, dev), len(caches), B, *lists,
+                                   entry_tokens, window, sinks, max_kept), stream)
+
+
+class KvPool:
+    """The lsa_kv_pool that the caches of one or several layers share: refs [n_pages], page_table [B, pages] and kv_len [B],
+    all int32. Holds the tensors; the calls on the pool change their contents."""
+
+    def __init__(self, *, refs, page_table, kv_len, page_tokens):
+        fn, i32 = "KvPool", _torch().int32
+        if refs.dim() != 1 or kv_len.dim() != 1 or page_table.dim() != 2:
+            _refuse(fn, "refs must be [n_pages], kv_len [B] and page_table [B, pages]")
+        self.device = dev = refs.get_device()
+        self.n_pages, self.B, self.page_tokens = refs.shape[0], kv_len.shape[0], page_tokens
+        _int32(fn, page_tokens)
+        _want(fn, "refs", refs, i32, (self.n_pages,), dev)
+        _want(fn, "kv_len", kv_len, i32, (self.B,), dev)
+        _want(fn, "page_table", page_table, i32, (self.B, page_table.shape[1]), dev)
+        self.refs, self.page_table, self.kv_len = refs, page_table, kv_len
+        self._c = _KvPool(_p(refs), _p(page_table), _p(kv_len), page_table.shape[1], self.B, self.n_pages, page_tokens)
+        self.ref = ctypes.byref(self._c)
+
+
+def kv_extend(pool, n_new, *, missing=None, stream=None):
+    """lsa_kv_extend: n_new [B] int32, missing [B] int32 or None."""
+    fn, i32 = "lsa_kv_extend", _torch().int32
+    _want(fn, "n_new", n_new, i32, (pool.B,), pool.device)
+    missing_at = None
+    if missing is not None:
+        _want(fn, "missing", missing, i32, (pool.B,), pool.device)
+        missing_at = missing.data_ptr()
+    _launch(pool.device, fn, _kv_extend, (pool.ref, n_new.data_ptr(), missing_at), stream)
+
+
+def kv_fork_workspace_size(n) -> int:
+    return int(_kv_fork_ws(n))
+
+
+def kv_fork(pool, caches, src, dst, *, status, workspace, stream=None):
+    """lsa_kv_fork: `caches` a list of KvCache, one a layer; src, dst and status [n] int32; workspace a tensor of at least
+    kv_fork_workspace_size(n) bytes."""
+    fn, i32, dev = "lsa_kv_fork", _torch().int32, pool.device
+    n = src.numel()
+    _want(fn, "src", src, i32, (n,), dev)
+    _want(fn, "dst", dst, i32, (n,), dev)
+    _want(fn, "status", status, i32, (n,), dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(fn, f"workspace must be contiguous and on device {dev}")
+    _launch(dev, fn, _kv_fork, (pool.ref, _layers(fn, "caches", caches, dev), len(caches), n, src.data_ptr(), dst.data_ptr(),
+                                status.data_ptr(), workspace.data_ptr(), workspace.nbytes), stream)
+
+
+def kv_free(pool, seqs, *, stream=None):
+    """lsa_kv_free: seqs [n] int32."""
+    fn = "lsa_kv_free"
+    n = seqs.numel()
+    _want(fn, "seqs", seqs, _torch().int32, (n,), pool.device)
+    _launch(pool.device, fn, _kv_free, (pool.ref, n, seqs.data_ptr()), stream)
