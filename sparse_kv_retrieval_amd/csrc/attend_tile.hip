@@ -231,37 +231,79 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   };
   auto seen = [&](int t) __attribute__((always_inline)) { return t <= e_row && (t > w_row || t < a.sinks) && (!SEEN || t >= f_row); };
 
+  // The maximum is raised by the greatest score and the greatest bias of 32 keys, which may not meet. It is then up to 31 slope log2(e)
+  // too high: 2^45 for a slope of 1, for which fp32 and bf16 have room. Blocks with steeper heads look at each key.
+  const bool steep = BIAS && __any(!(fabsf(slope) <= LOG2E));
+  // A cap makes a score of minus infinity finite, so masked places hold NaN instead. In bf16 the probabilities are then held below
+  // 1, where the clamp changes no other one.
+  constexpr float SHIFT = CAP && !FP8 ? ATTEND_LAZY : 0.f;
   // Scores of 32 keys before their softmax: register i of a lane is key 8 (i / 4) + 4 h + i % 4. Applies the mask and
   // raises the maximum; returns whether it rose for some row of the wave, and then what to scale by in `fall`.
   auto settle = [&](int buf, int t0, int u, bool whole, bool here0, bool here1, f32x16& s, float& fall) __attribute__((always_inline)) -> bool {
-    if constexpr (CAP || BIAS) {  // scores in base 2 from here on, capped and with their bias
-      const int near = p_row - (t0 + 32 * u + 4 * h);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[i] *= FP8 ? s_kc[buf][2 * u + i / 8] : c;
-        if constexpr (CAP) s[i] = cap_score(a, s[i]);
-        if constexpr (BIAS) s[i] = __builtin_fmaf(-slope, fabsf((float)(near - (8 * (i / 4) + i % 4))), s[i]);
-      }
-    }
+    uint32_t visible = ~0u;
     if (!whole) {
       // a bit for each of the 32 keys from the lane's first on: x <= hi, and x > lo or x < few
       const int base = t0 + 32 * u + 4 * h;
-      const uint32_t in = low_bits(e_row - base + 1) & (~low_bits(w_row - base + 1) | low_bits(a.sinks - base)) &
-                          (SEEN ? ~low_bits(f_row - base) : ~0u) & ((here0 ? 0x0000FFFFu : 0u) | (here1 ? 0xFFFF0000u : 0u));
+      visible = low_bits(e_row - base + 1) & (~low_bits(w_row - base + 1) | low_bits(a.sinks - base)) &
+                          (SEEN ? ~low_bits(f_row - base) : ~0u) &
+                          ((here0 ? 0x0000FFFFu : 0u) | (here1 ? 0xFFFF0000u : 0u));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const uint32_t see = __builtin_amdgcn_sbfe((int)in, 8 * (i / 4) + i % 4, 1);  // all ones or none
+        const uint32_t see = __builtin_amdgcn_sbfe((int)visible, 8 * (i / 4) + i % 4, 1);  // all ones or none
         s[i] = __uint_as_float((__float_as_uint(s[i]) & see) | (0xFF800000u & ~see));
       }
     }
+    // Without a cap the bias is taken as linear in the position, slope * (t - p). Beyond the row, where only a prefix is seen, the scores
+    // make up for it.
+    const bool bent = BIAS && !CAP && a.prefix_end && t0 + 32 * u + 31 > w.p_lo;
+    if (bent) {
+      const int beyond = t0 + 32 * u + 4 * h - p_row;
+      float back[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) back[x] = -2.f * slope / (FP8 ? s_kc[buf][2 * u + x] : c);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = __builtin_fmaf(back[i / 8], (float)max(beyond + 8 * (i / 4) + i % 4, 0), s[i]);
+    }
+    // where NaN stands for what is masked, a maximum that passes it on shows the others
+    auto greater = [](float x, float y) __attribute__((always_inline)) { return CAP ? __builtin_elementwise_maximum(x, y) : fmaxf(x, y); };
     float top = s[0], top1 = s[8];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
-      top = fmaxf(top, s[i]);
-      top1 = fmaxf(top1, s[8 + i]);
+      top = greater(top, s[i]);
+      top1 = greater(top1, s[8 + i]);
     }
-    if constexpr (CAP || BIAS) top = fmaxf(top, top1);
-    else top = FP8 ? fmaxf(top * s_kc[buf][2 * u], top1 * s_kc[buf][2 * u + 1]) : fmaxf(top, top1) * c;
+    top = FP8 ? greater(top * s_kc[buf][2 * u], top1 * s_kc[buf][2 * u + 1]) : greater(top, top1) * c;
+    if constexpr (CAP) {
+      top = cap_score(a, top);
+      l = __builtin_fmaf(top, 0.f, l);
+    }
+    if constexpr (BIAS) {
+      if (!steep) {
+        // the greatest bias of the 32 keys: the nearest one's, or with a negative slope the farthest one's
+        const int lo = p_row - (t0 + 32 * u + 31), hi = lo + 31;
+        const int by = slope < 0.f ? (CAP ? max(-lo, hi) : hi) : bent ? lo : max(CAP ? max(lo, -hi) : lo, 0);
+        top = __builtin_fmaf(-slope, (float)by, top);
+      } else {
+        const float d0 = (float)(p_row - (t0 + 32 * u + 4 * h));
+        top = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float y = s[i] * (FP8 ? s_kc[buf][2 * u + i / 8] : c), d = d0 - (float)(8 * (i / 4) + i % 4);
+          if constexpr (CAP) {
+            y = visible >> (8 * (i / 4) + i % 4) & 1 ? cap_score(a, y) : y;
+            d = fabsf(d);
+          }
+          top = fmaxf(top, __builtin_fmaf(-slope, d, y));
+        }
+      }
+    }
+    if (CAP && !whole) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t see = __builtin_amdgcn_sbfe((int)visible, 8 * (i / 4) + i % 4, 1);
+        s[i] = __uint_as_float((__float_as_uint(s[i]) & see) | (0x7FC00000u & ~see));
+      }
+    }
     if (!__any(top > m + ATTEND_LAZY)) return false;
     const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
     const float high = fmaxf(m, fmaxf(__uint_as_float(o[0]), __uint_as_float(o[1])));
@@ -287,19 +329,40 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto step = [&](int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next, int old_buf, int old_u) __attribute__((always_inline)) {
+  auto step = [&](int t0, int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next, int old_buf, int old_u) __attribute__((always_inline)) {
     constexpr int E = 16 / KS;  // exponentials of a group
     static_assert(KS == 2 * DT, "as many key steps as value operands");
-    float c2[2], add[2] = {-m, -m}, inv[2] = {1.f, 1.f};
-    c2[0] = c2[1] = CAP || BIAS ? 1.f : c;
+    float c2[2] = {c, c}, add[2] = {-m, -m}, inv[2] = {1.f, 1.f};
     if constexpr (FP8) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if constexpr (!CAP && !BIAS) c2[x] = s_kc[buf][2 * u + x];
+        c2[x] = s_kc[buf][2 * u + x];
         add[x] = s_vlog[buf][2 * u + x] - m;
         inv[x] = s_vinv[buf][2 * u + x];
       }
     }
+    const float d0 = BIAS ? (float)(p_row - (t0 + 32 * u + 4 * h)) : 0.f;
+    float line[2] = {add[0], add[1]};
+    if constexpr (CAP) {
+      c2[0] *= a.two_over_cap; c2[1] *= a.two_over_cap;
+      add[0] += a.cap_log2 - SHIFT; add[1] += a.cap_log2 - SHIFT;
+      line[0] = add[0]; line[1] = add[1];
+    }
+    if constexpr (BIAS) {
+      line[0] = __builtin_fmaf(-slope, d0, add[0]);
+      line[1] = __builtin_fmaf(-slope, d0, add[1]);
+    }
+    auto prob = [&](int i) __attribute__((always_inline)) {
+      const float at = (float)(8 * (i / 4) + i % 4);
+      float y = line[i / 8];
+      if constexpr (BIAS && CAP) y = __builtin_fmaf(-slope, fabsf(d0 - at), add[i / 8]);
+      else if constexpr (BIAS) y = __builtin_fmaf(slope, at, y);
+      if constexpr (!CAP) return __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c2[i / 8], y));
+      const float r = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[i] * c2[i / 8]));
+      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(-2.f * a.cap_log2, r, y));
+      // NaN in a masked place becomes 0: in bf16 by the clamp of the exponential itself, which costs nothing
+      return FP8 ? fmaxf(e, 0.f) : __builtin_amdgcn_fmed3f(e, 0.f, 1.f);
+    };
     uint32_t packed[8];
     s_next = (f32x16)(0.f);
 #pragma unroll
@@ -312,8 +375,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       acc[x % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vf[x % 3]), p[x / DT], acc[x % DT], 0, 0, 0);
 #pragma unroll
       for (int i = E * x; i < E * (x + 1); i += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c2[i / 8], add[i / 8]));
-        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 1], c2[i / 8], add[i / 8]));
+        const float e0 = prob(i), e1 = prob(i + 1);
         if constexpr (FP8) {
           l = __builtin_fmaf(e0, inv[i / 8], l);
           l = __builtin_fmaf(e1, inv[i / 8], l);
@@ -385,7 +447,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     // The probabilities before this step's belong to the maximum before it: the output is scaled after them.
     ahead(buf, 1, old, 1);
     bool rose = settle(buf, t0, 0, whole, h0, h1, s0, fall);
-    step(buf, 0, s0, buf, 1, s1, old, 1);
+    step(t0, buf, 0, s0, buf, 1, s1, old, 1);
     if (rose) scale_out(fall);
     // The next tile: its buffer was last read two barriers ago.
     if (i + 1 < count) {
@@ -399,7 +461,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     ahead(nb, 0, buf, 0);
     rose = settle(buf, t0, 1, whole, h2, h3, s1, fall);
     // after the last tile the next scores are those of an old buffer, and not used
-    step(buf, 1, s1, nb, 0, s0, buf, 0);
+    step(t0, buf, 1, s1, nb, 0, s0, buf, 0);
     if (rose) scale_out(fall);
     if (!whole) {
       const u32x4 odd = *(const u32x4*)s_odd[buf];
@@ -428,6 +490,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   }
 
   const float sum = sum_halves(l);
+  m += SHIFT;
   if (r >= w.n) return;
   if (parts <= 1) {
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
