@@ -27,7 +27,7 @@ struct Kept {
 };
 
 // For a whole wave, which agrees on the result.
-__device__ __forceinline__ Kept find_kept(const CompactArgs& a, int b) {
+__device__ __forceinline__ Kept find_kept(const KeptArgs& a, int b) {
   Kept k;
   const int64_t cap = a.from.table_stride << a.from.pt_log2;
   k.len = (int32_t)min((int64_t)max(a.kv_len[b], 0), cap);
@@ -39,10 +39,20 @@ __device__ __forceinline__ Kept find_kept(const CompactArgs& a, int b) {
   k.far = 0;
   const int n = max(a.count[b], 0);
   if (n == 0 || k.near == k.first) return k;
-  // the number of entries <= x
-  auto upto = [&](int32_t x) { return wave_find(n + 1, x, [&](int i) -> int64_t { return i == 0 ? INT64_MIN : k.list[i - 1]; }); };
-  k.lo = upto(k.first / a.r - 1);
-  const int hi = upto((k.near - 1) / a.r);
+  // The numbers of entries <= x and <= y, with the lanes at 64 places of both ends' ranges at once.
+  const int32_t x = k.first / a.r - 1, y = (k.near - 1) / a.r;
+  const int lane = threadIdx.x & 63;
+  int hi = 0;
+  for (int nx = n + 1, ny = n + 1; nx > 1 || ny > 1;) {
+    const int sx = (nx + 63) >> 6, sy = (ny + 63) >> 6, ax = lane * sx, ay = lane * sy;
+    const int px = k.lo + (ax < nx ? ax : 0), py = hi + (ay < ny ? ay : 0);
+    const int32_t ex = px > 0 ? k.list[px - 1] : INT32_MIN, ey = py > 0 ? k.list[py - 1] : INT32_MIN;
+    const int cx = __popcll(__ballot(ax < nx && ex <= x)) - 1, cy = __popcll(__ballot(ay < ny && ey <= y)) - 1;
+    k.lo += max(cx, 0) * sx; hi += max(cy, 0) * sy;
+    nx = min(sx, nx - max(cx, 0) * sx); ny = min(sy, ny - max(cy, 0) * sy);
+  }
+  k.lo = uni(k.lo);
+  hi = uni(hi);
   if (hi <= k.lo) return k;
   const int64_t begin = (int64_t)k.list[k.lo] * a.r, end = (int64_t)k.list[hi - 1] * a.r + a.r;
   k.cut = (int32_t)min(max((int64_t)k.first - begin, (int64_t)0), (int64_t)a.r - 1);
@@ -52,7 +62,7 @@ __device__ __forceinline__ Kept find_kept(const CompactArgs& a, int b) {
 }
 
 // The position that the i-th kept token has, or -1 (a list that is not ascending may hold anything).
-__device__ __forceinline__ int32_t kept_token(const CompactArgs& a, const Kept& k, int32_t i) {
+__device__ __forceinline__ int32_t kept_token(const KeptArgs& a, const Kept& k, int32_t i) {
   if (i < k.first) return i;
   const int64_t at = (int64_t)i - k.first;
   if (at >= k.far) return at - k.far < k.len - k.near ? (int32_t)(k.near + (at - k.far)) : -1;
@@ -69,7 +79,7 @@ __device__ __forceinline__ int32_t page_at(const PageMap& m, int b, int32_t pos)
   return page >= 0 && page < m.n_pages ? page : -1;
 }
 
-__global__ __launch_bounds__(CP_THREADS) void kept_kernel(const CompactArgs a, int32_t* kept) {
+__global__ __launch_bounds__(CP_THREADS) void kept_kernel(const KeptArgs a, int32_t* kept) {
   const int b = blockIdx.x * CP_WAVES + (threadIdx.x >> 6);
   if (b >= a.B) return;
   const Kept k = find_kept(a, b);
@@ -95,17 +105,17 @@ __global__ __launch_bounds__(CP_THREADS) void compact_kernel(const CompactArgs a
   const int group = (int)(id % a.groups), page_i = (int)((id / a.groups) % a.pages), b = (int)(id / a.groups / a.pages);
   const int32_t to_page = page_at(a.to, b, page_i * PT);
   if (to_page < 0) return;
-  const Kept k = find_kept(a, b);
+  const Kept k = find_kept(a.what, b);
   const int32_t i0 = page_i * PT, m = (int32_t)min(min(k.all(), (int64_t)a.max_kept) - i0, (int64_t)PT);
   if (m <= 0) return;
   for (int i = threadIdx.x; i < PT; i += CP_THREADS) {
     int32_t page = -1, tok = -1;
     if (i < m) {
-      tok = kept_token(a, k, i0 + i);
-      if (tok >= 0) page = page_at(a.from, b, tok);
+      tok = kept_token(a.what, k, i0 + i);
+      if (tok >= 0) page = page_at(a.what.from, b, tok);
     }
     s_page[i] = page;
-    s_row[i] = page < 0 ? -1 : (((int64_t)page * a.n_kv) << a.from.pt_log2) + (tok & ((1 << a.from.pt_log2) - 1));
+    s_row[i] = page < 0 ? -1 : (((int64_t)page * a.n_kv) << a.what.from.pt_log2) + (tok & ((1 << a.what.from.pt_log2) - 1));
   }
   __syncthreads();
   const int end = min((group + 1) * a.per_group, a.tiles);
@@ -126,7 +136,7 @@ __global__ __launch_bounds__(CP_THREADS) void compact_kernel(const CompactArgs a
           const int u = (i + e) * 64 + lane;
           const int64_t row = s_row[u / U];
           here[e] = row >= 0;
-          if (here[e]) x[e] = __builtin_nontemporal_load((const u32x4*)(src + (row + ((int64_t)h << a.from.pt_log2)) * ROW + u % U * 16));
+          if (here[e]) x[e] = __builtin_nontemporal_load((const u32x4*)(src + (row + ((int64_t)h << a.what.from.pt_log2)) * ROW + u % U * 16));
         }
 #pragma unroll
         for (int e = 0; e < P; ++e)
@@ -148,7 +158,7 @@ __global__ __launch_bounds__(CP_THREADS) void compact_kernel(const CompactArgs a
         x[e] = (u32x4){0, 0, 0, 0};
         s[e] = 0.f;
         if (here[e]) {
-          x[e] = __builtin_nontemporal_load((const u32x4*)(src + (row + ((int64_t)h << a.from.pt_log2)) * ROW + u % U * 16));
+          x[e] = __builtin_nontemporal_load((const u32x4*)(src + (row + ((int64_t)h << a.what.from.pt_log2)) * ROW + u % U * 16));
           s[e] = scales[(int64_t)s_page[u / U] * a.n_kv + h];
         }
       }
@@ -186,7 +196,7 @@ __global__ __launch_bounds__(CP_THREADS) void compact_kernel(const CompactArgs a
   }
 }
 
-hipError_t launch_kv_kept(const CompactArgs& a, int32_t* kept, hipStream_t s) {
+hipError_t launch_kv_kept(const KeptArgs& a, int32_t* kept, hipStream_t s) {
   kept_kernel<<<(a.B + CP_WAVES - 1) / CP_WAVES, CP_THREADS, 0, s>>>(a, kept);
   return hipGetLastError();
 }
@@ -194,7 +204,7 @@ hipError_t launch_kv_kept(const CompactArgs& a, int32_t* kept, hipStream_t s) {
 template <bool FP8, int D>
 static hipError_t launch_page(const CompactArgs& a, hipStream_t s) {
   constexpr int U = D * (FP8 ? 1 : 2) / 16;
-  const dim3 grid((unsigned)((int64_t)a.B * a.pages * a.groups));
+  const dim3 grid((unsigned)((int64_t)a.what.B * a.pages * a.groups));
   switch (a.to.pt_log2) {
     case 4: compact_kernel<FP8, D, 16 * U / 64><<<grid, CP_THREADS, 0, s>>>(a); break;
     case 5: compact_kernel<FP8, D, 32 * U / 64><<<grid, CP_THREADS, 0, s>>>(a); break;

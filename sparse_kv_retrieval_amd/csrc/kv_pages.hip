@@ -16,8 +16,8 @@ static constexpr int PG_THREADS = 256;    // of a block that goes through one se
 static constexpr int TAKE_THREADS = 1024; // of the block that takes pages
 static constexpr int TAKE_WAVES = TAKE_THREADS / 64;
 static constexpr int TAKE_CHUNK = 16 * TAKE_THREADS;  // pages looked at together
-static constexpr int TAKE_HELD = 4096;    // pages found before they are given out
 static constexpr int PER_THREAD = POOL_MAX / TAKE_THREADS;
+static constexpr int TAKE_HELD = 8192;    // pages found before they are given out
 
 __device__ __forceinline__ bool is_page(const PoolArgs& p, int32_t page) { return page >= 0 && page < p.n_pages; }
 
@@ -86,165 +86,192 @@ __global__ __launch_bounds__(PG_THREADS) void share_kernel(const PoolArgs p, int
   }
 }
 
-// Inclusive sum over the threads of a block of TAKE_THREADS, and the whole sum. `s_sums` is read until the next barrier of
+struct Two {
+  int32_t a, b;
+};
+// Inclusive sums over the threads of a block of TAKE_THREADS, and the whole sums. `s_sums` is read until the next barrier of
 // the caller's.
-template <typename T>
-__device__ __forceinline__ T block_scan(T x, T* s_sums, T* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const T y = __shfl_up(x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 63) s_sums[wave] = x;
+__device__ __forceinline__ Two block_scan(Two x, Two* s_sums, Two* total) {
+  const int wave = threadIdx.x >> 6;
+  x = {wave_scan(x.a), wave_scan(x.b)};
+  if ((threadIdx.x & 63) == 63) s_sums[wave] = x;
   __syncthreads();
-  T before = 0, all = 0;
+  Two all = {0, 0};
 #pragma unroll
   for (int w = 0; w < TAKE_WAVES; ++w) {
-    const T y = s_sums[w];
-    if (w < wave) before += y;
-    all += y;
+    const Two y = s_sums[w];
+    if (w < wave) x = {x.a + y.a, x.b + y.b};
+    all = {all.a + y.a, all.b + y.b};
   }
   *total = all;
-  return before + x;
+  return x;
 }
 
-// Which of the pages base .. base + 15 are free, as bits.
-__device__ __forceinline__ uint32_t free_bits(const PoolArgs& p, int64_t base) {
+// A chunk of pages is four runs of 4 * TAKE_THREADS; a thread has four pages of each, so that its neighbours' lie beside them. Which of
+// them are free, four bits a run.
+__device__ __forceinline__ uint32_t free_bits(const PoolArgs& p, int64_t chunk) {
   uint32_t bits = 0;
-  if (base + 16 <= p.n_pages) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x4 r = *(const u32x4*)(p.refs + base + 4 * i);
+  for (int i = 0; i < 4; ++i) {
+    const int64_t base = chunk + 4 * ((int64_t)i * TAKE_THREADS + threadIdx.x);
+    if (base + 4 <= p.n_pages) {
+      const u32x4 r = *(const u32x4*)(p.refs + base);
 #pragma unroll
       for (int e = 0; e < 4; ++e) bits |= ((int32_t)r[e] <= 0 ? 1u : 0u) << (4 * i + e);
+    } else {
+      for (int e = 0; e < 4 && base + e < p.n_pages; ++e) bits |= (p.refs[base + e] <= 0 ? 1u : 0u) << (4 * i + e);
     }
-  } else {
-    for (int i = 0; i < 16 && base + i < p.n_pages; ++i) bits |= (p.refs[base + i] <= 0 ? 1u : 0u) << i;
   }
   return bits;
 }
 
-// Looks for free pages from page *at on until `want` are found or all were looked at; the first TAKE_HELD of them go to s_ids, in
-// ascending order. Returns how many there are (at most `want`); *at becomes the first page of the last chunk, where a search
-// that goes on after those pages were taken begins.
-__device__ __forceinline__ int32_t find_free(const PoolArgs& p, int64_t* at, int32_t want, int32_t* s_ids, int32_t (*s_sums)[TAKE_WAVES]) {
+// Looks for free pages from page *at on, whose chunk's bits are `next`, until `want` are found or all were looked at; the first TAKE_HELD
+// of them go to s_ids, in ascending order. Returns how many there are (at most `want`); *at becomes the first page of the last chunk,
+// where a search that goes on after those pages were taken begins.
+__device__ __forceinline__ int32_t find_free(const PoolArgs& p, int64_t* at, uint32_t next, int32_t want, int32_t* s_ids, Two (*s_sums)[TAKE_WAVES]) {
   int64_t found = 0, chunk = *at;
   int turn = 0;
-  uint32_t next = free_bits(p, chunk + 16 * (int64_t)threadIdx.x);
+  const int32_t most = min(want, TAKE_HELD);
   for (; found < want && chunk < p.n_pages; chunk += TAKE_CHUNK, turn ^= 1) {
     *at = chunk;
     const uint32_t bits = next;
     // the next chunk is on its way while this one is counted
-    next = free_bits(p, chunk + TAKE_CHUNK + 16 * (int64_t)threadIdx.x);
-    int32_t total;
-    const int32_t n = __popc(bits), upto = block_scan(n, s_sums[turn], &total);
-    int64_t rank = found + upto - n;
-    for (uint32_t left = bits; left && rank < min(want, TAKE_HELD); left &= left - 1, ++rank)
-      s_ids[rank] = (int32_t)(chunk + 16 * threadIdx.x + __ffs(left) - 1);
-    found += total;
+    next = free_bits(p, chunk + TAKE_CHUNK);
+    // the runs' counts, two to a number: none is above 4 * TAKE_THREADS
+    auto count = [&](int i) -> int32_t { return __popc(bits >> (4 * i) & 15); };
+    const Two mine = {count(0) | count(1) << 16, count(2) | count(3) << 16};
+    Two all;
+    const Two upto = block_scan(mine, s_sums[turn], &all);
+    const Two before = {upto.a - mine.a, upto.b - mine.b};
+    const int32_t ends[4] = {all.a & 0xFFFF, all.a >> 16, all.b & 0xFFFF, all.b >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int64_t rank = found + ((i < 2 ? before.a : before.b) >> (16 * (i & 1)) & 0xFFFF);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (bits >> (4 * i + e) & 1) {
+          if (rank < most) s_ids[rank] = (int32_t)(chunk + 4 * (i * TAKE_THREADS + (int)threadIdx.x) + e);
+          ++rank;
+        }
+      found += ends[i];
+    }
   }
   __syncthreads();  // s_ids is whole
   return (int32_t)min(found, (int64_t)want);
 }
 
+// Sequence i * TAKE_THREADS + (thread) is the thread's i-th. What all of them have beyond the first is skipped where there are few.
 __global__ __launch_bounds__(TAKE_THREADS) void extend_kernel(const PoolArgs p, const int32_t* n_new, int32_t* missing) {
   __shared__ int32_t s_ids[TAKE_HELD], s_upto[POOL_MAX], s_have[POOL_MAX];
-  __shared__ int32_t s_sums[2][TAKE_WAVES];
-  __shared__ int64_t s_sums64[TAKE_WAVES];
+  __shared__ Two s_sums[2][TAKE_WAVES];
   __shared__ int32_t s_limit;
-  const int b0 = PER_THREAD * threadIdx.x;
-  int64_t need[PER_THREAD], mine = 0, total;
-  int32_t after[PER_THREAD];  // the length with the new tokens
+  constexpr int LOW = 18;  // bits of a sum that are added apart: TAKE_THREADS times 2^18 fits 32 bits
+  int64_t total = 0;
+  int32_t need[PER_THREAD] = {}, upto[PER_THREAD], after[PER_THREAD];  // pages, their sum up to here, the length with the new tokens
   bool fits[PER_THREAD];
 #pragma unroll
   for (int i = 0; i < PER_THREAD; ++i) {
-    need[i] = 0;
-    fits[i] = true;
-    if (b0 + i >= p.B) continue;
-    const int64_t len = held_len(p, b0 + i), more = max(n_new[b0 + i], 0);
-    const int64_t have = pages_of(p, len), want = pages_of(p, len + more);
-    fits[i] = more == 0 || (want <= p.table_stride && len + more <= INT32_MAX);
-    after[i] = (int32_t)(fits[i] ? len + more : len);
-    need[i] = fits[i] ? want - have : 0;
-    s_have[b0 + i] = (int32_t)have;
-    mine += need[i];
+    if (i * TAKE_THREADS >= p.B) break;
+    const int b = i * TAKE_THREADS + threadIdx.x;
+    if (b < p.B) {
+      const int64_t len = held_len(p, b), more = max(n_new[b], 0), have = pages_of(p, len), want = pages_of(p, len + more);
+      fits[i] = more == 0 || (want <= p.table_stride && len + more <= INT32_MAX);
+      after[i] = (int32_t)(fits[i] ? len + more : len);
+      need[i] = fits[i] ? (int32_t)(want - have) : 0;
+      s_have[b] = (int32_t)have;
+    }
+    Two all;
+    const Two sum = block_scan({need[i] & ((1 << LOW) - 1), need[i] >> LOW}, s_sums[i & 1], &all);
+    upto[i] = (int32_t)min(total + ((int64_t)sum.b << LOW) + sum.a, (int64_t)INT32_MAX);
+    if (b < p.B) s_upto[b] = upto[i];
+    total += ((int64_t)all.b << LOW) + all.a;
   }
-  int64_t upto = block_scan(mine, s_sums64, &total) - mine;
   if (threadIdx.x == 0) s_limit = 0;
   __syncthreads();
   int64_t at = 0;
   int32_t found = 0;
-  if (total > 0) {
-    // all that are asked for, or all that there are: the number decides who gets any
-    found = find_free(p, &at, (int32_t)min(total, (int64_t)p.n_pages), s_ids, s_sums);
-  }
+  // all that are asked for, or all that there are: the number decides who gets any
+  if (total > 0) found = find_free(p, &at, free_bits(p, 0), (int32_t)min(total, (int64_t)p.n_pages), s_ids, s_sums);
 #pragma unroll
   for (int i = 0; i < PER_THREAD; ++i) {
-    if (b0 + i >= p.B) continue;
-    upto += need[i];
-    const bool granted = need[i] == 0 || upto <= found;
-    s_upto[b0 + i] = (int32_t)min(upto, (int64_t)INT32_MAX);
-    if (granted && need[i] > 0) atomicMax(&s_limit, (int32_t)upto);
-    if (missing) missing[b0 + i] = !fits[i] ? -1 : granted ? 0 : (int32_t)min(need[i], (int64_t)INT32_MAX);
-    if (granted && fits[i]) p.kv_len[b0 + i] = after[i];
+    if (i * TAKE_THREADS >= p.B) break;
+    const int b = i * TAKE_THREADS + threadIdx.x;
+    if (b >= p.B) continue;
+    const bool granted = need[i] == 0 || upto[i] <= found;
+    if (granted && need[i] > 0 && upto[i] > s_limit) atomicMax(&s_limit, upto[i]);
+    if (missing) missing[b] = !fits[i] ? -1 : granted ? 0 : need[i];
+    if (granted && fits[i]) p.kv_len[b] = after[i];
   }
+  if (total == 0) return;
   __syncthreads();
   const int32_t limit = s_limit;
   // s_ids holds the first of them; where there are more, the search goes on behind those that are taken by now
   if (found > TAKE_HELD) at = 0;
   for (int32_t done = 0; done < limit;) {
     const int32_t n = min(limit - done, TAKE_HELD);
-    if (done > 0) find_free(p, &at, n, s_ids, s_sums);
-    for (int32_t x = threadIdx.x; x < n; x += TAKE_THREADS) {
-      const int32_t rank = done + x;
-      int lo = 0, hi = p.B - 1;  // the first sequence with s_upto > rank
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s_upto[mid] > rank) hi = mid;
-        else lo = mid + 1;
+    if (done > 0) find_free(p, &at, free_bits(p, at), n, s_ids, s_sums);
+    constexpr int UN = 4;  // pages of a thread whose sequences are looked for side by side
+    for (int32_t x0 = 0; x0 < n; x0 += UN * TAKE_THREADS) {
+      int32_t seq[UN] = {};  // how many sequences end at or before the page's rank
+#pragma unroll 1
+      for (int step = POOL_MAX / 2; step; step >>= 1) {
+        if (step >= p.B) continue;
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          const int32_t rank = done + x0 + u * TAKE_THREADS + (int32_t)threadIdx.x;
+          if (seq[u] + step < p.B && s_upto[seq[u] + step - 1] <= rank) seq[u] += step;
+        }
       }
-      const int32_t page = s_ids[x], before = lo > 0 ? s_upto[lo - 1] : 0;
-      p.refs[page] = 1;
-      p.table[lo * p.table_stride + s_have[lo] + (rank - before)] = page;
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int32_t x = x0 + u * TAKE_THREADS + (int32_t)threadIdx.x;
+        if (x >= n) break;
+        const int32_t page = s_ids[x], before = seq[u] > 0 ? s_upto[seq[u] - 1] : 0;
+        p.refs[page] = 1;
+        p.table[seq[u] * p.table_stride + s_have[seq[u]] + (done + x - before)] = page;
+      }
     }
     done += n;
     __syncthreads();  // the counts are written before they are looked at again, and s_ids is read
   }
 }
 
-// The last pages of a fork: one page for each pair that copies, lowest first.
+// The last pages of a fork: one page for each pair that copies, lowest first. Pairs lie in the threads as sequences do above.
 __global__ __launch_bounds__(TAKE_THREADS) void take_tails_kernel(const PoolArgs p, int n, const int32_t* dst, int32_t* status, ForkPair* pairs) {
-  __shared__ int32_t s_ids[TAKE_HELD];
-  __shared__ int32_t s_sums[2][TAKE_WAVES], s_first[TAKE_WAVES];
-  static_assert(TAKE_HELD >= POOL_MAX, "every pair's page is held at once");
-  const int i0 = PER_THREAD * threadIdx.x;
-  int32_t tail[PER_THREAD], mine = 0, total;
+  __shared__ int32_t s_ids[POOL_MAX];  // every pair's page is held at once
+  __shared__ Two s_sums[2][TAKE_WAVES];
+  static_assert(TAKE_HELD >= POOL_MAX, "find_free fills no more than are wanted");
+  const uint32_t front = free_bits(p, 0);  // asked for beside the pairs
+  int32_t total = 0, found = 0, tail[PER_THREAD] = {}, rank[PER_THREAD];
 #pragma unroll
   for (int i = 0; i < PER_THREAD; ++i) {
-    tail[i] = i0 + i < n ? pairs[i0 + i].tail : 0;
-    mine += tail[i] > 0;
+    if (i * TAKE_THREADS >= n) break;
+    const int x = i * TAKE_THREADS + threadIdx.x;
+    if (x < n) tail[i] = pairs[x].tail;
+    Two all;
+    const Two sum = block_scan({tail[i] > 0, 0}, s_sums[i & 1], &all);
+    rank[i] = total + sum.a - 1;
+    total += all.a;
   }
-  int32_t rank = block_scan(mine, s_first, &total) - mine, found = 0;
+  __syncthreads();
   int64_t at = 0;
-  if (total > 0) found = find_free(p, &at, total, s_ids, s_sums);
+  if (total > 0) found = find_free(p, &at, front, total, s_ids, s_sums);
 #pragma unroll
   for (int i = 0; i < PER_THREAD; ++i) {
-    if (i0 + i >= n) continue;
+    const int x = i * TAKE_THREADS + threadIdx.x;
+    if (i * TAKE_THREADS >= n) break;
+    if (x >= n) continue;
     int32_t st = tail[i] < 0 ? -1 : 0;
-    if (tail[i] > 0) {
-      if (rank < found) {
-        const int32_t page = s_ids[rank], t = dst[i0 + i], len = p.kv_len[t];
-        p.refs[page] = 1;
-        p.table[t * p.table_stride + (len >> p.pt_log2)] = page;
-        p.kv_len[t] = len + tail[i];
-        pairs[i0 + i].dst_page = page;
-      } else {
-        st = 1;
-      }
-      ++rank;
+    if (tail[i] > 0 && rank[i] < found) {
+      const int32_t page = s_ids[rank[i]], t = dst[x], len = p.kv_len[t];
+      p.refs[page] = 1;
+      p.table[t * p.table_stride + (len >> p.pt_log2)] = page;
+      p.kv_len[t] = len + tail[i];
+      pairs[x].dst_page = page;
+    } else if (tail[i] > 0) {
+      st = 1;
     }
-    status[i0 + i] = st;
+    status[x] = st;
   }
 }
 
@@ -273,7 +300,7 @@ hipError_t launch_kv_extend(const PoolArgs& p, const int32_t* n_new, int32_t* mi
 hipError_t launch_kv_fork(const PoolArgs& p, int n, const int32_t* src, const int32_t* dst, int32_t* status, ForkPair* pairs,
                           hipStream_t s) {
   share_kernel<<<n, PG_THREADS, 0, s>>>(p, n, src, dst, pairs);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   take_tails_kernel<<<1, TAKE_THREADS, 0, s>>>(p, n, dst, status, pairs);
   return hipGetLastError();

@@ -23,20 +23,27 @@ struct PageMap {
   int32_t n_pages, pt_log2;
 };
 
-struct CompactArgs {
-  PageMap from, to;
+// Which tokens are kept.
+struct KeptArgs {
+  PageMap from;
   const int32_t* kv_len;
   const int32_t* idx;
   const int64_t* idx_offsets;
   const int32_t* count;
-  int32_t B, r, window, sinks, max_kept, n_kv;
+  int32_t B, r, window, sinks;
+};
+
+struct CompactArgs {
+  KeptArgs what;
+  PageMap to;
+  int32_t max_kept, n_kv;
   int32_t pages;             // destination pages of a sequence that the launch looks at
   int32_t groups, per_group; // blocks of a page, and the (layer, K or V, head) tiles of each
   int32_t tiles;             // L * 2 * n_kv
   CompactLayer layer[KV_LAYERS];
 };
 
-hipError_t launch_kv_kept(const CompactArgs& a, int32_t* kept, hipStream_t s);
+hipError_t launch_kv_kept(const KeptArgs& a, int32_t* kept, hipStream_t s);
 hipError_t launch_kv_compact(const CompactArgs& a, bool fp8, int d, hipStream_t s);
 
 // ---------------------------------------------------------------- the pool

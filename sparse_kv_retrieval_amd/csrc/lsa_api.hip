@@ -1081,13 +1081,13 @@ lsa_status check_layers(const lsa_kv_cache* c, int32_t L, const char* name, bool
 PageMap page_map(const KvView& v) { return {v.table, v.table_stride, v.n_pages, v.pt_log2}; }
 
 // The arguments that lsa_kv_kept and lsa_kv_compact share.
-lsa_status compact_args(CompactArgs* a, const KvView& from, int32_t B, const int32_t* idx, const int64_t* idx_offsets,
+lsa_status kept_args(KeptArgs* a, const KvView& from, int32_t B, const int32_t* idx, const int64_t* idx_offsets,
                         const int32_t* count, int32_t entry_tokens, int32_t window, int32_t sinks) {
   if (B < 1 || B > kKvMaxB) return fail(LSA_ERR_UNSUPPORTED, "B must be in [1, %d] (got %d)", kKvMaxB, B);
   if (!idx || !idx_offsets || !count) return fail(LSA_ERR_INVALID_ARG, "idx, idx_offsets and count must be set");
   if (entry_tokens < 1 || entry_tokens > 128) return fail(LSA_ERR_UNSUPPORTED, "entry_tokens must be in [1, 128] (got %d)", entry_tokens);
   if (window < 0 || sinks < 0) return fail(LSA_ERR_INVALID_ARG, "window and sinks must not be negative");
-  a->from = page_map(from); a->kv_len = from.kv_len; a->n_kv = from.n_kv;
+  a->from = page_map(from); a->kv_len = from.kv_len;
   a->idx = idx; a->idx_offsets = idx_offsets; a->count = count;
   a->B = B; a->r = entry_tokens; a->window = window; a->sinks = sinks;
   return LSA_OK;
@@ -1119,12 +1119,12 @@ extern "C" {
 
 lsa_status lsa_kv_kept(const lsa_kv_cache* from, int32_t B, const int32_t* idx, const int64_t* idx_offsets, const int32_t* count,
                        int32_t entry_tokens, int32_t window, int32_t sinks, int32_t* kept_out, hipStream_t stream) {
-  CompactArgs a{};
+  KeptArgs a{};
   KvView v;
   bool fp8 = false;
   lsa_status s;
   if ((s = check_cache(from, &fp8, &v)) != LSA_OK) return s;
-  if ((s = compact_args(&a, v, B, idx, idx_offsets, count, entry_tokens, window, sinks)) != LSA_OK) return s;
+  if ((s = kept_args(&a, v, B, idx, idx_offsets, count, entry_tokens, window, sinks)) != LSA_OK) return s;
   if (!kept_out) return fail(LSA_ERR_INVALID_ARG, "kept_out must be set");
   const hipError_t e = launch_kv_kept(a, kept_out, stream);
   return e == hipSuccess ? LSA_OK : hip_fail("lsa_kv_kept launch", e);
@@ -1141,12 +1141,13 @@ lsa_status lsa_kv_compact(const lsa_kv_cache* from, const lsa_kv_cache* to, int3
   if ((s = check_layers(to, L, "to", true, &to_fp8, &w)) != LSA_OK) return s;
   if (fp8 != to_fp8 || v.n_kv != w.n_kv || from->d_h != to->d_h)
     return fail(LSA_ERR_INVALID_ARG, "from and to must have equal dtype, n_kv and d_h");
-  if ((s = compact_args(&a, v, B, idx, idx_offsets, count, entry_tokens, window, sinks)) != LSA_OK) return s;
+  if ((s = kept_args(&a.what, v, B, idx, idx_offsets, count, entry_tokens, window, sinks)) != LSA_OK) return s;
   const int32_t pt = to->page_tokens;
   if (max_kept < 0 || max_kept > to->table_stride * pt)
     return fail(LSA_ERR_INVALID_ARG, "max_kept must be in [0, table_stride * page_tokens] of the destination (got %d)", max_kept);
   if (max_kept == 0) return LSA_OK;
   a.to = page_map(w);
+  a.n_kv = v.n_kv;
   a.max_kept = max_kept;
   a.pages = (max_kept - 1) / pt + 1;
   const int64_t all = (int64_t)B * a.pages;

@@ -627,14 +627,20 @@ def attend_topk(cache, q, *, idx, count, out, scale, entry_tokens=1, window=0, s
 
 
 # ------------------------------------------------------------------ kept tokens and pages
+def _vector(fn, name, t, dtype, n, device):
+    """As _want for a [n] tensor (n None: of any length), and its address."""
+    if t.dtype is not dtype or t.dim() != 1 or (n is not None and len(t) != n) or t.get_device() != device or not t.is_contiguous():
+        _want(fn, name, t, dtype, (t.numel() if n is None else n,), device)
+    return t.data_ptr()
+
+
 def _lists(fn, cache, idx, idx_offsets, count):
     torch, B, dev = _torch(), cache.B, cache.device
-    _want(fn, "idx", idx, torch.int32, (idx.numel(),), dev)
-    if idx_offsets.shape not in ((B,), (B + 1,)):
-        _refuse(fn, f"idx_offsets must have {B} elements, or one more (got {list(idx_offsets.shape)})")
-    _want(fn, "idx_offsets", idx_offsets, torch.int64, idx_offsets.shape, dev)
-    _want(fn, "count", count, torch.int32, (B,), dev)
-    return idx.data_ptr(), idx_offsets.data_ptr(), count.data_ptr()
+    n = len(idx_offsets)
+    if n != B and n != B + 1:
+        _refuse(fn, f"idx_offsets must have {B} elements, or one more (got {n})")
+    return (_vector(fn, "idx", idx, torch.int32, None, dev), _vector(fn, "idx_offsets", idx_offsets, torch.int64, n, dev),
+            _vector(fn, "count", count, torch.int32, B, dev))
 
 
 def _layers(fn, name, caches, device):
@@ -650,8 +656,8 @@ def kv_kept(cache, *, idx, idx_offsets, count, out, entry_tokens=1, window=0, si
     fn = "lsa_kv_kept"
     _int32(fn, entry_tokens, window, sinks)
     lists = _lists(fn, cache, idx, idx_offsets, count)
-    _want(fn, "out", out, _torch().int32, (cache.B,), cache.device)
-    _launch(cache.device, fn, _kv_kept, (cache.ref, cache.B, *lists, entry_tokens, window, sinks, out.data_ptr()), stream)
+    out_at = _vector(fn, "out", out, _torch().int32, cache.B, cache.device)
+    _launch(cache.device, fn, _kv_kept, (cache.ref, cache.B, *lists, entry_tokens, window, sinks, out_at), stream)
 
 
 def kv_compact(caches, to, *, idx, idx_offsets, count, max_kept, entry_tokens=1, window=0, sinks=0, stream=None):
@@ -690,12 +696,9 @@ class KvPool:
 def kv_extend(pool, n_new, *, missing=None, stream=None):
     """lsa_kv_extend: n_new [B] int32, missing [B] int32 or None."""
     fn, i32 = "lsa_kv_extend", _torch().int32
-    _want(fn, "n_new", n_new, i32, (pool.B,), pool.device)
-    missing_at = None
-    if missing is not None:
-        _want(fn, "missing", missing, i32, (pool.B,), pool.device)
-        missing_at = missing.data_ptr()
-    _launch(pool.device, fn, _kv_extend, (pool.ref, n_new.data_ptr(), missing_at), stream)
+    at = _vector(fn, "n_new", n_new, i32, pool.B, pool.device)
+    missing_at = None if missing is None else _vector(fn, "missing", missing, i32, pool.B, pool.device)
+    _launch(pool.device, fn, _kv_extend, (pool.ref, at, missing_at), stream)
 
 
 def kv_fork_workspace_size(n) -> int:
@@ -707,18 +710,15 @@ def kv_fork(pool, caches, src, dst, *, status, workspace, stream=None):
     kv_fork_workspace_size(n) bytes."""
     fn, i32, dev = "lsa_kv_fork", _torch().int32, pool.device
     n = src.numel()
-    _want(fn, "src", src, i32, (n,), dev)
-    _want(fn, "dst", dst, i32, (n,), dev)
-    _want(fn, "status", status, i32, (n,), dev)
+    at = [_vector(fn, name, t, i32, n, dev) for name, t in (("src", src), ("dst", dst), ("status", status))]
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse(fn, f"workspace must be contiguous and on device {dev}")
-    _launch(dev, fn, _kv_fork, (pool.ref, _layers(fn, "caches", caches, dev), len(caches), n, src.data_ptr(), dst.data_ptr(),
-                                status.data_ptr(), workspace.data_ptr(), workspace.nbytes), stream)
+    _launch(dev, fn, _kv_fork, (pool.ref, _layers(fn, "caches", caches, dev), len(caches), n, *at, workspace.data_ptr(),
+                                workspace.nbytes), stream)
 
 
 def kv_free(pool, seqs, *, stream=None):
     """lsa_kv_free: seqs [n] int32."""
     fn = "lsa_kv_free"
     n = seqs.numel()
-    _want(fn, "seqs", seqs, _torch().int32, (n,), pool.device)
-    _launch(pool.device, fn, _kv_free, (pool.ref, n, seqs.data_ptr()), stream)
+    _launch(pool.device, fn, _kv_free, (pool.ref, n, _vector(fn, "seqs", seqs, _torch().int32, n, pool.device)), stream)
