@@ -140,7 +140,7 @@ __global__ __launch_bounds__(CP_THREADS) void compact_kernel(const CompactArgs a
         }
 #pragma unroll
         for (int e = 0; e < P; ++e)
-          if (here[e]) *(u32x4*)(dst + ((i + e) * 64 + lane) * 16) = x[e];
+          if (here[e]) __builtin_nontemporal_store(x[e], (u32x4*)(dst + ((i + e) * 64 + lane) * 16));
       }
     } else {
       const float* scales = is_v ? l.v_scale : l.k_scale;
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(CP_THREADS) void compact_kernel(const CompactArgs a
           widen_codes(x[e][w], s[e], y);
           z[w] = pack_e4m3(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
         }
-        *(u32x4*)(dst + (e * 64 + lane) * 16) = z;
+        __builtin_nontemporal_store(z, (u32x4*)(dst + (e * 64 + lane) * 16));
       }
     }
   }

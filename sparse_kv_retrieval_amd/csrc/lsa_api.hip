@@ -653,7 +653,7 @@ namespace {
 // Limits of the paged-cache calls.
 constexpr int32_t kKvMaxB = 4096, kKvMaxHeads = 1024, kKvMaxGroup = 1024;
 constexpr int64_t kMaxBlocks = (1 << 24) - 1;          // of 256 threads: a launch has fewer than 2^32
-constexpr int64_t kCompactBlocks = 2048;               // of a compaction: eight for each of 256 compute units
+constexpr int64_t kCompactBlocks = 8192;               // of a compaction, several rounds, so that none ends the call alone
 constexpr size_t kPartialBytes = (size_t)256 << 20;    // partial results of the tile kernel, where more than two splits fit
 
 bool multiple8(int64_t x) { return x % 8 == 0; }
