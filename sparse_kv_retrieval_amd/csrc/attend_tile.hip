@@ -42,6 +42,9 @@ static_assert(TL_M == 32 * TL_WAVES, "a wave has 32 rows");
 static constexpr int TL_BUFS = 3;
 static constexpr int TL_SUBS = TL_N / 16;
 static_assert(TL_WAVES == 2 * TL_SUBS, "one wave fetches 16 rows of K or of V");
+// Tiles whose places a block finds at once: a multiple of the buffers, and with those that are fetched ahead a thread for each 16 rows.
+static constexpr int TL_RUN = 96, TL_AHEAD = 3;
+static_assert(TL_RUN % TL_BUFS == 0 && (TL_RUN + TL_AHEAD) * TL_SUBS <= TL_THREADS, "places");
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -75,6 +78,9 @@ __device__ __forceinline__ void split_scale(float s, float* pow2, float* rest) {
   *rest = s * __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
+// Of a tile: bit i says that its i-th 16 keys are there, FLAG_WHOLE that all are and every row sees them.
+static constexpr uint32_t FLAG_WHOLE = 1u << TL_SUBS;
+
 template <bool FP8, int D, int FORM>
 __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const AttendArgs a) {
   constexpr int CPR = D / 8;                  // 16-byte chunks of a row in LDS
@@ -86,7 +92,8 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   __shared__ __attribute__((aligned(16))) char s_k[TL_BUFS][TL_N * ROWB], s_v[TL_BUFS][TL_N * ROWB];
   // what is left of the scales of 16 keys: of K times c, of V as log2 and reciprocal
   __shared__ __attribute__((aligned(16))) float s_kc[TL_BUFS][TL_SUBS], s_vlog[TL_BUFS][TL_SUBS], s_vinv[TL_BUFS][TL_SUBS];
-  __shared__ __attribute__((aligned(16))) int32_t s_here[TL_BUFS][TL_SUBS];  // whether the 16 keys are there
+  // Of 16 keys of a tile: where they lie, in rows (negative: nowhere), what the tile's subs and rows have (see FLAG_WHOLE), and its position.
+  __shared__ __attribute__((aligned(16))) u32x4 s_place[TL_RUN + TL_AHEAD][TL_SUBS];
   __shared__ __attribute__((aligned(16))) int32_t s_odd[TL_BUFS][TL_SUBS];   // whether values were taken out
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), col = lane & 31, h = lane >> 5;
@@ -118,20 +125,34 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     for (int s = 0; s < KS; ++s) q[s] = as_bf16x8((*(const u32x4*)(from + 16 * s) & keep) ^ flip);
   }
 
-  // The 16 tokens of tile i that this wave fetches: the first one's position, or -1 where no row sees
-  // any of them, and the page that holds them. The page is asked for one tile ahead of its use, so
-  // that reading it never waits for the tile's own loads.
-  auto tokens = [&](int i) __attribute__((always_inline)) -> int {
-    if (i >= count) return -1;
-    const int t = w.near.tile(first + i) * TL_N + sub * 16;
-    return t > end_hi<FORM>(w) || !some_begin<FORM>(a, w, t, t + 15) ? -1 : t;
-  };
   const int32_t* table = a.c.table + w.b * a.c.table_stride;
-  auto page_of = [&](int t) __attribute__((always_inline)) -> int32_t { return table[max(t, 0) >> a.c.pt_log2]; };
-  auto place = [&](int t, int32_t page) __attribute__((always_inline)) -> int64_t {
-    page = uni(page);
-    if (t < 0 || page < 0 || page >= a.c.n_pages) return -1;
+  // The cached row of a position that some row sees, or -1.
+  auto row_of = [&](int t) __attribute__((always_inline)) -> int64_t {
+    const int32_t page = table[t >> a.c.pt_log2];
+    if (page < 0 || page >= a.c.n_pages) return -1;
     return (((int64_t)page * a.c.n_kv + kv) << a.c.pt_log2) + (t & ((1 << a.c.pt_log2) - 1));
+  };
+  auto whole_tile = [&](int t0) __attribute__((always_inline)) { return t0 + TL_N - 1 <= end_lo<FORM>(w) && all_begin<FORM>(a, w, t0, t0 + TL_N - 1); };
+  // Finds the places of the tiles from `base` on, a thread for each 16 keys, so that the loop over the tiles has no page to wait for and
+  // few scalar instructions: two waves a SIMD hide little of either.
+  auto resolve = [&](int base) __attribute__((always_inline)) {
+    const int x = tid / TL_SUBS;  // its tile
+    if (x >= TL_RUN + TL_AHEAD) return;
+    const int i = base + x, t0 = i < count ? w.near.tile(first + i) * TL_N : 0, t = t0 + tid % TL_SUBS * 16;
+    int64_t row = -1;
+    if (i < count && t <= end_hi<FORM>(w) && some_begin<FORM>(a, w, t, t + 15)) row = row_of(t);
+    const uint32_t here = (uint32_t)(__ballot(row >= 0) >> (lane & ~(TL_SUBS - 1))) & ((1u << TL_SUBS) - 1);
+    const uint32_t flags = here | (i < count && here == (1u << TL_SUBS) - 1 && whole_tile(t0) ? FLAG_WHOLE : 0u);
+    s_place[x][tid % TL_SUBS] = (u32x4){(uint32_t)row, (uint32_t)((uint64_t)row >> 32), flags, (uint32_t)t0};
+  };
+  struct Place {
+    int64_t row;
+    uint32_t flags;
+    int32_t t0;
+  };
+  auto place_of = [&](int x) __attribute__((always_inline)) -> Place {
+    const u32x4 y = s_place[x][sub];
+    return {uni((int64_t)(((uint64_t)y[1] << 32) | y[0])), (uint32_t)uni((int32_t)y[2]), uni((int32_t)y[3])};
   };
 
   u32x4 in[LOADS];
@@ -144,19 +165,17 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     for (int i = 0; i < LOADS; ++i) in[i] = *(const u32x4*)(src + row0 * (SRC * 16) + (uint32_t)((i * 64 + lane) * 16));
     if constexpr (FP8) in_scale = src_scale[row0 >> a.c.pt_log2];
   };
-  auto whole_tile = [&](int t0) __attribute__((always_inline)) { return t0 + TL_N - 1 <= end_lo<FORM>(w) && all_begin<FORM>(a, w, t0, t0 + TL_N - 1); };
   // Values that no row of the block sees become 0: a probability of 0 would not clear an infinity. (Keys
   // may stay, their scores are masked.) Where some rows see a value and others do not, one that is not
   // finite becomes 0 as well, and the tile is marked: rescue() brings it to the rows that see it.
-  auto store = [&](int buf, int i, int64_t at) __attribute__((always_inline)) {
-    const int t0 = w.near.tile(first + i) * TL_N + sub * 16;
-    if (is_v) {
+  auto store = [&](int buf, const Place& of) __attribute__((always_inline)) {
+    if (is_v && !(of.flags & FLAG_WHOLE)) {
       uint32_t odd = 0;
-      if (at < 0 || !whole_tile(t0 - sub * 16)) {
+      {
 #pragma unroll
         for (int e = 0; e < LOADS; ++e) {
-          const int t = t0 + (e * 64 + lane) / SRC;
-          const bool some = at >= 0 && t <= end_hi<FORM>(w) && some_begin<FORM>(a, w, t, t);
+          const int t = of.t0 + sub * 16 + (e * 64 + lane) / SRC;
+          const bool some = of.row >= 0 && t <= end_hi<FORM>(w) && some_begin<FORM>(a, w, t, t);
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const uint32_t x = some ? in[e][z] : 0u, bad = not_finite<FP8>(x);
@@ -167,12 +186,10 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       }
       const bool any = __any(odd != 0);
       if (lane == 0) s_odd[buf][sub] = any;
-    } else if (lane == 0) {
-      s_here[buf][sub] = at >= 0;
     }
     float pow2 = 1.f, rest = 1.f;
     if constexpr (FP8) {
-      if (at >= 0) split_scale(in_scale, &pow2, &rest);
+      if (of.row >= 0) split_scale(in_scale, &pow2, &rest);
       if (lane == 0) {
         if (is_v) {
           s_vlog[buf][sub] = __log2f(rest);
@@ -192,10 +209,11 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
         // Eight lanes write at once and meet 32 banks: half of them begin with the upper eight codes, or they would
         // all write even chunks, two to a bank.
         const bool turn = lane & 4;
+      const uint32_t y0 = in[e][0], y1 = in[e][1], y2 = in[e][2], y3 = in[e][3];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const bool upper = turn != (x == 1);
-          const uint32_t c0 = upper ? in[e][2] : in[e][0], c1 = upper ? in[e][3] : in[e][1];
+          const uint32_t c0 = upper ? y2 : y0, c1 = upper ? y3 : y1;
           const u32x2 lo = widen4(c0, pow2), hi = widen4(c1, pow2);
           *(u32x4*)(d + ((2 * ch + upper) ^ sw) * 16) = (u32x4){lo[0], lo[1], hi[0], hi[1]};
         }
@@ -401,7 +419,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     for (int j = 0; j < TL_N; ++j) {
       const int t = t0 + j;
       if (t > end_hi<FORM>(w) || !some_begin<FORM>(a, w, t, t)) continue;
-      const int64_t row = place(t, page_of(t));
+      const int64_t row = row_of(t);
       if (row < 0) continue;
       const char* from = a.c.v + row * (SRC * 16);
       const bool sees = seen(t);
@@ -417,20 +435,17 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     }
   };
 
-  int t_next = tokens(0);
-  int32_t page = page_of(t_next);
-  int64_t at = place(t_next, page);
-  t_next = tokens(1);
-  page = page_of(t_next);
   f32x16 s0 = (f32x16)(0.f), s1;
   float fall = 1.f;
+  Place now{}, next{};  // of the tile that is worked on, and of the one after it
   if (count > 0) {
-    fetch(at);
-    store(0, 0, at);
-    at = place(t_next, page);
-    t_next = tokens(2);
-    page = page_of(t_next);
-    fetch(at);  // beyond the run: row 0, not used
+    resolve(0);
+    __syncthreads();
+    now = place_of(0);
+    next = place_of(1);
+    fetch(now.row);
+    store(0, now);
+    fetch(next.row);  // beyond the run: row 0, not used
     // the first step's second product is of no probabilities and these values
     for (int i = tid; i < TL_N * ROWB / 16; i += TL_THREADS) *(u32x4*)(s_v[TL_BUFS - 1] + 16 * i) = (u32x4){0, 0, 0, 0};
     __syncthreads();
@@ -438,25 +453,20 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     for (int x = 0; x < KS; ++x) s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(k_operand(0, 0, x)), q[x], s0, 0, 0, 0);
   }
   // tile i, in a buffer known when compiled: its operands' LDS addresses are constants beside the lane's
-  auto tile = [&](int i, auto which) __attribute__((always_inline)) {
+  auto tile = [&](int i, int base, auto which) __attribute__((always_inline)) {
     constexpr int buf = decltype(which)::value, nb = (buf + 1) % TL_BUFS, old = (buf + TL_BUFS - 1) % TL_BUFS;
-    const int t0 = w.near.tile(first + i) * TL_N;
-    const u32x4 here = *(const u32x4*)s_here[buf];
-    const bool h0 = uni((int)here[0]), h1 = uni((int)here[1]), h2 = uni((int)here[2]), h3 = uni((int)here[3]);
-    const bool whole = h0 && h1 && h2 && h3 && whole_tile(t0);
+    const int t0 = now.t0;
+    const bool whole = now.flags & FLAG_WHOLE, h0 = now.flags & 1, h1 = now.flags & 2, h2 = now.flags & 4, h3 = now.flags & 8;
     // The probabilities before this step's belong to the maximum before it: the output is scaled after them.
     ahead(buf, 1, old, 1);
     bool rose = settle(buf, t0, 0, whole, h0, h1, s0, fall);
     step(t0, buf, 0, s0, buf, 1, s1, old, 1);
     if (rose) scale_out(fall);
-    // The next tile: its buffer was last read two barriers ago.
-    if (i + 1 < count) {
-      store(nb, i + 1, at);
-      at = place(t_next, page);
-      t_next = tokens(i + 3);
-      page = page_of(t_next);
-      fetch(at);
-    }
+    // The next tile: its buffer was last read two barriers ago. Beyond the run it is row 0, and not used.
+    store(nb, next);
+    now = next;
+    next = place_of(i - base + 2);
+    fetch(next.row);
     lds_barrier();  // the loads of the tile after next stay in flight
     ahead(nb, 0, buf, 0);
     rose = settle(buf, t0, 1, whole, h2, h3, s1, fall);
@@ -478,10 +488,17 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   typedef std::integral_constant<int, 0> B0;
   typedef std::integral_constant<int, 1> B1;
   typedef std::integral_constant<int, 2> B2;
-  for (int i = 0; i < count; i += 3) {
-    tile(i, B0{});
-    if (i + 1 < count) tile(i + 1, B1{});
-    if (i + 2 < count) tile(i + 2, B2{});
+  for (int base = 0; base < count; base += TL_RUN) {
+    if (base > 0) {
+      __syncthreads();
+      resolve(base);
+      __syncthreads();
+    }
+    for (int i = base, end = min(base + TL_RUN, count); i < end; i += 3) {
+      tile(i, base, B0{});
+      if (i + 1 < end) tile(i + 1, base, B1{});
+      if (i + 2 < end) tile(i + 2, base, B2{});
+    }
   }
   if (count > 0) {
     if (count % 3 == 1) last(B0{});
