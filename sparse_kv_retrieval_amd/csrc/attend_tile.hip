@@ -168,27 +168,27 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   // Values that no row of the block sees become 0: a probability of 0 would not clear an infinity. (Keys
   // may stay, their scores are masked.) Where some rows see a value and others do not, one that is not
   // finite becomes 0 as well, and the tile is marked: rescue() brings it to the rows that see it.
-  auto store = [&](int buf, const Place& of) __attribute__((always_inline)) {
+  float pow2 = 1.f;
+  auto clean = [&](int buf, const Place& of) __attribute__((always_inline)) {
     if (is_v && !(of.flags & FLAG_WHOLE)) {
       uint32_t odd = 0;
-      {
 #pragma unroll
-        for (int e = 0; e < LOADS; ++e) {
-          const int t = of.t0 + sub * 16 + (e * 64 + lane) / SRC;
-          const bool some = of.row >= 0 && t <= end_hi<FORM>(w) && some_begin<FORM>(a, w, t, t);
+      for (int e = 0; e < LOADS; ++e) {
+        const int t = of.t0 + sub * 16 + (e * 64 + lane) / SRC;
+        const bool some = of.row >= 0 && t <= end_hi<FORM>(w) && some_begin<FORM>(a, w, t, t);
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const uint32_t x = some ? in[e][z] : 0u, bad = not_finite<FP8>(x);
-            odd |= bad;
-            in[e][z] = x & ~bad;
-          }
+        for (int z = 0; z < 4; ++z) {
+          const uint32_t x = some ? in[e][z] : 0u, bad = not_finite<FP8>(x);
+          odd |= bad;
+          in[e][z] = x & ~bad;
         }
       }
       const bool any = __any(odd != 0);
       if (lane == 0) s_odd[buf][sub] = any;
     }
-    float pow2 = 1.f, rest = 1.f;
     if constexpr (FP8) {
+      float rest = 1.f;
+      pow2 = 1.f;
       if (of.row >= 0) split_scale(in_scale, &pow2, &rest);
       if (lane == 0) {
         if (is_v) {
@@ -199,27 +199,27 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
         }
       }
     }
+  };
+  // the e-th 16 bytes of each lane
+  auto store = [&](int buf, int e) __attribute__((always_inline)) {
     char* dst = is_v ? s_v[buf] : s_k[buf];
-#pragma unroll
-    for (int e = 0; e < LOADS; ++e) {
-      const int at_row = (e * 64 + lane) / SRC, ch = (e * 64 + lane) % SRC, rr = sub * 16 + at_row;
-      char* d = dst + rr * ROWB;
-      const int sw = is_v ? v_swizzle<CPR>(rr) : k_swizzle<CPR>(rr);
-      if constexpr (FP8) {
-        // Eight lanes write at once and meet 32 banks: half of them begin with the upper eight codes, or they would
-        // all write even chunks, two to a bank.
-        const bool turn = lane & 4;
+    const int at_row = (e * 64 + lane) / SRC, ch = (e * 64 + lane) % SRC, rr = sub * 16 + at_row;
+    char* d = dst + rr * ROWB;
+    const int sw = is_v ? v_swizzle<CPR>(rr) : k_swizzle<CPR>(rr);
+    if constexpr (FP8) {
+      // Eight lanes write at once and meet 32 banks: half of them begin with the upper eight codes, or they would
+      // all write even chunks, two to a bank.
+      const bool turn = lane & 4;
       const uint32_t y0 = in[e][0], y1 = in[e][1], y2 = in[e][2], y3 = in[e][3];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const bool upper = turn != (x == 1);
-          const uint32_t c0 = upper ? y2 : y0, c1 = upper ? y3 : y1;
-          const u32x2 lo = widen4(c0, pow2), hi = widen4(c1, pow2);
-          *(u32x4*)(d + ((2 * ch + upper) ^ sw) * 16) = (u32x4){lo[0], lo[1], hi[0], hi[1]};
-        }
-      } else {
-        *(u32x4*)(d + (ch ^ sw) * 16) = in[e];
+      for (int x = 0; x < 2; ++x) {
+        const bool upper = turn != (x == 1);
+        const uint32_t c0 = upper ? y2 : y0, c1 = upper ? y3 : y1;
+        const u32x2 lo = widen4(c0, pow2), hi = widen4(c1, pow2);
+        *(u32x4*)(d + ((2 * ch + upper) ^ sw) * 16) = (u32x4){lo[0], lo[1], hi[0], hi[1]};
       }
+    } else {
+      *(u32x4*)(d + (ch ^ sw) * 16) = in[e];
     }
   };
 
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   // One step over 32 keys (buf, u) does three things side by side: the scores of the next 32 keys, this
   // one's probabilities, and the second product of the ones before. The order is fixed group by group: one matrix
   // instruction of each product (they do not wait for each other), the LDS reads of the group after the
-  // next, and a share of the exponentials. What is left of V's scale rides in the exponent, and leaves
+  // next, a share of the exponentials, and what `beside` does. What is left of V's scale rides in the exponent, and leaves
   // the sum again by its reciprocal.
   bf16x8 p[2] = {as_bf16x8((u32x4){0, 0, 0, 0}), as_bf16x8((u32x4){0, 0, 0, 0})};
   u32x4 kf[3], vf[3];
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto step = [&](int t0, int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next, int old_buf, int old_u) __attribute__((always_inline)) {
+  auto step = [&](int t0, int buf, int u, const f32x16& s, int next_buf, int next_u, f32x16& s_next, int old_buf, int old_u, auto beside) __attribute__((always_inline)) {
     constexpr int E = 16 / KS;  // exponentials of a group
     static_assert(KS == 2 * DT, "as many key steps as value operands");
     float c2[2] = {c, c}, add[2] = {-m, -m}, inv[2] = {1.f, 1.f};
@@ -404,6 +404,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
         packed[i / 2] = pack_bf16(e0, e1);
         asm volatile("" : "+v"(packed[i / 2]), "+v"(l));  // here, and not sunk to where they are used
       }
+      beside(x);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -444,7 +445,9 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     now = place_of(0);
     next = place_of(1);
     fetch(now.row);
-    store(0, now);
+    clean(0, now);
+#pragma unroll
+    for (int e = 0; e < LOADS; ++e) store(0, e);
     fetch(next.row);  // beyond the run: row 0, not used
     // the first step's second product is of no probabilities and these values
     for (int i = tid; i < TL_N * ROWB / 16; i += TL_THREADS) *(u32x4*)(s_v[TL_BUFS - 1] + 16 * i) = (u32x4){0, 0, 0, 0};
@@ -460,18 +463,26 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     // The probabilities before this step's belong to the maximum before it: the output is scaled after them.
     ahead(buf, 1, old, 1);
     bool rose = settle(buf, t0, 0, whole, h0, h1, s0, fall);
-    step(t0, buf, 0, s0, buf, 1, s1, old, 1);
+    // Beside this step the next tile goes to its buffer, which was last read two barriers ago, and the one after it is asked for. Beyond
+    // the run it is row 0, and not used.
+    clean(nb, next);
+    step(t0, buf, 0, s0, buf, 1, s1, old, 1, [&](int x) __attribute__((always_inline)) {
+      constexpr int PER = (LOADS + KS - 3) / (KS - 2);  // stores of a group, from the second one to the last but one
+#pragma unroll
+      for (int e = 0; e < LOADS; ++e)
+        if (x == 1 + e / PER) store(nb, e);
+      if (x == KS - 1) {
+        now = next;
+        next = place_of(i - base + 2);
+        fetch(next.row);
+      }
+    });
     if (rose) scale_out(fall);
-    // The next tile: its buffer was last read two barriers ago. Beyond the run it is row 0, and not used.
-    store(nb, next);
-    now = next;
-    next = place_of(i - base + 2);
-    fetch(next.row);
     lds_barrier();  // the loads of the tile after next stay in flight
     ahead(nb, 0, buf, 0);
     rose = settle(buf, t0, 1, whole, h2, h3, s1, fall);
     // after the last tile the next scores are those of an old buffer, and not used
-    step(t0, buf, 1, s1, nb, 0, s0, buf, 0);
+    step(t0, buf, 1, s1, nb, 0, s0, buf, 0, [](int) {});
     if (rose) scale_out(fall);
     if (!whole) {
       const u32x4 odd = *(const u32x4*)s_odd[buf];
