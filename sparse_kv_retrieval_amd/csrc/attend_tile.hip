@@ -138,7 +138,8 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   auto resolve = [&](int base) __attribute__((always_inline)) {
     const int x = tid / TL_SUBS;  // its tile
     if (x >= TL_RUN + TL_AHEAD) return;
-    const int i = base + x, t0 = i < count ? w.near.tile(first + i) * TL_N : 0, t = t0 + tid % TL_SUBS * 16;
+    // With a bias the near keys go first: far ones hardly ever raise a maximum.
+    const int i = base + x, t0 = i < count ? w.near.tile(first + (BIAS ? count - 1 - i : i)) * TL_N : 0, t = t0 + tid % TL_SUBS * 16;
     int64_t row = -1;
     if (i < count && t <= end_hi<FORM>(w) && some_begin<FORM>(a, w, t, t + 15)) row = row_of(t);
     const uint32_t here = (uint32_t)(__ballot(row >= 0) >> (lane & ~(TL_SUBS - 1))) & ((1u << TL_SUBS) - 1);
