@@ -335,12 +335,19 @@ class Pipeline:
 
     # ------------------------------------------------------------- core attention of the decode steps
     def alloc_attention(self, *, n_q, n_kv, d_h=128, dtype="bf16", page_tokens=64, entry_tokens=4, window=128, sinks=4,
-                        max_steps=64, rot_dim=None, theta=10000.0):
+                        max_steps=64, rot_dim=None, theta=10000.0, softcap=0.0, slopes=None):
         """A paged cache per layer for every sequence's N_b * entry_tokens prompt tokens and max_steps more, and the
         buffers of attend_step. The lists that step() makes hold entries of the prompt, so the steps' own tokens are seen
-        through the window alone: it must cover max_steps."""
+        through the window alone: it must cover max_steps. softcap and slopes ([n_q] float32 on the device) are the backbone's
+        cap of its scores and its biases by distance (lsa_attend_topk_ex)."""
         if window < max_steps:
             raise ValueError(f"a window of {window} tokens would lose steps' tokens within max_steps = {max_steps}")
+        if softcap != 0 and not 2.0 ** -10 <= softcap <= 1024:
+            raise ValueError(f"softcap must be 0 or in [2^-10, 1024] (got {softcap})")
+        if slopes is not None:
+            device = torch.empty(0, device=self.device).get_device()
+            lsa._want("alloc_attention", "slopes", slopes, torch.float32, (n_q,), device)
+        self.softcap, self.slopes = softcap, slopes
         w, L, B = self.w, self.w.L, self.w.B
         bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
         self.entry_tokens, self.window, self.sinks, self.n_q, self.n_kv = entry_tokens, window, sinks, n_q, n_kv
@@ -438,7 +445,7 @@ class Pipeline:
                 lsa.attend_topk(self.caches[l], self.q_rot[l], idx=self.step_idx[l], count=self.step_count[l],
                                 entry_tokens=self.entry_tokens, scale=self.q_rot[l].shape[2] ** -0.5, window=self.window,
                                 sinks=self.sinks, out=self.attn_out[l], lse=self.attn_lse[l], workspace=self.attn_workspace,
-                                stream=stream)
+                                softcap=self.softcap, slopes=self.slopes, stream=stream)
 
     def load(self, stream=None):
         """The load step: from the host pool when there is one, else from HBM."""
