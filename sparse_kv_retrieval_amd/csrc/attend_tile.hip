@@ -118,11 +118,29 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   const int f_row = SEEN ? first_seen(a, w.t0 + tok) : 0;
   const int e_row = SEEN ? last_seen(a, w.t0 + tok, p_row, w.len) : p_row;
   const float slope = BIAS ? a.slopes[head] * LOG2E : 0.f;
+  // The wave's queries come, and its output leaves, in whole rows, through LDS that no tile is in: a lane's own pieces of its row are 32 bytes
+  // of a line here and 16 there. mine(row, chunk): where the wave's 32 rows lie, swizzled like keys.
+  static_assert(TL_WAVES / 2 * 32 <= TL_BUFS * TL_N, "half the waves' rows fit the keys' buffers");
+  constexpr int UNITS = 32 * CPR / 64;
+  auto mine = [&](int row, int chunk) __attribute__((always_inline)) {
+    return (wave < TL_WAVES / 2 ? s_k[0] : s_v[0]) + (wave % (TL_WAVES / 2) * 32 + row) * ROWB + (chunk ^ k_swizzle<CPR>(row)) * 16;
+  };
+  // what row `row` of the wave has of x
+  auto of_row = [&](int64_t x, int row) __attribute__((always_inline)) {
+    const uint32_t lo = __shfl((int)(uint32_t)x, row), hi = __shfl((int)(uint32_t)((uint64_t)x >> 32), row);
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+  };
   bf16x8 q[KS];
   {
-    const uint16_t* from = a.q + (w.t0 + tok) * a.q_stride + (int64_t)head * D + 8 * h;
+    const int64_t from = (w.t0 + tok) * a.q_stride + (int64_t)head * D;
+    u32x4 x[UNITS];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) q[s] = as_bf16x8((*(const u32x4*)(from + 16 * s) & keep) ^ flip);
+    for (int i = 0; i < UNITS; ++i) x[i] = *(const u32x4*)(a.q + of_row(from, i * (64 / CPR) + lane / CPR) + lane % CPR * 8);
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) *(u32x4*)mine(i * (64 / CPR) + lane / CPR, lane % CPR) = x[i];
+    // a wave's LDS accesses are in order, and no other wave's touch these rows before the barrier behind the places
+#pragma unroll
+    for (int s = 0; s < KS; ++s) q[s] = as_bf16x8((*(const u32x4*)mine(col, 2 * s + h) & keep) ^ flip);
   }
 
   const int32_t* table = a.c.table + w.b * a.c.table_stride;
@@ -520,18 +538,28 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
 
   const float sum = sum_halves(l);
   m += SHIFT;
-  if (r >= w.n) return;
   if (parts <= 1) {
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t* dst = a.out + (w.t0 + tok) * a.out_stride + (int64_t)head * D + 4 * h;
+    __syncthreads();  // no wave reads keys or values any more
+    int l2 = lane;
+    asm volatile("" : "+v"(l2));  // or the addresses of the beginning stay in registers until here
+    const int c2 = l2 & 31, h2 = l2 >> 5;
 #pragma unroll
     for (int e = 0; e < DT; ++e)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *(u32x2*)(dst + 32 * e + 2 * i) = (u32x2){pack_bf16(acc[e][i] * inv, acc[e][i + 1] * inv),
-                                                  pack_bf16(acc[e][i + 2] * inv, acc[e][i + 3] * inv)};
-    if (a.lse && h == 0) a.lse[(w.t0 + tok) * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (m + __log2f(sum)) * LN2;
-  } else {
+        *(u32x2*)(mine(c2, 4 * e + i / 4) + 8 * h2) = (u32x2){pack_bf16(acc[e][i] * inv, acc[e][i + 1] * inv),
+                                                              pack_bf16(acc[e][i + 2] * inv, acc[e][i + 3] * inv)};
+    const int64_t to = (w.t0 + tok) * a.out_stride + (int64_t)head * D;
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      const int unit_row = i * (64 / CPR) + l2 / CPR;
+      const int64_t at = of_row(to, unit_row);
+      const u32x4 y = *(const u32x4*)mine(unit_row, l2 % CPR);
+      if (wave * 32 + unit_row < w.n) *(u32x4*)(a.out + at + l2 % CPR * 8) = y;
+    }
+    if (a.lse && h == 0 && r < w.n) a.lse[(w.t0 + tok) * a.n_q + head] = sum == 0.f ? -__builtin_inff() : (m + __log2f(sum)) * LN2;
+  } else if (r < w.n) {
     const int64_t to = ((int64_t)split * a.T + (w.t0 - a.first_row + tok)) * a.n_q + head;
 #pragma unroll
     for (int e = 0; e < DT; ++e)
