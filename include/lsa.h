@@ -694,8 +694,9 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache /* host */, int32_t B, cons
  * directions), and a prompt's prefix of n tokens has prefix_end n in every row.
  *
  * Everything else is as for the plain calls, whose workspaces of the same sizes
- * they take. Precision: the capped score is formed in fp32, off by about
- * 2^-22 softcap; the bias is added in fp32, off by 2^-23 of its size.
+ * they take. Precision: the capped score is formed in fp32, off by at most
+ * 2^-20 softcap; the bias is added in fp32, off by 2^-23 of its size. A score
+ * whose products overflow fp32 with both signs is NaN, as in the plain call.
  * Supported: as the plain calls; softcap 0 or in [2^-10, 1024]; prefix_end only
  * without a window; lsa_attend_topk_ex takes neither doc_start nor prefix_end.
  * ---------------------------------------------------------------------- */

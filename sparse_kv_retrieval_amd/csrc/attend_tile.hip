@@ -8,8 +8,11 @@
 // lane's 16 scores of a 32-key half tile belong to one row and become the second product's operand
 // where they are (half h holds keys 8a + 4h + 0..3). Tiles of 64 keys go through three LDS buffers as
 // bf16 rows, swizzled so that no read or write meets in a bank, and V's operand comes from the transposing
-// LDS load. A wave fetches 16 rows of K or of V (one page) to registers one tile ahead of their LDS store and
-// two ahead of their use: one barrier per tile.
+// LDS load. A wave fetches 16 rows of K or of V (one page) to registers; beside a tile's first step the next tile goes
+// from there to LDS and the one after it is asked for: one barrier per tile. Where 16 rows lie, and whether all rows
+// see them all, is found for 96 tiles at once and waits in LDS, so that a tile begins with one LDS read instead of a chain of
+// two dependent reads of memory (two prompts of 4981 and 4888 tokens 831 against 858 us). Queries come and outputs
+// leave through LDS in whole rows: a lane's own pieces are 16 and 32 bytes of a line (799 against 815 us).
 //
 // Schedule. Three steps are in work at once: the scores of the next 32 keys, the exponentials of these and
 // the second product of the ones before, one matrix instruction of each product and two exponentials
@@ -20,15 +23,24 @@
 // goes in there, exactly; what is left of a scale that is no power of two rides in the exponentials'
 // argument and costs nothing.
 //
+// Forms (kv.hpp has the mathematics). Each is an instance of its own, so the plain one pays for none. Only tiles that
+// FLAG_WHOLE does not name look at masks. A cap adds an exponential and a reciprocal a score; masked scores are NaN
+// there, which the last exponential's clamp turns into 0. A bias is linear in the position up to the row itself, so it is one more
+// addend of the exponential's argument, and the maximum of 32 keys is bounded by the greatest score plus the greatest bias.
+// With a bias tiles go from the nearest to the farthest: the maximum then hardly ever rises (2107 against 2565 us for 2048
+// tokens on top of 30,720). Documents and prefixes shorten the range of tiles a block goes through.
+//
 // Measured on MI355X (64 query heads, 8 key heads, d_h 128; torch's bf16 matrix product of 8192^3 reaches
-// 1269 TFLOP/s there; the kernel's time in a trace): 2048 tokens on top of 30,720 in e4m3 2.1 ms (1.01 PFLOP/s); prompts of
-// 4981 and 4888 tokens in bf16 850 us (0.94 PFLOP/s); of 7203 and 6711 tokens with a window of 1024 593 us (0.73 PFLOP/s of
-// visible pairs). The matrix
-// pipes are busy 42 % of the time in the first, the vector ALUs about as long; without exponentials, LDS
-// reads, staging and maxima the second still takes 617 us. A block's first tile, its queries and its output
-// cost some 6 us that nothing overlaps, as one block fills a CU's registers and LDS: they are what
-// short and windowed prompts pay. Blocks of four waves and two buffers, two to a CU, were slower (2428 and 925 us
-// against 2190 and 865).
+// 1195 TFLOP/s there; whole calls in turn): 2048 tokens on top of 30,720 in e4m3 2.02 ms (1.05 PFLOP/s), with a bias 2.09;
+// prompts of 4981 and 4888 tokens in bf16 811 us (0.98 PFLOP/s), with a cap 1054; of 7203 and 6711 tokens with a window of 1024
+// 571 us (0.76 PFLOP/s of visible pairs); 8192 tokens of packed documents of 89 to 1519 220 us. The matrix
+// pipes are busy 49 % of the time in a plain prompt and 35 % in a capped one, the vector ALUs 50 and 67. Without
+// the exponentials a prompt takes 5 % less, without transposing reads 2, fetches 3, LDS stores 2, half of the first product 11: no
+// single one bounds it. A block's rows, places, queries, first tile and output cost some 14 us that nothing overlaps, as one block fills a
+// CU's registers and LDS: they are what documents and short or windowed prompts pay. Slower were blocks of four waves and two
+// buffers, two to a CU (2428 and 925 us against 2190 and 865); 64 rows a wave in four waves (1005 against 857); masks by
+// branches inside the groups (capped 1140 against 1076); exponentials before the maximum is known, and again where it rose
+// (biased 3311 against 2597).
 #include <type_traits>
 
 #include "kv.hpp"

@@ -8,6 +8,9 @@
 //
 // Everything here is bound by latency: launches and a few dependent reads (length, table, refs). Giving back and sharing have one
 // block per sequence, so that no two threads look at one entry; taking has one block, which needs no order between blocks.
+// Measured on MI355X, the kernels alone: 8 sequences of up to 4096 tokens free 2.5, extend 6.1, fork 3.2 + 4.4 + 2.5 us (share, take, copy); 64 sequences,
+// 16 of them admitted, eight samples each, over 29,177 pages 4.0, 9.9 and 4.9 + 6.0 + 3.7. A fork
+// in one launch of one block was slower (11.9 against 7.2 us): the pairs' entries then have one CU's latency after another.
 #include "kv_pages.hpp"
 
 namespace lsa {

@@ -1159,7 +1159,7 @@ lsa_status lsa_kv_compact(const lsa_kv_cache* from, const lsa_kv_cache* to, int3
       const lsa_kv_cache &x = from[l0 + l], &y = to[l0 + l];
       a.layer[l] = {(const char*)x.k, (const char*)x.v, x.k_scale, x.v_scale, (char*)y.k, (char*)y.v, y.k_scale, y.v_scale};
     }
-    // A page's tokens are found once a block: as few blocks a page as fill the device, each with a tile a wave at least.
+    // A page's tokens are found once a block: as few blocks a page as make kCompactBlocks, each with a tile a wave at least.
     a.tiles = n * 2 * a.n_kv;
     const int64_t groups = std::min<int64_t>((a.tiles + 3) / 4, (kCompactBlocks + all - 1) / all);
     a.per_group = (int32_t)((a.tiles + groups - 1) / groups);
