@@ -404,7 +404,7 @@ __device__ __forceinline__ float sum_column(float x) {
 }
 
 // A base-2 score y as cap * tanh(y / cap) with cap in the same unit: 1 - 2 / (1 + e^(2 z)) is tanh z, and no clamp is needed,
-// as the exponential's overflow and underflow give the two limits. Off by about 2^-23 cap_log2.
+// as the exponential's overflow and underflow give the two limits. Off by less than 2^-20 cap_log2.
 __device__ __forceinline__ float cap_score(const AttendArgs& a, float y) {
   const float e = __builtin_amdgcn_exp2f(y * a.two_over_cap);
   return __builtin_fmaf(-2.f * a.cap_log2, __builtin_amdgcn_rcpf(1.f + e), a.cap_log2);
