@@ -39,8 +39,10 @@
 // (44 bytes of scratch a lane): 64 rows over 131,072 tokens in bf16 take 108 us (5.0 TB/s) where 16 rows take 93 (5.8).
 //
 // Forms (kv.hpp). Caps and biases are instances of their own: the plain ones are as they were. What they add hides behind the
-// reads with 16 rows: 8 x 125,000 tokens take 609 us plain, 624 capped, 639 with a bias and with both (bf16; 333, 337, 338 and 344 in
-// e4m3). It shows with 64 rows, where one wave a SIMD has to do it: 8 x 40,000 tokens in bf16 take 45, 52, 56 and 57 us.
+// reads with 16 rows: 8 x 125,000 tokens take 610 us plain, 613 capped, 625 with a bias and 627 with both (bf16; 333, 336, 337 and 342 in
+// e4m3). Registers are what they are short of: a row's window, document and prefix lie in LDS, and a tile's distances are one number a row
+// and lane (without these bf16 spilled 8 and 19 registers instead of 2 and 8: 624, 639 and 639 us). With 64 rows, where one
+// wave a SIMD has to do it all, 8 x 40,000 tokens in bf16 take 46, 47, 47 and 52 us (45, 52, 56 and 57 before).
 #include "kv.hpp"
 
 namespace lsa {
@@ -135,6 +137,8 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
   constexpr bool SEEN = (FORM & FORM_SEEN) != 0, CAP = (FORM & FORM_CAP) != 0, BIAS = (FORM & FORM_BIAS) != 0;
   __shared__ int64_t s_row[RUN * PLACES];  // cached row of the place, or -1: nothing there
   __shared__ int32_t s_tok[LISTED && BIAS ? RUN * PLACES : 1];  // position of the place
+  // SEEN: what the rows' window, document and prefix let them see; only tiles at an edge ask, and registers are short
+  __shared__ int32_t s_edge[SEEN ? 3 : 1][SEEN ? M : 1];
   __shared__ float s_o[AT_WAVES][M][D + 4];
   __shared__ float s_m[AT_WAVES][M], s_l[AT_WAVES][M];
 
@@ -287,7 +291,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
   resolve(first, min(RUN, count));
   // the block's queries: lane column = row
   bf16x8 q[RT][KS];
-  int32_t p_row[RT], w_row[RT], f_row[SEEN ? RT : 1], e_row[SEEN ? RT : 1];
+  int32_t p_row[RT], w_row[SEEN ? 1 : RT];
   float slope[BIAS ? RT : 1];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -296,10 +300,12 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
     const int row = w.r0 + (live ? r : w.n - 1);
     const int tok = row / a.G;
     p_row[rt] = w.p0 + tok;
-    w_row[rt] = window_start(a, p_row[rt]);
-    if constexpr (SEEN) {
-      f_row[rt] = first_seen(a, w.t0 + tok);
-      e_row[rt] = last_seen(a, w.t0 + tok, p_row[rt], w.len);
+    if constexpr (!SEEN) {
+      w_row[rt] = window_start(a, p_row[rt]);
+    } else if (tid < 16) {  // for all waves, behind the places' barrier
+      s_edge[0][r] = window_start(a, p_row[rt]);
+      s_edge[1][r] = first_seen(a, w.t0 + tok);
+      s_edge[2][r] = last_seen(a, w.t0 + tok, p_row[rt], w.len);
     }
     if constexpr (BIAS) slope[rt] = a.slopes[h * a.G + (row - tok * a.G)] * LOG2E;
     const uint16_t* src = a.q + (w.t0 + tok) * a.q_stride + (int64_t)(h * a.G + (row - tok * a.G)) * D;
@@ -382,14 +388,22 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
     }
     if constexpr (BIAS) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int at = 16 * (j / 4) + 4 * g + j % 4, tok = LISTED ? s_tok[32 * i + at] : w.near.tile(base + i) * 32 + at;
+      for (int rt = 0; rt < RT; ++rt) {
+        // the distance to the lane's first key, and from there on
+        const float d = LISTED ? 0.f : (float)(p_row[rt] - (w.near.tile(base + i) * 32 + 4 * g));
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) x[rt][j] = __builtin_fmaf(-slope[rt], fabsf((float)(p_row[rt] - tok)), x[rt][j]);
+        for (int j = 0; j < 8; ++j) {
+          const int at = 16 * (j / 4) + j % 4;
+          const float far = LISTED ? (float)(p_row[rt] - s_tok[32 * i + at + 4 * g]) : d - (float)at;
+          x[rt][j] = __builtin_fmaf(-slope[rt], fabsf(far), x[rt][j]);
+        }
       }
     }
     auto sees = [&](int rt, int tok) {
-      if constexpr (SEEN) return tok <= e_row[rt] && tok >= f_row[rt] && (tok > w_row[rt] || tok < a.sinks);
+      if constexpr (SEEN) {
+        const int r = rt * 16 + col;
+        return tok <= s_edge[2][r] && tok >= s_edge[1][r] && (tok > s_edge[0][r] || tok < a.sinks);
+      }
       else return tok <= p_row[rt] && (tok > w_row[rt] || tok < a.sinks);
     };
     // masks
