@@ -280,8 +280,10 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   };
   auto seen = [&](int t) __attribute__((always_inline)) { return t <= e_row && (t > w_row || t < a.sinks) && (!SEEN || t >= f_row); };
 
-  // The maximum is raised by the greatest score and the greatest bias of 32 keys, which may not meet. It is then up to 31 slope log2(e)
-  // too high: 2^45 for a slope of 1, for which fp32 and bf16 have room. Blocks with steeper heads look at each key.
+  // The maximum is raised by the greatest score that a row sees among 32 keys and the greatest bias of the 32, which may not meet. Where it
+  // sees one of them it is then up to 31 slope log2(e) too high: 2^45 for a slope of 1, for which fp32 and bf16 have room. Where it sees none
+  // they must not raise it at all: their biases may be any distance away from those of the keys that it does see. Blocks with steeper
+  // heads look at each key.
   const bool steep = BIAS && __any(!(fabsf(slope) <= LOG2E));
   // A cap makes a score of minus infinity finite, so masked places hold NaN instead. In bf16 the probabilities are then held below
   // 1, where the clamp changes no other one.
@@ -325,6 +327,9 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     if constexpr (CAP) {
       top = cap_score(a, top);
       l = __builtin_fmaf(top, 0.f, l);
+      // The cap of minus infinity is finite. By the mask and not by the score, as a score of minus infinity that is seen counts as -cap; and
+      // without a bias no score lies below -cap, so there it does no harm.
+      if (BIAS && !whole) top = visible & 0x0F0F0F0Fu ? top : -__builtin_inff();
     }
     if constexpr (BIAS) {
       if (!steep) {
