@@ -747,7 +747,7 @@ lsa_status lsa_attend_topk_ex(const lsa_kv_cache* cache /* host */, int32_t B, c
  * scale becomes the least power of two (at least 2^-118) with |x| <= 448 scale
  * for every finite x = code * old scale that goes there, and codes are stored as
  * e4m3(x / scale), to nearest even (x formed in fp32; NaN, and x beyond fp32, as
- * NaN). A code whose page's scale was the same stays the same.
+ * NaN). But a code whose page's scale was the same stays the same, bit for bit.
  * Supported: 1 <= B <= 4096; 1 <= L <= 1024; dtype, d_h and n_kv equal in from
  * and to; page_tokens may differ; 1 <= entry_tokens <= 128; the pages that
  * max_kept takes, times B and 2 n_kv, at most 2^24 - 1.

@@ -190,6 +190,7 @@ __global__ __launch_bounds__(CP_THREADS) void compact_kernel(const CompactArgs a
 #pragma unroll
       for (int e = 0; e < NL; ++e) {
         if (!here[e]) continue;
+        asm volatile("" : "+v"(x[e]));  // widened again: the values of the maximum would take four times the registers
         u32x4 z;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -197,6 +198,7 @@ __global__ __launch_bounds__(CP_THREADS) void compact_kernel(const CompactArgs a
           widen_codes(x[e][w], s[e], y);
           z[w] = pack_e4m3(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
         }
+        if (s[e] == scale) z = x[e];  // NaN keeps its sign there too
         __builtin_nontemporal_store(z, (u32x4*)(dst + (e * 64 + lane) * 16));
       }
     }
