@@ -695,8 +695,10 @@ lsa_status lsa_attend_topk(const lsa_kv_cache* cache /* host */, int32_t B, cons
  *
  * Everything else is as for the plain calls, whose workspaces of the same sizes
  * they take. Precision: the capped score is formed in fp32, off by at most
- * 2^-20 softcap; the bias is added in fp32, off by 2^-23 of its size. A score
- * whose products overflow fp32 with both signs is NaN, as in the plain call.
+ * 2^-20 softcap; the bias is formed and added in fp32, off by at most 2^-22 of
+ * its size, or by 2^-18 where that is more. A score whose products overflow fp32
+ * with both signs is NaN, as in the plain call; one that loses a bias beyond fp32
+ * is minus infinity.
  * Supported: as the plain calls; softcap 0 or in [2^-10, 1024]; prefix_end only
  * without a window; lsa_attend_topk_ex takes neither doc_start nor prefix_end.
  * ---------------------------------------------------------------------- */

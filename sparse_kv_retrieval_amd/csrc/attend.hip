@@ -307,7 +307,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_split_blocks(16 * RT, D)) void a
       s_edge[1][r] = first_seen(a, w.t0 + tok);
       s_edge[2][r] = last_seen(a, w.t0 + tok, p_row[rt], w.len);
     }
-    if constexpr (BIAS) slope[rt] = a.slopes[h * a.G + (row - tok * a.G)] * LOG2E;
+    if constexpr (BIAS) slope[rt] = slope_log2(a, h * a.G + (row - tok * a.G));
     const uint16_t* src = a.q + (w.t0 + tok) * a.q_stride + (int64_t)(h * a.G + (row - tok * a.G)) * D;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {

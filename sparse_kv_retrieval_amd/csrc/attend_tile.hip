@@ -129,7 +129,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
   const int p_row = w.p0 + tok, w_row = window_start(a, p_row);
   const int f_row = SEEN ? first_seen(a, w.t0 + tok) : 0;
   const int e_row = SEEN ? last_seen(a, w.t0 + tok, p_row, w.len) : p_row;
-  const float slope = BIAS ? a.slopes[head] * LOG2E : 0.f;
+  const float slope = BIAS ? slope_log2(a, head) : 0.f;
   // The wave's queries come, and its output leaves, in whole rows, through LDS that no tile is in: a lane's own pieces of its row are 32 bytes
   // of a line here and 16 there. mine(row, chunk): where the wave's 32 rows lie, swizzled like keys.
   static_assert(TL_WAVES / 2 * 32 <= TL_BUFS * TL_N, "half the waves' rows fit the keys' buffers");
@@ -282,9 +282,13 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
 
   // The maximum is raised by the greatest score that a row sees among 32 keys and the greatest bias of the 32, which may not meet. Where it
   // sees one of them it is then up to 31 slope log2(e) too high: 2^45 for a slope of 1, for which fp32 and bf16 have room. Where it sees none
-  // they must not raise it at all: their biases may be any distance away from those of the keys that it does see. Blocks with steeper
-  // heads look at each key.
-  const bool steep = BIAS && __any(!(fabsf(slope) <= LOG2E));
+  // they must not raise it at all: their biases may be any distance away from those of the keys that it does see. Waves with
+  // steeper heads look at each key. (So do those of so small a scale that a bias in units of the products would overflow.)
+  const bool steep = BIAS && ((!CAP && c < 0x1p-96f) || __any(!(fabsf(slope) <= LOG2E)));
+  // There, without a cap, settle() makes the scores whole, in base 2 and with their biases. A line through 32 keys is off by some 2^-24 of 31
+  // slopes, which is much beside a near key's own bias; and far keys' scores have to be the numbers that their maximum is one of.
+  const bool made = !CAP && steep;
+  const float line_slope = made ? 0.f : slope;
   // A cap makes a score of minus infinity finite, so masked places hold NaN instead. In bf16 the probabilities are then held below
   // 1, where the clamp changes no other one.
   constexpr float SHIFT = CAP && !FP8 ? ATTEND_LAZY : 0.f;
@@ -306,7 +310,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
     }
     // Without a cap the bias is taken as linear in the position, slope * (t - p). Beyond the row, where only a prefix is seen, the scores
     // make up for it.
-    const bool bent = BIAS && !CAP && a.prefix_end && t0 + 32 * u + 31 > w.p_lo;
+    const bool bent = BIAS && !CAP && !made && a.prefix_end && t0 + 32 * u + 31 > w.p_lo;
     if (bent) {
       const int beyond = t0 + 32 * u + 4 * h - p_row;
       float back[2];
@@ -342,12 +346,12 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
         top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          float y = s[i] * (FP8 ? s_kc[buf][2 * u + i / 8] : c), d = d0 - (float)(8 * (i / 4) + i % 4);
-          if constexpr (CAP) {
-            y = visible >> (8 * (i / 4) + i % 4) & 1 ? cap_score(a, y) : y;
-            d = fabsf(d);
-          }
-          top = fmaxf(top, __builtin_fmaf(-slope, d, y));
+          const int at = 8 * (i / 4) + i % 4;
+          float y = s[i] * (FP8 ? s_kc[buf][2 * u + i / 8] : c);
+          if constexpr (CAP) y = visible >> at & 1 ? cap_score(a, y) : y;
+          y = __builtin_fmaf(-slope, fabsf(d0 - (float)at), y);
+          if constexpr (!CAP) s[i] = y = visible >> at & 1 ? y : -__builtin_inff();
+          top = fmaxf(top, y);
         }
       }
     }
@@ -395,6 +399,7 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
         inv[x] = s_vinv[buf][2 * u + x];
       }
     }
+    if (made) c2[0] = c2[1] = 1.f;
     const float d0 = BIAS ? (float)(p_row - (t0 + 32 * u + 4 * h)) : 0.f;
     float line[2] = {add[0], add[1]};
     if constexpr (CAP) {
@@ -403,19 +408,21 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       line[0] = add[0]; line[1] = add[1];
     }
     if constexpr (BIAS) {
-      line[0] = __builtin_fmaf(-slope, d0, add[0]);
-      line[1] = __builtin_fmaf(-slope, d0, add[1]);
+      line[0] = __builtin_fmaf(-line_slope, d0, add[0]);
+      line[1] = __builtin_fmaf(-line_slope, d0, add[1]);
     }
     auto prob = [&](int i) __attribute__((always_inline)) {
       const float at = (float)(8 * (i / 4) + i % 4);
       float y = line[i / 8];
       if constexpr (BIAS && CAP) y = __builtin_fmaf(-slope, fabsf(d0 - at), add[i / 8]);
-      else if constexpr (BIAS) y = __builtin_fmaf(slope, at, y);
+      else if constexpr (BIAS) y = __builtin_fmaf(line_slope, at, y);
       if constexpr (!CAP) return __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c2[i / 8], y));
       const float r = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[i] * c2[i / 8]));
       const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(-2.f * a.cap_log2, r, y));
-      // NaN in a masked place becomes 0: in bf16 by the clamp of the exponential itself, which costs nothing
-      return FP8 ? fmaxf(e, 0.f) : __builtin_amdgcn_fmed3f(e, 0.f, 1.f);
+      // NaN in a masked place becomes 0: in bf16 by the clamp of the exponential itself, which costs nothing. A steep bias of far keys alone is
+      // rounded otherwise than in their maximum; the upper end keeps what that may make of it from being an infinity, which a later
+      // maximum's factor of 0 would not clear. (e4m3: 2^8, times what may be left of a scale.)
+      return FP8 && !BIAS ? fmaxf(e, 0.f) : __builtin_amdgcn_fmed3f(e, 0.f, FP8 ? 0x1p35f : 1.f);
     };
     uint32_t packed[8];
     s_next = (f32x16)(0.f);

@@ -410,6 +410,11 @@ __device__ __forceinline__ float cap_score(const AttendArgs& a, float y) {
   return __builtin_fmaf(-2.f * a.cap_log2, __builtin_amdgcn_rcpf(1.f + e), a.cap_log2);
 }
 
+// A head's slope in base 2. A finite one stays finite: infinity times a distance of 0 would be NaN.
+__device__ __forceinline__ float slope_log2(const AttendArgs& a, int32_t head) {
+  return __builtin_amdgcn_fmed3f(a.slopes[head] * LOG2E, ATTEND_LOWEST, -ATTEND_LOWEST);
+}
+
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 // Two floats to packed bf16, to nearest even (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {

@@ -113,3 +113,77 @@ def test_capped_scores_of_minus_infinity_count(torch, lsa):
         want = v.cumsum(0) / n[:, None]
         tol = (2.0 ** -8 + 200 * 2.0 ** -24 + 2.0 ** -16) * (v.abs().cumsum(0) / n[:, None]) + 2.0 ** -8 * want.abs()
         assert ((out.double() - want[:, None]).abs() <= tol[:, None]).all()
+
+
+# ------------------------------------------------------------------ steep ones
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("slope", [3.0, -3.0])
+@pytest.mark.parametrize("dtype,d,G", [("bf16", 128, 1), ("fp8", 64, 3), ("fp8", 128, 8)])
+def test_steep(torch, lsa, softcap, slope, dtype, d, G):
+    """Beyond a slope of 1: prompts, windows, prefixes and documents, and pages that are not there."""
+    totals, news = [300, 97, 900], [300, 97, 140]
+    s = Setup(torch, lsa, totals, dtype=dtype, n_kv=1, d=d, pt=32, seed=31)
+    for name in ("k", "v"):
+        if dtype == "fp8":
+            s.parts[name + "_scale"].mul_(1.37)
+    s.decode()
+    s.table[2, 5] = -1
+    s.table_dev.copy_(torch.from_numpy(s.table))
+    form = (softcap, slope)
+    compare(torch, lsa, s, news, form, G)
+    compare(torch, lsa, s, news, form, G, window=60, sinks=5)
+    doc, prefix = documents(s.g, news, totals, 5, 150), np.repeat(np.array([200, 97, 850], np.int32), news)
+    compare(torch, lsa, s, news, form, G, doc=doc)
+    compare(torch, lsa, s, news, form, G, prefix=prefix)
+    compare(torch, lsa, s, news, form, G, doc=doc, prefix=prefix)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("slope", [300.0, 1e6, 1e9, 1e36, 3.4e38])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("rows", [3, 90])
+def test_steep_rows_see_themselves(torch, lsa, softcap, slope, dtype, rows):
+    """So steep a bias leaves a row its own key, which loses nothing: out is that key's value, lse that key's score."""
+    s = Setup(torch, lsa, [rows + 400], dtype=dtype, n_kv=1, d=64, pt=16, seed=32)
+    q = bf16(torch, s.g, (rows, 4, 64), 2.0)
+    out, lse = run(torch, lsa, s, q, offsets([rows]), softcap=softcap, slopes=np.full(4, slope, np.float32))
+    where = [(int(s.table[0, p // 16]), 0, p % 16) for p in range(400, 400 + rows)]
+    k, v = (np.stack([s.decoded[x][i] for i in where]) for x in ("k", "v"))
+    y = np.einsum("rhd,rd->rh", q.cpu().double().numpy(), k) * 0.125
+    big = np.einsum("rhd,rd->rh", np.abs(q.cpu().double().numpy()), np.abs(k)) * 0.125
+    want = softcap * np.tanh(y / softcap) if softcap else y
+    assert (out.cpu().double().numpy() == v[:, None]).all()  # cached values are bf16 numbers, and the weight is 1
+    # as in check(), for one key and a bias of 0
+    dx = 2 * (64 + 4) * 2.0 ** -24 * big + 2.0 ** -22 * big + 2.0 ** -20 * softcap
+    assert (np.abs(lse.cpu().double().numpy() - want) <= 2 * dx + 2.0 ** -24 + 2.0 ** -20 * (1 + np.abs(want))).all()
+
+
+@pytest.mark.parametrize("rows", [3, 90])
+def test_steep_listed(torch, lsa, rows):
+    """The same for listed entries and the window."""
+    s = Setup(torch, lsa, [100 + rows, 40], dtype="bf16", n_kv=1, d=64, pt=16, seed=33)
+    q = bf16(torch, s.g, (2, 4, 64), 2.0)
+    idx = torch.tensor([[3, 9], [2, 5]], dtype=torch.int32, device="cuda")
+    count = torch.tensor([2, 2], dtype=torch.int32, device="cuda")
+    size = lsa.attend_topk_workspace_size(s.cache, n_q=4, k=2, window=20)
+    ws = torch.empty(max(size, 16), dtype=torch.uint8, device="cuda")
+    for slope in (300.0, 1e9, 3.4e38):
+        out, lse = torch.empty_like(q), torch.empty(2, 4, device="cuda")
+        lsa.attend_topk(s.cache, q, idx=idx, count=count, out=out, lse=lse, scale=0.125, window=20, workspace=ws,
+                        slopes=torch.full((4,), slope, device="cuda"))
+        for b, t in enumerate(s.totals):
+            v = s.parts["v"][int(s.table[b, (t - 1) // 16]), 0, (t - 1) % 16]
+            assert (out[b] == v).all() and torch.isfinite(lse[b]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("scale", [1e-39, 1e-30, -1e-30, 0.0])
+def test_biases_alone(torch, lsa, dtype, scale):
+    """Scales that leave nothing of the scores: what counts is the bias, on both sides of a row."""
+    s = Setup(torch, lsa, [200, 90], dtype=dtype, n_kv=1, d=64, pt=16, seed=34)
+    q = bf16(torch, s.g, (290, 2, 64), 2.0)
+    prefix = np.repeat(np.array([150, 0], np.int32), [200, 90])
+    for slope in (0.3, -0.2, 2.5):
+        f = dict(slopes=np.full(2, slope, np.float32))
+        out, lse = run(torch, lsa, s, q, offsets([200, 90]), scale=scale, prefix=prefix, **f)
+        check(s, q, out, lse, some_rows([200, 90], s.totals, 20), scale=scale, prefix=prefix, tag=f"{scale} {slope}", **f)
