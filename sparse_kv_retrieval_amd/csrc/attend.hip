@@ -39,10 +39,10 @@
 // (44 bytes of scratch a lane): 64 rows over 131,072 tokens in bf16 take 108 us (5.0 TB/s) where 16 rows take 93 (5.8).
 //
 // Forms (kv.hpp). Caps and biases are instances of their own: the plain ones are as they were. What they add hides behind the
-// reads with 16 rows: 8 x 125,000 tokens take 610 us plain, 613 capped, 625 with a bias and 627 with both (bf16; 333, 336, 337 and 342 in
+// reads with 16 rows: 8 x 125,000 tokens take 609 us plain, 612 capped, 623 with a bias and 626 with both (bf16; 333, 336, 336 and 342 in
 // e4m3). Registers are what they are short of: a row's window, document and prefix lie in LDS, and a tile's distances are one number a row
 // and lane (without these bf16 spilled 8 and 19 registers instead of 2 and 8: 624, 639 and 639 us). With 64 rows, where one
-// wave a SIMD has to do it all, 8 x 40,000 tokens in bf16 take 46, 47, 47 and 52 us (45, 52, 56 and 57 before).
+// wave a SIMD has to do it all, 8 x 40,000 tokens in bf16 take 45, 47, 47 and 52 us (45, 52, 56 and 57 before).
 #include "kv.hpp"
 
 namespace lsa {

@@ -31,10 +31,11 @@
 // tokens on top of 30,720). Documents and prefixes shorten the range of tiles a block goes through.
 //
 // Measured on MI355X (64 query heads, 8 key heads, d_h 128; torch's bf16 matrix product of 8192^3 reaches
-// 1195 TFLOP/s there; whole calls in turn): 2048 tokens on top of 30,720 in e4m3 2.02 ms (1.05 PFLOP/s), with a bias 2.09;
-// prompts of 4981 and 4888 tokens in bf16 814 us (0.98 PFLOP/s), with a cap 1011; of 7203 and 6711 tokens with a window of 1024
-// 571 us (0.76 PFLOP/s of visible pairs); 8192 tokens of packed documents of 89 to 1519 214 us. The matrix
-// pipes are busy 49 % of the time in a plain prompt and 35 % in a capped one, the vector ALUs 50 and 67. Without
+// 1397 TFLOP/s there, warmed in the same way; whole calls in turn): 2048 tokens on top of 30,720 in e4m3 1.94 ms (1.10 PFLOP/s), with a bias 2.02;
+// prompts of 4981 and 4888 tokens in bf16 788 us (1.01 PFLOP/s), with a cap 1019; of 7203 and 6711 tokens with a window of 1024
+// 561 us (0.77 PFLOP/s of visible pairs); 8192 tokens of packed documents of 89 to 1519 215 us. The matrix
+// pipes are busy 50 % of the time in a plain prompt and 35 % in a capped one, the vector ALUs 51 and 67: together some 100 %, so the two
+// hardly work at once, although a wave's own groups have work for both. Without
 // the exponentials a prompt takes 5 % less, without transposing reads 2, fetches 3, LDS stores 2, half of the first product 11: no
 // single one bounds it. A block's rows, places, queries, first tile and output cost some 14 us that nothing overlaps, as one block fills a
 // CU's registers and LDS: they are what documents and short or windowed prompts pay. Slower were blocks of four waves and two

@@ -10,12 +10,16 @@
 // Shape. A block has one destination page of one sequence. It finds the page's tokens once, for all layers, heads, K and V;
 // then each wave takes tiles (layer, K or V, head) in turn, whole in its registers between the maximum and the
 // store, so that a wave waits for no other one. Tiles of a page are shared among blocks until some 8192 are there: the last of fewer,
-// longer ones end the call alone, and each block finds its tokens anew (2048, 4096, 8192 and 16,384: 359, 348, 343 and 357 us
-// for the case below).
+// longer ones end the call alone, and each block finds its tokens anew. With 2048, 4096, 8192 and 16,384 (us, kept 13.5 %):
+//   8 x 125,000 tokens, three layers, eight heads of 128   bf16 678, 641, 626, 636    e4m3 364, 347, 343, 343
+//   32 x 4096 to 131,071, one layer, bf16                  245, 245, 237, 248
+//   64 x 4000, three layers, pages of 16, e4m3             115, 112, 109, 116
+//   1 x 125,000, three layers, e4m3                        50, 49, 49, 49
+//   1 x 125,000, one layer, bf16; 32 ragged, two heads of 64, e4m3; 1 x 8000, 16 layers, bf16    all four within 3 %
 //
 // Bound by HBM: each kept row is read and written once, and nothing reads either again soon, so both go past the caches
-// (non-temporal stores: 360 against 378 us). Measured on MI355X: 13.5 % of the entries of 8 x 125,000 tokens, three layers of 8
-// heads, e4m3, d_h 128, 1.67 GB read and written: 337 to 348 us (4.8 to 5.0 TB/s; a copy of 1 GiB 5.06). One short sequence is bound by latency: the two ends,
+// (non-temporal stores: 360 against 378 us). Measured on MI355X: the first of these shapes, 3.34 GB read and written in bf16 626 us (5.3 TB/s) and
+// 1.67 in e4m3 343 to 347 (4.8 to 4.9; a copy of 1 GiB 5.1). One short sequence is bound by latency: the two ends,
 // list, page and row are four to five dependent reads, 8 us.
 #include "kv_pages.hpp"
 

@@ -4,7 +4,8 @@
 // So refs, table and lengths are the whole state: there is no list of free pages to keep in order, counts are sums
 // and do not depend on the order of their atomics, and the pages that a call takes depend on the state alone. The price is a
 // search of refs, 4 bytes a page, by one block of 1024 threads: 16,384 pages a round trip to memory, and none where no
-// sequence crosses the end of a page.
+// sequence crosses the end of a page. It begins at page 0, so it grows with the pages in use: where only the last ones are free, extend
+// takes 13, 29 and 96 us over 30,000, 120,000 and 500,000 pages.
 //
 // Everything here is bound by latency: launches and a few dependent reads (length, table, refs). Giving back and sharing have one
 // block per sequence, so that no two threads look at one entry; taking has one block, which needs no order between blocks.
