@@ -422,8 +422,8 @@ __global__ __launch_bounds__(TL_THREADS, 2) void attend_tile_kernel(const Attend
       const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(-2.f * a.cap_log2, r, y));
       // NaN in a masked place becomes 0: in bf16 by the clamp of the exponential itself, which costs nothing. A steep bias of far keys alone is
       // rounded otherwise than in their maximum; the upper end keeps what that may make of it from being an infinity, which a later
-      // maximum's factor of 0 would not clear. (e4m3: 2^8, times what may be left of a scale.)
-      return FP8 && !BIAS ? fmaxf(e, 0.f) : __builtin_amdgcn_fmed3f(e, 0.f, FP8 ? 0x1p35f : 1.f);
+      // maximum's factor of 0 would not clear. (e4m3: 2^8, times the most that is left of a scale, 2^28.)
+      return FP8 && !BIAS ? fmaxf(e, 0.f) : __builtin_amdgcn_fmed3f(e, 0.f, FP8 ? 0x1p36f : 1.f);
     };
     uint32_t packed[8];
     s_next = (f32x16)(0.f);
